@@ -28,29 +28,29 @@ TYPES = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
 def listed():
     return [
         # one decoding step of 16 sequences through the gate (or up) matrices of eight experts kept in 16 bits
-        dict(name="experts fwd, decode", op="fwd", tokens=16, experts=8, k=2, h=4096, n=14336, skew=1.1, type="f16"),
+        dict(name="experts fwd decode", op="fwd", tokens=16, experts=8, k=2, h=4096, n=14336, skew=1.1, type="f16"),
         # a prefill of 4096 tokens through the same matrices, the busiest expert with ten times the rows of the idlest
-        dict(name="experts fwd, prefill", op="fwd", tokens=4096, experts=8, k=2, h=4096, n=14336, skew=1.1, type="bf16"),
+        dict(name="experts fwd prefill", op="fwd", tokens=4096, experts=8, k=2, h=4096, n=14336, skew=1.1, type="bf16"),
         # a ragged batch on sizes that are no multiple of a tile
-        dict(name="experts fwd, odd", op="fwd", tokens=333, experts=16, k=4, h=1000, n=757, skew=0.7, type="f16"),
+        dict(name="experts fwd odd", op="fwd", tokens=333, experts=16, k=4, h=1000, n=757, skew=0.7, type="f16"),
         # training step of a layer of many small experts: the rows' gradient through the gate matrix
         dict(name="experts dgrad", op="dgrad", tokens=4096, experts=64, k=6, h=1408, n=2048, skew=0.5, type="bf16"),
         # and that of the matrices, in 32 bits for the optimizer
         dict(name="experts wgrad", op="wgrad", tokens=4096, experts=64, k=6, h=2048, n=1408, skew=0.5, type="bf16"),
         # one token through a dense matrix held in 8 bits
-        dict(name="int8, one token", op="i8", tokens=1, experts=0, k=1, h=4096, n=14336, skew=0.0, type="f16"),
+        dict(name="int8 one token", op="i8", tokens=1, experts=0, k=1, h=4096, n=14336, skew=0.0, type="f16"),
         # a prefill through the dense down matrix in 8 bits
-        dict(name="int8, prefill", op="i8", tokens=4096, experts=0, k=1, h=14336, n=4096, skew=0.0, type="bf16"),
+        dict(name="int8 prefill", op="i8", tokens=4096, experts=0, k=1, h=14336, n=4096, skew=0.0, type="bf16"),
         # 256 tokens on 64 experts in 8 bits: about 24 rows an expert
-        dict(name="int8, experts", op="i8", tokens=256, experts=64, k=6, h=2048, n=1408, skew=0.5, type="f16"),
+        dict(name="int8 experts", op="i8", tokens=256, experts=64, k=6, h=2048, n=1408, skew=0.5, type="f16"),
         # odd sizes in 8 bits
-        dict(name="int8, odd", op="i8", tokens=201, experts=0, k=1, h=1530, n=1111, skew=0.0, type="bf16"),
+        dict(name="int8 odd", op="i8", tokens=201, experts=0, k=1, h=1530, n=1111, skew=0.0, type="bf16"),
         # the two norms between two blocks of one decoded token
-        dict(name="norms, one token", op="norm", tokens=1, h=4096, type="f16", residual="f16", gate="vector"),
+        dict(name="norms one token", op="norm", tokens=1, h=4096, type="f16", residual="f16", gate="vector"),
         # and of a long prefill with the residual stream in 32 bits
-        dict(name="norms, prefill", op="norm", tokens=16384, h=4096, type="bf16", residual="f32", gate="vector"),
+        dict(name="norms prefill", op="norm", tokens=16384, h=4096, type="bf16", residual="f32", gate="vector"),
         # their gradients in a training step, with a gate of every token's own
-        dict(name="norms, gradients", op="norm_grad", tokens=8192, h=4096, type="bf16", residual="bf16", gate="token"),
+        dict(name="norms gradients", op="norm_grad", tokens=8192, h=4096, type="bf16", residual="bf16", gate="token"),
     ]
 
 
