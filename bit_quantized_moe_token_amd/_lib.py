@@ -12,12 +12,13 @@ LIB_PATH = os.path.join(_HERE, "libmoeq.so")
 
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_HIP = range(5)
 FMT_INT, FMT_BITPLANE = 0, 1
-F16, F32 = 0, 1
+F16, F32, BF16 = 0, 1, 2
 PATH_AUTO, PATH_STREAM, PATH_TILED = 0, 1, 3
 
 c_void_p = ctypes.c_void_p
 c_size_t = ctypes.c_size_t
 c_i32 = ctypes.c_int32
+c_i64 = ctypes.c_int64
 c_u8p = ctypes.POINTER(ctypes.c_uint8)
 c_vpp = ctypes.POINTER(ctypes.c_void_p)
 
@@ -41,6 +42,10 @@ class Routing(ctypes.Structure):
 
 class FfnOptions(ctypes.Structure):
     _fields_ = [("path", c_i32), ("split_k", c_i32)]
+
+
+class Groups(ctypes.Structure):
+    _fields_ = [("offsets", c_void_p), ("pairs", c_void_p), ("E", c_i32), ("P", c_i32), ("T", c_i32), ("k", c_i32)]
 
 
 # (name, restype, argtypes) of every exported entry point
@@ -88,6 +93,16 @@ SIGNATURES = [
     ("moeq_ffn_noalloc_max_bytes", c_i32, [ctypes.POINTER(c_size_t)]),
     ("moeq_expert_ffn_noalloc", c_i32, [c_void_p, c_void_p, c_i32, c_i32, ctypes.POINTER(Routing), c_i32,
                                         c_void_p, c_i32, ctypes.POINTER(FfnOptions), c_void_p]),
+    ("moeq_grouped_gemm", c_i32, [ctypes.POINTER(Groups), c_void_p, c_i64, c_void_p, c_i64, c_i64, c_i32, c_i32, c_i32,
+                                  c_i32, c_void_p, c_i64, c_i32, c_void_p]),
+    ("moeq_grouped_wgrad", c_i32, [ctypes.POINTER(Groups), c_void_p, c_i64, c_void_p, c_i64, c_i32, c_i32, c_i32,
+                                   c_void_p, c_i64, c_i64, c_i32, c_void_p]),
+    ("moeq_quantize_i8", c_i32, [c_void_p, c_i64, c_i32, c_i32, c_i32, c_void_p, c_i64, c_void_p, c_void_p]),
+    ("moeq_gemm_i8", c_i32, [ctypes.POINTER(Groups), c_void_p, c_i64, c_void_p, c_void_p, c_i64, c_i64, c_void_p, c_i32,
+                             c_i32, c_void_p, c_i64, c_i32, c_void_p]),
+    ("moeq_linear_i8_workspace_size", c_i32, [c_i32, c_i32, ctypes.POINTER(c_size_t)]),
+    ("moeq_linear_i8", c_i32, [ctypes.POINTER(Groups), c_void_p, c_i64, c_i32, c_void_p, c_i64, c_i64, c_void_p, c_i32,
+                               c_i32, c_void_p, c_i64, c_i32, c_void_p, c_size_t, c_void_p]),
     ("moeq_profile_enable", c_i32, [c_i32]),
     ("moeq_profile_read", c_i32, [c_i32, ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(c_i32),
                                   ctypes.POINTER(ctypes.c_double), ctypes.POINTER(c_i32)]),

@@ -355,6 +355,186 @@ def moe_forward(layer, logits, x, k, n_comp, routing=None, out=None, out_dtype=t
     return out, routing
 
 
+# --------------------------------- expert matrices in 16 or 8 bits
+
+_DTYPE = {torch.float16: _lib.F16, torch.bfloat16: _lib.BF16, torch.float32: _lib.F32}
+_16BIT = (torch.float16, torch.bfloat16)
+
+
+def _like(t, dtypes, ndim, dev, name):
+    """Checks a strided operand: on device index `dev`, one of `dtypes`,
+    `ndim` dimensions, the last one contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on another device than the other tensors")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {dtypes}, got {t.dtype}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions, got shape {tuple(t.shape)}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+
+
+def _ld(t):
+    """Elements between the rows of t (its row length when there is one row)."""
+    return t.stride(-2) if t.shape[-2] > 1 else t.shape[-1]
+
+
+def _flat(t, n, dtype, dev, name):
+    _like(t, (dtype,), 1, dev, name)
+    if t.shape[0] != n:
+        raise ValueError(f"{name} must have {n} elements, got {t.shape[0]}")
+
+
+def _groups(T, E, offsets, pairs, k, dev):
+    """moeq_groups of sorted rows, and their count."""
+    if offsets is None:
+        if E != 1:
+            raise ValueError("offsets are needed with more than one expert")
+    else:
+        _flat(offsets, E + 1, torch.int32, dev, "offsets")
+    P = T
+    if pairs is not None:
+        _like(pairs, (torch.int32,), 1, dev, "pairs")
+        P = pairs.shape[0]
+    return _lib.Groups(offsets.data_ptr() if offsets is not None else None,
+                       pairs.data_ptr() if pairs is not None else None, E, P, T, k), P
+
+
+def _out(out, shape, dtype, dtypes, dev, name="out"):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+    _like(out, dtypes, len(shape), dev, name)
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(out.shape)}")
+    return out
+
+
+def _launch(name, dev, *args):
+    """Calls entry point `name` on the current stream of device `dev`."""
+    f = getattr(lib(), name)
+    if torch._C._cuda_getDevice() == dev:
+        st = f(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, torch._C._cuda_getCurrentRawStream(dev))
+    check(st, name)
+
+
+def grouped_gemm(x, w, offsets, pairs=None, k=1, trans=False, out=None, out_dtype=None):
+    """Products of expert-sorted rows with their expert's matrix (see
+    moeq_grouped_gemm): out[r] = x[pairs[r] // k] @ w[e].T, or @ w[e] with
+    trans, for the rows offsets[e] <= r < offsets[e + 1] of every expert e.
+
+    x fp16 or bf16 [T, K]; w of the same type [E, N, K] ([E, K, N] with
+    trans); offsets int32 [E + 1]; pairs int32 [P] or None (out[r] from
+    x[r]).  Returns [P, N] of out_dtype (x's type, or float32); rows outside
+    the offsets are left as they were (undefined in a new tensor)."""
+    dev = x.get_device() if isinstance(x, torch.Tensor) else -1
+    _like(x, _16BIT, 2, dev, "x")
+    _like(w, (x.dtype,), 3, dev, "w")
+    T, K = x.shape
+    E, N, Kw = w.shape if not trans else (w.shape[0], w.shape[2], w.shape[1])
+    if Kw != K:
+        raise ValueError(f"x has {K} columns, w {Kw}")
+    g, P = _groups(T, E, offsets, pairs, k, dev)
+    out = _out(out, (P, N), out_dtype or x.dtype, (x.dtype, torch.float32), dev)
+    _launch("moeq_grouped_gemm", dev, g, x.data_ptr(), _ld(x), w.data_ptr(), _ld(w), w.stride(0), int(trans), N, K,
+            _DTYPE[x.dtype], out.data_ptr(), _ld(out), _DTYPE[out.dtype])
+    return out
+
+
+def grouped_wgrad(dy, x, offsets, pairs=None, k=1, out=None, out_dtype=torch.float32):
+    """Gradient of the experts' matrices (see moeq_grouped_wgrad): out[e] =
+    sum over e's sorted rows r of the outer product of dy[r] and
+    x[pairs[r] // k].  dy [P, N] and x [T, K] of one 16-bit type; returns
+    [E, N, K] of out_dtype (float32 or that type)."""
+    dev = dy.get_device() if isinstance(dy, torch.Tensor) else -1
+    _like(dy, _16BIT, 2, dev, "dy")
+    _like(x, (dy.dtype,), 2, dev, "x")
+    N, (T, K) = dy.shape[1], x.shape
+    E = offsets.shape[0] - 1 if offsets is not None else 1
+    g, P = _groups(T, E, offsets, pairs, k, dev)
+    if P != dy.shape[0]:
+        raise ValueError(f"dy has {dy.shape[0]} rows for {P} sorted rows")
+    out = _out(out, (E, N, K), out_dtype, (dy.dtype, torch.float32), dev)
+    _launch("moeq_grouped_wgrad", dev, g, dy.data_ptr(), _ld(dy), x.data_ptr(), _ld(x), N, K, _DTYPE[dy.dtype],
+            out.data_ptr(), _ld(out), out.stride(0), _DTYPE[out.dtype])
+    return out
+
+
+def quantize_i8(x):
+    """8-bit codes int8 [rows, cols] and fp32 scales [rows] of the rows of x
+    (fp16, bf16 or fp32; see moeq_quantize_i8).  A matrix per expert goes in
+    as [E, N, K] and gives [E, N, K] and [E, N]."""
+    dev = x.get_device() if isinstance(x, torch.Tensor) else -1
+    if isinstance(x, torch.Tensor) and x.dim() == 3:
+        q, s = quantize_i8(x.reshape(-1, x.shape[-1]))
+        return q.view(x.shape), s.view(x.shape[:2])
+    _like(x, tuple(_DTYPE), 2, dev, "x")
+    q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+    s = torch.empty((x.shape[0],), dtype=torch.float32, device=x.device)
+    _launch("moeq_quantize_i8", dev, x.data_ptr(), _ld(x), x.shape[0], x.shape[1], _DTYPE[x.dtype], q.data_ptr(),
+            x.shape[1], s.data_ptr())
+    return q, s
+
+
+def _i8_weights(x, wq, sw, dev):
+    """(E, N, row and matrix strides) of 8-bit matrices [N, K] or [E, N, K]."""
+    _like(wq, (torch.int8,), 3 if isinstance(wq, torch.Tensor) and wq.dim() == 3 else 2, dev, "wq")
+    E = wq.shape[0] if wq.dim() == 3 else 1
+    N = wq.shape[-2]
+    if wq.shape[-1] != x.shape[1]:
+        raise ValueError(f"x has {x.shape[1]} columns, wq {wq.shape[-1]}")
+    _like(sw, (torch.float32,), wq.dim() - 1, dev, "sw")
+    if sw.shape != wq.shape[:-1] or not sw.is_contiguous():
+        raise ValueError(f"sw must be contiguous of shape {tuple(wq.shape[:-1])}, got {tuple(sw.shape)}")
+    return E, N, _ld(wq), wq.stride(0) if wq.dim() == 3 else 0
+
+
+def gemm_i8(xq, sx, wq, sw, offsets=None, pairs=None, k=1, out=None, out_dtype=torch.float16):
+    """Products of 8-bit codes with their scales (see moeq_gemm_i8): rows xq
+    int8 [T, K] with sx fp32 [T]; one matrix wq int8 [N, K] with sw [N], or
+    one per expert [E, N, K] with sw [E, N] and the sorted rows of
+    grouped_gemm.  Returns [P, N]."""
+    dev = xq.get_device() if isinstance(xq, torch.Tensor) else -1
+    _like(xq, (torch.int8,), 2, dev, "xq")
+    T, K = xq.shape
+    _flat(sx, T, torch.float32, dev, "sx")
+    E, N, ldw, stride_w = _i8_weights(xq, wq, sw, dev)
+    g, P = _groups(T, E, offsets, pairs, k, dev)
+    out = _out(out, (P, N), out_dtype, tuple(_DTYPE), dev)
+    _launch("moeq_gemm_i8", dev, g, xq.data_ptr(), _ld(xq), sx.data_ptr(), wq.data_ptr(), ldw, stride_w, sw.data_ptr(),
+            N, K, out.data_ptr(), _ld(out), _DTYPE[out.dtype])
+    return out
+
+
+def linear_i8(x, wq, sw, offsets=None, pairs=None, k=1, out=None, out_dtype=None, ws=None):
+    """gemm_i8 of the rows x (fp16, bf16 or fp32 [T, K]) coded as by
+    quantize_i8 (see moeq_linear_i8).  ws: uint8 workspace tensor, or None
+    for one of the call's own.  Returns [P, N] of out_dtype (x's type)."""
+    dev = x.get_device() if isinstance(x, torch.Tensor) else -1
+    _like(x, tuple(_DTYPE), 2, dev, "x")
+    T, K = x.shape
+    E, N, ldw, stride_w = _i8_weights(x, wq, sw, dev)
+    g, P = _groups(T, E, offsets, pairs, k, dev)
+    out = _out(out, (P, N), out_dtype or x.dtype, tuple(_DTYPE), dev)
+    if ws is None:
+        ws = torch.empty((linear_i8_workspace_size(T, K),), dtype=torch.uint8, device=x.device)
+    else:
+        _like(ws, (torch.uint8,), 1, dev, "ws")
+    _launch("moeq_linear_i8", dev, g, x.data_ptr(), _ld(x), _DTYPE[x.dtype], wq.data_ptr(), ldw, stride_w, sw.data_ptr(),
+            N, K, out.data_ptr(), _ld(out), _DTYPE[out.dtype], ws.data_ptr(), ws.numel())
+    return out
+
+
+def linear_i8_workspace_size(T, K):
+    n = ctypes.c_size_t(0)
+    check(lib().moeq_linear_i8_workspace_size(T, K, ctypes.byref(n)), "moeq_linear_i8_workspace_size")
+    return n.value
+
+
 # ------------------------------------------------------------ profiling
 
 def profile_enable(on=True):

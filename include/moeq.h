@@ -69,7 +69,7 @@ typedef enum {
 } moeq_status;
 
 typedef enum { MOEQ_FMT_INT = 0, MOEQ_FMT_BITPLANE = 1 } moeq_format;
-typedef enum { MOEQ_F16 = 0, MOEQ_F32 = 1 } moeq_dtype;
+typedef enum { MOEQ_F16 = 0, MOEQ_F32 = 1, MOEQ_BF16 = 2 } moeq_dtype;
 
 /* Name of a status code (static string). */
 const char *moeq_status_string(moeq_status s);
@@ -446,6 +446,101 @@ moeq_status moeq_expert_ffn_noalloc(const moeq_layer *L, const uint16_t *x, int3
                                     int32_t k, const moeq_routing *r, int32_t n_comp,
                                     void *y, int32_t y_dtype, const moeq_ffn_options *opts,
                                     hipStream_t stream);
+
+/* ---------------------------------------- expert matrices in 16 or 8 bits -- */
+
+/*
+ * The blocks of a layer that are not held in 2 to 4 bits ([MxMoE] abstract:
+ * the precision differs per linear block; experts are used unevenly), and
+ * what training or calibration of such a block needs: products of rows
+ * sorted by expert with each expert's own matrix, over ragged row counts.
+ *
+ * moeq_groups — which rows meet which matrix.  Sorted row r (0 <= r < P)
+ * belongs to expert e when offsets[e] <= r < offsets[e + 1], and reads
+ * source row pairs[r] / k of a [T, ...] operand (expert_offsets,
+ * sorted_pairs and k of a moeq_routing; P = T * k).
+ *   offsets DEVICE [E + 1] int32, or NULL: one expert (E = 1), all P rows.
+ *   pairs   DEVICE [P] int32, or NULL: sorted row r reads row r (T >= P, k
+ *           is then ignored).
+ *   1 <= E <= 256; P, T >= 0; k >= 1.
+ * The counts stay on the device: nothing is read back.  Offsets outside
+ * [0, P] are taken as the nearer end; a pair whose source row lies outside
+ * [0, T) reads a row of zeros; rows at or behind offsets[E] (and before
+ * offsets[0]) belong to no expert and are left as they were.
+ *
+ * Matrices of the calls below have any row stride of at least their row
+ * length ("ld", in elements) and any alignment of whole elements; strides
+ * and bases of 16 bytes are the fast case.  Row lengths are limited to 2^20.
+ * Outputs may not overlap inputs.
+ */
+typedef struct {
+  const int32_t *offsets;
+  const int32_t *pairs;
+  int32_t E, P, T, k;
+} moeq_groups;
+
+/*
+ * moeq_grouped_gemm — for every sorted row r of expert e
+ *   trans 0:  y[r, n] = sum_c x[src(r), c] * w_e[n, c]   w_e [N, K]
+ *   trans 1:  y[r, n] = sum_c x[src(r), c] * w_e[c, n]   w_e [K, N]
+ * (c < K, n < N).  trans 1 with the forward's matrices takes the gradient of
+ * its output back to its (sorted) input rows.
+ *   x DEVICE [T, K], w DEVICE E matrices stride_w elements apart, both of
+ *   dtype MOEQ_F16 or MOEQ_BF16; y DEVICE [P, N] of y_dtype (dtype or
+ *   MOEQ_F32).  Products and sums are fp32, rounded once to y_dtype.
+ */
+moeq_status moeq_grouped_gemm(const moeq_groups *g, const void *x, int64_t ldx, const void *w, int64_t ldw,
+                              int64_t stride_w, int32_t trans, int32_t N, int32_t K, int32_t dtype, void *y,
+                              int64_t ldy, int32_t y_dtype, hipStream_t stream);
+
+/*
+ * moeq_grouped_wgrad — gradient of the experts' matrices:
+ *   dw_e[n, c] = sum over e's sorted rows r of dy[r, n] * x[src(r), c]
+ * An expert without rows gets zeros.  (dy = x without pairs gives the
+ * experts' second-moment matrices x^T x that calibration uses.)
+ *   dy DEVICE [P, N], x DEVICE [T, K] of dtype MOEQ_F16 or MOEQ_BF16;
+ *   dw DEVICE E matrices [N, K] stride_dw elements apart, of dw_dtype (dtype
+ *   or MOEQ_F32).  Sums are fp32 over the rows in order.
+ */
+moeq_status moeq_grouped_wgrad(const moeq_groups *g, const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                               int32_t N, int32_t K, int32_t dtype, void *dw, int64_t lddw, int64_t stride_dw,
+                               int32_t dw_dtype, hipStream_t stream);
+
+/*
+ * moeq_quantize_i8 — symmetric 8-bit codes of every row, in fp32:
+ *   a = max |x|,  scale = a / 127,  code = rint(x * (127 / a))
+ * (each quotient and product rounded to fp32, rint = half to even; codes in
+ * -127..127).  A row with a < 2^-118 gets codes 0 and scale 1; a row that
+ * holds an infinity or a NaN gets codes 0 and scale NaN (so that what is
+ * computed from it is NaN).
+ *   x DEVICE [rows, cols] of dtype MOEQ_F16, MOEQ_BF16 or MOEQ_F32;
+ *   codes DEVICE [rows, cols] int8 out; scales DEVICE [rows] fp32 out.
+ */
+moeq_status moeq_quantize_i8(const void *x, int64_t ldx, int32_t rows, int32_t cols, int32_t dtype, int8_t *codes,
+                             int64_t ldc, float *scales, hipStream_t stream);
+
+/*
+ * moeq_gemm_i8 — products of 8-bit codes with a scale per source row
+ * (token) and per (expert, output channel):
+ *   y[r, n] = (sum_c xq[src(r), c] * wq_e[n, c]) * sx[src(r)] * sw[e, n]
+ * The integer sum is exact (K <= 131072); the scaling is fp32, rounded once
+ * to y_dtype.
+ *   xq DEVICE [T, K] int8, sx DEVICE [T] fp32; wq DEVICE E matrices [N, K]
+ *   int8 stride_w elements apart, sw DEVICE [E, N] fp32; y DEVICE [P, N] of
+ *   y_dtype MOEQ_F16, MOEQ_BF16 or MOEQ_F32.
+ *
+ * moeq_linear_i8 — the same from rows x [T, K] of dtype MOEQ_F16, MOEQ_BF16
+ * or MOEQ_F32, coded as by moeq_quantize_i8 (bit for bit what the two calls
+ * give).  ws DEVICE, 16-byte aligned, at least
+ * moeq_linear_i8_workspace_size bytes, for this call alone while it runs.
+ */
+moeq_status moeq_gemm_i8(const moeq_groups *g, const int8_t *xq, int64_t ldx, const float *sx, const int8_t *wq,
+                         int64_t ldw, int64_t stride_w, const float *sw, int32_t N, int32_t K, void *y, int64_t ldy,
+                         int32_t y_dtype, hipStream_t stream);
+moeq_status moeq_linear_i8_workspace_size(int32_t T, int32_t K, size_t *bytes);
+moeq_status moeq_linear_i8(const moeq_groups *g, const void *x, int64_t ldx, int32_t dtype, const int8_t *wq,
+                           int64_t ldw, int64_t stride_w, const float *sw, int32_t N, int32_t K, void *y,
+                           int64_t ldy, int32_t y_dtype, void *ws, size_t ws_bytes, hipStream_t stream);
 
 /* ---------------------------------------------------------- profiling -- */
 

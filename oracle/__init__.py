@@ -14,6 +14,8 @@ Modules
   forward  routing, counting sort, dequantization, compensated linears,
            SwiGLU expert FFN and gate-weighted combine (the evaluation step)
   layer    a lazily quantized layer built from fp16 weights with ``ptq``
+  products products of expert-sorted rows with one matrix per expert, their
+           gradients, 8-bit codes of rows
 
 Everything is plain numpy in float64, except where the method fixes a storage
 precision (fp16 scales, LUT entries and factors; uint8 codes and zeros) —
