@@ -48,6 +48,12 @@ class Groups(ctypes.Structure):
     _fields_ = [("offsets", c_void_p), ("pairs", c_void_p), ("E", c_i32), ("P", c_i32), ("T", c_i32), ("k", c_i32)]
 
 
+class Norm(ctypes.Structure):
+    _fields_ = [("T", c_i32), ("H", c_i32), ("dtype", c_i32), ("res_dtype", c_i32), ("w_pre", c_void_p),
+                ("w_post", c_void_p), ("gate", c_void_p), ("gate_per_token", c_i32), ("post_norm", c_i32),
+                ("alpha", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
 # (name, restype, argtypes) of every exported entry point
 SIGNATURES = [
     ("moeq_status_string", ctypes.c_char_p, [c_i32]),
@@ -103,6 +109,10 @@ SIGNATURES = [
     ("moeq_linear_i8_workspace_size", c_i32, [c_i32, c_i32, ctypes.POINTER(c_size_t)]),
     ("moeq_linear_i8", c_i32, [ctypes.POINTER(Groups), c_void_p, c_i64, c_i32, c_void_p, c_i64, c_i64, c_void_p, c_i32,
                                c_i32, c_void_p, c_i64, c_i32, c_void_p, c_size_t, c_void_p]),
+    ("moeq_block_norm", c_i32, [ctypes.POINTER(Norm), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    ("moeq_block_norm_grad_workspace_size", c_i32, [c_i32, c_i32, ctypes.POINTER(c_size_t)]),
+    ("moeq_block_norm_grad", c_i32, [ctypes.POINTER(Norm), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                     c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     ("moeq_profile_enable", c_i32, [c_i32]),
     ("moeq_profile_read", c_i32, [c_i32, ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(c_i32),
                                   ctypes.POINTER(ctypes.c_double), ctypes.POINTER(c_i32)]),

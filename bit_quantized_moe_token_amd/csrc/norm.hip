@@ -1,0 +1,513 @@
+// Norms around a block: the block's output is normed, gated and added to the
+// scaled residual, and the sum is normed for the next block, in one pass
+// over the rows; and the gradients of all of it.  (What joins expert layers:
+// the layer's y becomes the next layer's x.)
+//
+//   b = 1 / sqrt(mean(y^2) + eps),   p = w_post * y * b   (p = y without post norm)
+//   r' = alpha r + gate * p          rounded to the residual's type
+//   a = 1 / sqrt(mean(r'^2) + eps),  n = w_pre * r' * a
+//
+// Gradients from d_r' and d_n (u = r' a, v = y b, mean over the row):
+//   g = d_n w_pre,   dr = d_r' + a (g - u mean(g u)),   d_r = alpha dr
+//   c = dr gate w_post,  d_y = b (c - v mean(c v))      (d_y = dr gate without post norm)
+//   d_w_pre = sum_t d_n u,  d_w_post = sum_t dr gate v,  d_gate = dr p (summed
+//   over the tokens for a gate that all tokens share)
+//
+// Bound by memory: every row is read once and kept in registers (as stored)
+// through the row's two reductions.  Sums, statistics and gradients are
+// fp32; the squares' sums need the norms 1 / a and 1 / b anyway, so the
+// backward pass recomputes them from the rows that it reads in any case and
+// needs no saved statistics.
+#include "common.hpp"
+
+namespace moeq {
+
+struct NormArgs {
+  const void *res, *y, *w_pre, *w_post, *gate;
+  const void *d_res, *d_n;
+  void *res_out, *n, *d_y, *d_r, *d_gate;
+  float *part;                       // [grid][3][H] column sums of each workgroup
+  int64_t ld_gate;                   // 0: one gate row for all tokens
+  int32_t T, H, post, cols;          // cols: any column sum is wanted
+  float alpha, eps;
+};
+
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));   // 16 bytes at the alignment of an element
+typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
+
+template <int TY> struct Val;
+template <> struct Val<MOEQ_F16> {
+  static constexpr int size = 2;
+  using Loose = u32x4_a2;
+  static __device__ __forceinline__ float get(uint32_t bits) { return (float)__builtin_bit_cast(f16, (uint16_t)bits); }
+  static __device__ __forceinline__ uint32_t put(float v) { return __builtin_bit_cast(uint16_t, (f16)v); }
+};
+template <> struct Val<MOEQ_BF16> {
+  static constexpr int size = 2;
+  using Loose = u32x4_a2;
+  static __device__ __forceinline__ float get(uint32_t bits) { return __builtin_bit_cast(float, bits << 16); }
+  static __device__ __forceinline__ uint32_t put(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+};
+template <> struct Val<MOEQ_F32> {
+  static constexpr int size = 4;
+  using Loose = u32x4_a4;
+  static __device__ __forceinline__ float get(uint32_t bits) { return __builtin_bit_cast(float, bits); }
+  static __device__ __forceinline__ uint32_t put(float v) { return __builtin_bit_cast(uint32_t, v); }
+};
+
+// Eight consecutive elements as stored.  Loads and stores need no alignment
+// beyond an element's; of a row's last piece only the first n exist.
+template <int TY>
+struct Oct {
+  static constexpr int W = Val<TY>::size * 2;   // dwords
+  using Loose = typename Val<TY>::Loose;
+  uint32_t w[W];
+
+  __device__ __forceinline__ void load(const void *base, int64_t i, int n) {
+    const uint8_t *p = (const uint8_t *)base + i * Val<TY>::size;
+    if (n >= 8) {
+#pragma unroll
+      for (int q = 0; q < W / 4; ++q) {
+        const u32x4 v = ((const __attribute__((address_space(1))) Loose *)p)[q];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[4 * q + j] = v[j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < W; ++j) w[j] = 0;
+#pragma unroll
+      for (int j = 0; j < 7; ++j)
+        if (j < n) {
+          if constexpr (TY == MOEQ_F32) w[j] = gld<uint32_t>(p + 4 * j);
+          else w[j / 2] |= (uint32_t)gld<uint16_t>(p + 2 * j) << (16 * (j & 1));
+        }
+    }
+  }
+  __device__ __forceinline__ float operator[](int j) const {
+    if constexpr (TY == MOEQ_F32) return Val<TY>::get(w[j]);
+    else return Val<TY>::get((w[j / 2] >> (16 * (j & 1))) & 0xffffu);
+  }
+  __device__ __forceinline__ void pack(const float *v) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      if constexpr (TY == MOEQ_F32) w[j] = Val<TY>::put(v[j]);
+      else w[j] = Val<TY>::put(v[2 * j]) | (Val<TY>::put(v[2 * j + 1]) << 16);
+    }
+  }
+  __device__ __forceinline__ void store(void *base, int64_t i, int n) const {
+    uint8_t *p = (uint8_t *)base + i * Val<TY>::size;
+    if (n >= 8) {
+#pragma unroll
+      for (int q = 0; q < W / 4; ++q)
+        ((__attribute__((address_space(1))) Loose *)p)[q] = u32x4{w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]};
+    } else {
+#pragma unroll
+      for (int j = 0; j < 7; ++j)
+        if (j < n) {
+          if constexpr (TY == MOEQ_F32) *(uint32_t *)(p + 4 * j) = w[j];
+          else *(uint16_t *)(p + 2 * j) = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
+        }
+    }
+  }
+};
+
+// Sums of N values over the NT threads of a row.  NT > 64: the waves' sums
+// meet in LDS; the caller alternates `buf` (0, 1) between reductions, so
+// that one barrier each is enough.
+template <int NT, int N>
+__device__ __forceinline__ void row_sum(float *v, float *s, int buf) {
+#pragma unroll
+  for (int o = 32; o; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], o, kWave);
+  if constexpr (NT > 64) {
+    constexpr int NW = NT / 64;
+    float *p = s + buf * 3 * 16;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) p[i * 16 + (threadIdx.x >> 6)] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      v[i] = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) v[i] += p[i * 16 + w];
+    }
+  }
+}
+
+// Threads per workgroup: a row's NT, or four waves of one row each.
+constexpr int norm_block(int NT) { return NT == 64 ? 256 : NT; }
+
+// Thread t of a row holds the pieces of eight elements t, t + NT, ...
+template <int TY, int TR, int NT, int CH>
+__global__ void __launch_bounds__(norm_block(NT)) block_norm_kernel(NormArgs a) {
+  __shared__ float s[2 * 3 * 16];
+  const int t = threadIdx.x % NT;
+  const int64_t row = (int64_t)blockIdx.x * (norm_block(NT) / NT) + threadIdx.x / NT;
+  if (row >= a.T) return;      // (whole waves, and only where no barrier follows)
+  const int64_t at = row * a.H;
+  const float rh = 1.f / (float)a.H;
+  Oct<TR> r[CH];
+  Oct<TY> x[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int i = (c * NT + t) * 8;
+    r[c].load(a.res, at + i, a.H - i);
+    if (a.y) x[c].load(a.y, at + i, a.H - i);
+  }
+  if (a.y) {
+    float ss[1] = {0.f};
+    if (a.post) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss[0] += x[c][j] * x[c][j];
+      row_sum<NT, 1>(ss, s, 0);
+    }
+    const float b = a.post ? 1.f / __builtin_sqrtf(ss[0] * rh + a.eps) : 1.f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int i = (c * NT + t) * 8;
+      Oct<TY> w, g;
+      if (a.w_post) w.load(a.w_post, i, a.H - i);
+      if (a.gate) g.load(a.gate, row * a.ld_gate + i, a.H - i);
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float p = x[c][j] * b;
+        if (a.w_post) p *= w[j];
+        if (a.gate) p *= g[j];
+        v[j] = a.alpha * r[c][j] + p;
+      }
+      r[c].pack(v);
+      r[c].store(a.res_out, at + i, a.H - i);
+    }
+  }
+  float ss[1] = {0.f};
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int i = (c * NT + t) * 8;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss[0] += i + j < a.H ? r[c][j] * r[c][j] : 0.f;
+  }
+  row_sum<NT, 1>(ss, s, 1);
+  const float k = 1.f / __builtin_sqrtf(ss[0] * rh + a.eps);
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int i = (c * NT + t) * 8;
+    Oct<TY> w, o;
+    if (a.w_pre) w.load(a.w_pre, i, a.H - i);
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] = r[c][j] * k;
+      if (a.w_pre) v[j] *= w[j];
+    }
+    o.pack(v);
+    o.store(a.n, at + i, a.H - i);
+  }
+}
+
+// Gradients.  A workgroup takes a contiguous run of rows and keeps its
+// column sums in registers; they leave once, as one row of a.part per
+// workgroup, for the summing kernel below (no atomics: the order is fixed).
+template <int TY, int TR, int NT, int CH>
+__global__ void __launch_bounds__(norm_block(NT)) block_norm_grad_kernel(NormArgs a) {
+  constexpr int RW = norm_block(NT) / NT;   // rows at a time
+  __shared__ float s[2 * 3 * 16];
+  const int t = threadIdx.x % NT;
+  const int64_t unit = (int64_t)blockIdx.x * RW + threadIdx.x / NT, units = (int64_t)gridDim.x * RW;
+  const int64_t lo = unit * a.T / units, hi = (unit + 1) * a.T / units;
+  const float rh = 1.f / (float)a.H;
+  float sums[3][CH][8];       // d_w_pre, d_w_post, d_gate
+#pragma unroll
+  for (int q = 0; q < 3; ++q)
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sums[q][c][j] = 0.f;
+  for (int64_t row = lo; row < hi; ++row) {
+    const int64_t at = row * a.H;
+    Oct<TR> r[CH], dr[CH];
+    Oct<TY> x[CH], dn[CH];
+    float q3[3] = {0.f, 0.f, 0.f};         // sums of r^2, g r, y^2
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int i = (c * NT + t) * 8;
+      r[c].load(a.res, at + i, a.H - i);
+      dn[c].load(a.d_n, at + i, a.H - i);
+      if (a.d_res) dr[c].load(a.d_res, at + i, a.H - i);
+      if (a.y) x[c].load(a.y, at + i, a.H - i);
+    }
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int i = (c * NT + t) * 8;
+      Oct<TY> w;
+      if (a.w_pre) w.load(a.w_pre, i, a.H - i);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float g = a.w_pre ? dn[c][j] * w[j] : dn[c][j];
+        q3[0] += r[c][j] * r[c][j];
+        q3[1] += g * r[c][j];
+        if (a.y && a.post) q3[2] += x[c][j] * x[c][j];
+      }
+    }
+    row_sum<NT, 3>(q3, s, 0);
+    const float k = 1.f / __builtin_sqrtf(q3[0] * rh + a.eps);
+    const float m = q3[1] * k * rh;          // mean(g u)
+    const float b = a.post ? 1.f / __builtin_sqrtf(q3[2] * rh + a.eps) : 1.f;
+    float d[CH][8], z[1] = {0.f};           // dr, sum of c v
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int i = (c * NT + t) * 8;
+      Oct<TY> w, g, wp, o;
+      Oct<TR> out;
+      float ov[8], dv[8];
+      if (a.w_pre) w.load(a.w_pre, i, a.H - i);
+      if (a.y && a.w_post) wp.load(a.w_post, i, a.H - i);
+      if (a.y && a.gate) g.load(a.gate, row * a.ld_gate + i, a.H - i);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float gg = a.w_pre ? dn[c][j] * w[j] : dn[c][j], u = r[c][j] * k;
+        float e = k * (gg - u * m);
+        if (a.d_res) e += dr[c][j];
+        sums[0][c][j] += dn[c][j] * u;
+        ov[j] = a.y ? a.alpha * e : e;
+        dv[j] = 0.f;
+        if (a.y) {
+          const float q = x[c][j] * b, p = a.w_post ? q * wp[j] : q;
+          const float eg = a.gate ? e * g[j] : e;
+          sums[1][c][j] += eg * q;
+          if (a.gate) {
+            if (a.ld_gate) dv[j] = e * p;
+            else sums[2][c][j] += e * p;
+          }
+          d[c][j] = a.w_post ? eg * wp[j] : eg;
+          z[0] += d[c][j] * q;
+        }
+      }
+      out.pack(ov);
+      out.store(a.d_r, at + i, a.H - i);
+      if (a.y && a.gate && a.ld_gate) o.pack(dv), o.store(a.d_gate, at + i, a.H - i);
+    }
+    if (a.y) {
+      if (a.post) row_sum<NT, 1>(z, s, 1);
+      const float mz = z[0] * rh;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int i = (c * NT + t) * 8;
+        Oct<TY> o;
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = a.post ? b * (d[c][j] - x[c][j] * b * mz) : d[c][j];
+        o.pack(v);
+        o.store(a.d_y, at + i, a.H - i);
+      }
+    } else if (NT > 64) {
+      __syncthreads();        // s is written again by the next row's first reduction
+    }
+    if (a.y && !a.post && NT > 64) __syncthreads();
+  }
+  if (!a.cols) return;
+#pragma unroll
+  for (int q = 0; q < 3; ++q)
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int i = (c * NT + t) * 8;
+      float *p = a.part + (unit * 3 + q) * a.H + i;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) if (i + j < a.H) p[j] = sums[q][c][j];
+    }
+}
+
+// Column sums of the units' partial sums: 64 columns per workgroup, 16
+// threads a column, joined in a fixed order.
+__global__ void __launch_bounds__(1024) norm_columns_kernel(const float *__restrict__ part, int32_t units, int32_t H,
+                                                            float *d_w_pre, float *d_w_post, float *d_gate) {
+  __shared__ float s[16][64];
+  const int q = blockIdx.y, c = blockIdx.x * 64 + (threadIdx.x & 63), w = threadIdx.x >> 6;
+  float *out = q == 0 ? d_w_pre : q == 1 ? d_w_post : d_gate;
+  if (!out) return;
+  float v = 0.f;
+  if (c < H)
+    for (int u = w; u < units; u += 16) v += part[((int64_t)u * 3 + q) * H + c];
+  s[w][threadIdx.x & 63] = v;
+  __syncthreads();
+  if (w == 0 && c < H) {
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v += s[i][threadIdx.x];
+    out[c] = v;
+  }
+}
+
+constexpr int kNormMaxH = 32768;
+constexpr int kGradGroups = 512;   // most workgroups of the gradient kernel
+
+// Threads per row for rows of H.
+static int norm_threads(int H) { return H <= 1024 ? 64 : H <= 4096 ? 256 : H <= 8192 ? 512 : 1024; }
+
+// Units (rows in flight) of the gradient kernel.
+static int grad_units(int T, int H) {
+  const int rw = norm_threads(H) == 64 ? 4 : 1;
+  const int groups = std::min((T + rw - 1) / rw, kGradGroups);
+  return groups * rw;
+}
+
+template <int TY, int TR, int NT, int CH>
+static void launch_norm(const NormArgs &a, bool grad, hipStream_t s) {
+  constexpr int RW = norm_block(NT) / NT;
+  if (grad)
+    hipLaunchKernelGGL((block_norm_grad_kernel<TY, TR, NT, CH>), dim3(grad_units(a.T, a.H) / RW), dim3(norm_block(NT)), 0, s, a);
+  else
+    hipLaunchKernelGGL((block_norm_kernel<TY, TR, NT, CH>), dim3((a.T + RW - 1) / RW), dim3(norm_block(NT)), 0, s, a);
+}
+
+template <int TY, int TR>
+static void launch_norm_h(const NormArgs &a, bool grad, hipStream_t s) {
+  if (a.H <= 512) launch_norm<TY, TR, 64, 1>(a, grad, s);
+  else if (a.H <= 1024) launch_norm<TY, TR, 64, 2>(a, grad, s);
+  else if (a.H <= 2048) launch_norm<TY, TR, 256, 1>(a, grad, s);
+  else if (a.H <= 4096) launch_norm<TY, TR, 256, 2>(a, grad, s);
+  else if (a.H <= 8192) launch_norm<TY, TR, 512, 2>(a, grad, s);
+  else if (a.H <= 16384) launch_norm<TY, TR, 1024, 2>(a, grad, s);
+  else launch_norm<TY, TR, 1024, 4>(a, grad, s);
+}
+
+static void launch_norm_types(const NormArgs &a, int ty, int tr, bool grad, hipStream_t s) {
+  if (ty == MOEQ_F16 && tr == MOEQ_F16) launch_norm_h<MOEQ_F16, MOEQ_F16>(a, grad, s);
+  else if (ty == MOEQ_F16) launch_norm_h<MOEQ_F16, MOEQ_F32>(a, grad, s);
+  else if (ty == MOEQ_BF16 && tr == MOEQ_BF16) launch_norm_h<MOEQ_BF16, MOEQ_BF16>(a, grad, s);
+  else if (ty == MOEQ_BF16) launch_norm_h<MOEQ_BF16, MOEQ_F32>(a, grad, s);
+  else launch_norm_h<MOEQ_F32, MOEQ_F32>(a, grad, s);
+}
+
+static moeq_status check_norm(const char *who, const moeq_norm *d, const void *y) {
+  if (!d) return fail(MOEQ_ERR_INVALID, "%s: null description", who);
+  if (d->T < 0 || d->H < 1) return fail(MOEQ_ERR_INVALID, "%s: T=%d, H=%d", who, d->T, d->H);
+  if (d->H > kNormMaxH) return fail(MOEQ_ERR_UNSUPPORTED, "%s: H=%d above %d", who, d->H, kNormMaxH);
+  if (d->dtype != MOEQ_F16 && d->dtype != MOEQ_BF16 && d->dtype != MOEQ_F32)
+    return fail(MOEQ_ERR_INVALID, "%s: bad dtype %d", who, d->dtype);
+  if (d->res_dtype != d->dtype && d->res_dtype != MOEQ_F32)
+    return fail(MOEQ_ERR_INVALID, "%s: bad res_dtype %d", who, d->res_dtype);
+  if (d->post_norm != 0 && d->post_norm != 1) return fail(MOEQ_ERR_INVALID, "%s: post_norm=%d", who, d->post_norm);
+  if (d->w_post && !d->post_norm) return fail(MOEQ_ERR_INVALID, "%s: w_post without post_norm", who);
+  if (d->gate_per_token != 0 && d->gate_per_token != 1)
+    return fail(MOEQ_ERR_INVALID, "%s: gate_per_token=%d", who, d->gate_per_token);
+  if (d->T && !y && (d->w_post || d->gate)) return fail(MOEQ_ERR_INVALID, "%s: w_post or gate without y", who);
+  if (!(d->eps > 0.f) || !(d->eps < 1e30f)) return fail(MOEQ_ERR_INVALID, "%s: eps must be positive and finite", who);
+  if (!(__builtin_fabsf(d->alpha) < 1e30f)) return fail(MOEQ_ERR_INVALID, "%s: alpha must be finite", who);
+  const uintptr_t m = d->dtype == MOEQ_F32 ? 3 : 1;
+  if (((uintptr_t)d->w_pre | (uintptr_t)d->w_post | (uintptr_t)d->gate | (uintptr_t)y) & m)
+    return fail(MOEQ_ERR_INVALID, "%s: an operand is not aligned to its elements", who);
+  return MOEQ_OK;
+}
+
+// Row operands that the call needs: present and aligned.
+static moeq_status need_rows(const char *who, const char *name, const void *p, int dtype) {
+  if (!p) return fail(MOEQ_ERR_INVALID, "%s: null %s", who, name);
+  if ((uintptr_t)p & (dtype == MOEQ_F32 ? 3 : 1)) return fail(MOEQ_ERR_INVALID, "%s: %s is not aligned to its elements", who, name);
+  return MOEQ_OK;
+}
+
+static NormArgs norm_args(const moeq_norm *d, const void *res, const void *y) {
+  NormArgs a{};
+  a.res = res;
+  a.y = y;
+  a.w_pre = d->w_pre;
+  a.w_post = d->w_post;
+  a.gate = d->gate;
+  a.ld_gate = d->gate_per_token ? d->H : 0;
+  a.T = d->T;
+  a.H = d->H;
+  a.post = d->post_norm;
+  a.alpha = d->alpha;
+  a.eps = d->eps;
+  return a;
+}
+
+}  // namespace moeq
+
+using namespace moeq;
+
+#define MOEQ_TRY(e) do { const moeq_status st_ = (e); if (st_ != MOEQ_OK) return st_; } while (0)
+
+MOEQ_API moeq_status moeq_block_norm(const moeq_norm *d, const void *residual, const void *y, void *res_out, void *n,
+                                     hipStream_t stream) {
+  const char *who = "block_norm";
+  MOEQ_TRY(check_norm(who, d, y));
+  if (!d->T) return MOEQ_OK;
+  MOEQ_TRY(need_rows(who, "residual", residual, d->res_dtype));
+  MOEQ_TRY(need_rows(who, "n", n, d->dtype));
+  if (y) MOEQ_TRY(need_rows(who, "res_out", res_out, d->res_dtype));
+  NormArgs a = norm_args(d, residual, y);
+  a.res_out = res_out;
+  a.n = n;
+  prof_begin("block_norm", stream);
+  launch_norm_types(a, d->dtype, d->res_dtype, false, stream);
+  prof_end("block_norm", stream);
+  return check_launch("block_norm");
+}
+
+MOEQ_API moeq_status moeq_block_norm_grad_workspace_size(int32_t T, int32_t H, size_t *bytes) {
+  const char *who = "block_norm_grad_workspace_size";
+  if (!bytes) return fail(MOEQ_ERR_INVALID, "%s: null bytes", who);
+  if (T < 0 || H < 1) return fail(MOEQ_ERR_INVALID, "%s: T=%d, H=%d", who, T, H);
+  if (H > kNormMaxH) return fail(MOEQ_ERR_UNSUPPORTED, "%s: H=%d above %d", who, H, kNormMaxH);
+  *bytes = (size_t)grad_units(T, H) * 3 * (size_t)H * 4;
+  return MOEQ_OK;
+}
+
+MOEQ_API moeq_status moeq_block_norm_grad(const moeq_norm *d, const void *res, const void *y, const void *d_res,
+                                          const void *d_n, void *d_residual, void *d_y, float *d_w_pre,
+                                          float *d_w_post, void *d_gate, void *ws, size_t ws_bytes,
+                                          hipStream_t stream) {
+  const char *who = "block_norm_grad";
+  MOEQ_TRY(check_norm(who, d, y));
+  if (d->T) {
+    MOEQ_TRY(need_rows(who, "res", res, d->res_dtype));
+    MOEQ_TRY(need_rows(who, "d_n", d_n, d->dtype));
+    MOEQ_TRY(need_rows(who, "d_residual", d_residual, d->res_dtype));
+    if (y) MOEQ_TRY(need_rows(who, "d_y", d_y, d->dtype));
+    if (d_res) MOEQ_TRY(need_rows(who, "d_res", d_res, d->res_dtype));
+  }
+  if (d->gate) {
+    if (d->T || !d->gate_per_token) MOEQ_TRY(need_rows(who, "d_gate", d_gate, d->gate_per_token ? d->dtype : MOEQ_F32));
+  } else if (d_gate) {
+    return fail(MOEQ_ERR_INVALID, "%s: d_gate without gate", who);
+  }
+  if (d_w_post && (!d->post_norm || (d->T && !y))) return fail(MOEQ_ERR_INVALID, "%s: d_w_post without post norm", who);
+  if (((uintptr_t)d_w_pre | (uintptr_t)d_w_post) & 3) return fail(MOEQ_ERR_INVALID, "%s: misaligned weight gradient", who);
+  float *g_cols = d->gate && !d->gate_per_token ? (float *)d_gate : nullptr;
+  const bool cols = d_w_pre || d_w_post || g_cols;
+  const int units = grad_units(d->T, d->H);
+  const size_t need = (size_t)units * 3 * (size_t)d->H * 4;
+  if (cols && need) {
+    if (!ws || ((uintptr_t)ws & 15)) return fail(MOEQ_ERR_INVALID, "%s: null or misaligned workspace", who);
+    if (ws_bytes < need) return fail(MOEQ_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", who, ws_bytes, need);
+  }
+  if (d->T) {
+    NormArgs a = norm_args(d, res, y);
+    a.d_res = d_res;
+    a.d_n = d_n;
+    a.d_r = d_residual;
+    a.d_y = d_y;
+    a.d_gate = d_gate;
+    a.part = (float *)ws;
+    a.cols = cols;
+    prof_begin("block_norm_grad", stream);
+    launch_norm_types(a, d->dtype, d->res_dtype, true, stream);
+    prof_end("block_norm_grad", stream);
+    MOEQ_TRY(check_launch("block_norm_grad"));
+  }
+  if (cols) {
+    prof_begin("norm_columns", stream);
+    hipLaunchKernelGGL(norm_columns_kernel, dim3((d->H + 63) / 64, 3), dim3(1024), 0, stream, (const float *)ws, units,
+                       d->H, d_w_pre, d_w_post, g_cols);
+    prof_end("norm_columns", stream);
+    MOEQ_TRY(check_launch("norm_columns"));
+  }
+  return MOEQ_OK;
+}

@@ -30,7 +30,7 @@ __global__ void __launch_bounds__(256) quantize_i8_kernel(const void *__restrict
   __shared__ float s_top[4];
   const RowScale r = row_scale<4>(top, bad, s_top);
   int8_t *dst = codes + row * ldc;
-  for (int c = threadIdx.x; c < cols; c += 256) dst[c] = (int8_t)i8_code(elt_at<TY>(src, c), r.inv);
+  for (int c = threadIdx.x; c < cols; c += 256) dst[c] = (int8_t)i8_code(elt_at<TY>(src, c), r);
   if (threadIdx.x == 0) scales[row] = r.scale;
 }
 

@@ -5,21 +5,27 @@
 namespace moeq {
 
 struct RowScale {
-  float inv, scale;   // code = rint(x * inv), value = code * scale
+  float scale;   // code = rint(x / scale), value = code * scale
+  bool zero;     // every code is 0
 };
 
-// The row's scale from its largest magnitude.  Below 2^-118 the reciprocal
-// would leave the fp32 range: such a row is coded as zeros.
+// The row's scale from its largest magnitude.  A row below 2^-118, whose
+// scale would be subnormal, is coded as zeros.
 __device__ __forceinline__ RowScale row_scale_of(float top, bool bad) {
-  if (bad) return RowScale{0.f, __builtin_nanf("")};
-  if (top < 0x1p-118f) return RowScale{0.f, 1.f};
-  return RowScale{127.f / top, top / 127.f};
+  if (bad) return RowScale{__builtin_nanf(""), true};
+  if (top < 0x1p-118f) return RowScale{1.f, true};
+  return RowScale{top / 127.f, false};
 }
 
-// x * inv rounded to the nearest integer, half to even.  |x| <= top keeps it
-// within 127.  (inv = 0: the row's codes are 0, also for an infinity or NaN.)
-__device__ __forceinline__ int i8_code(float x, float inv) {
-  return inv == 0.f ? 0 : (int)__builtin_rintf(x * inv);
+// x / scale rounded to the nearest integer, half to even; |x| <= top keeps
+// it within 127.  The quotient is a correctly rounded division: for 16-bit
+// x it then rounds as the exact 127 x / top does.  (With integers X, A < 2^11
+// and powers of two aside, 127 X / A differs from a half (2 n + 1) / 2 by 0
+// or by at least 1 / (2 A), far above the fp32 error; and where it is a
+// half, A is a multiple of 127 and the scale exact.  A product with 127 / top
+// would round some of those halves the wrong way.)
+__device__ __forceinline__ int i8_code(float x, RowScale r) {
+  return r.zero ? 0 : (int)__builtin_rintf(x / r.scale);
 }
 
 // row_scale_of for a workgroup of NW waves that each hold part of one row

@@ -535,6 +535,124 @@ def linear_i8_workspace_size(T, K):
     return n.value
 
 
+# ------------------------------------------------ norms around a block
+
+def _dense(t, shape, dtype, dev, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on another device than the other tensors")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _norm(res, dtype, y, w_pre, w_post, gate, alpha, eps, post_norm, dev):
+    """moeq_norm of the checked operands."""
+    T, H = res.shape
+    if dtype not in _DTYPE:
+        raise TypeError(f"{dtype} is not a type of the norms")
+    vec = (H,)
+    if y is not None:
+        _dense(y, res.shape, dtype, dev, "y")
+    if w_pre is not None:
+        _dense(w_pre, vec, dtype, dev, "w_pre")
+    if w_post is not None:
+        _dense(w_post, vec, dtype, dev, "w_post")
+    per_token = gate is not None and gate.dim() == 2
+    if gate is not None:
+        _dense(gate, res.shape if per_token else vec, dtype, dev, "gate")
+    p = lambda t: t.data_ptr() if t is not None else None
+    return _lib.Norm(T, H, _DTYPE[dtype], _DTYPE[res.dtype], p(w_pre), p(w_post), p(gate), int(per_token),
+                     int(bool(post_norm)), alpha, eps)
+
+
+def _res(res, name):
+    dev = res.get_device() if isinstance(res, torch.Tensor) else -1
+    if dev < 0:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if res.dim() != 2 or res.dtype not in _DTYPE:
+        raise TypeError(f"{name} must be [T, H] of fp16, bf16 or fp32, got {tuple(res.shape)} {res.dtype}")
+    _dense(res, res.shape, res.dtype, dev, name)
+    return dev
+
+
+def block_norm(residual, y=None, w_pre=None, w_post=None, gate=None, alpha=1.0, eps=1e-6, post_norm=True,
+               res_out=None, n_out=None):
+    """The norms between two blocks (see moeq_block_norm): returns (r', n)
+    with r' = alpha * residual + gate * (w_post * y / rms(y)) (y itself in
+    place of its norm without post_norm) and n = w_pre * r' / rms(r').
+
+    residual [T, H] (y's type or float32); y [T, H] fp16, bf16 or fp32, or
+    None (r' is the residual itself, n of w_pre's type); w_pre, w_post [H],
+    gate [H] or [T, H] of y's type, or None (ones).  res_out may be the
+    residual and n_out may be y (in place)."""
+    dev = _res(residual, "residual")
+    dtype = y.dtype if y is not None else w_pre.dtype if w_pre is not None else residual.dtype
+    d = _norm(residual, dtype, y, w_pre, w_post, gate, alpha, eps, post_norm, dev)
+    if y is None:
+        if res_out is not None:
+            raise ValueError("res_out is not written without y")
+        r = residual
+    elif res_out is None:
+        r = torch.empty_like(residual)
+    else:
+        r = res_out
+        _dense(r, residual.shape, residual.dtype, dev, "res_out")
+    if n_out is None:
+        n = torch.empty(residual.shape, dtype=dtype, device=residual.device)
+    else:
+        n = n_out
+        _dense(n, residual.shape, dtype, dev, "n_out")
+    _launch("moeq_block_norm", dev, d, residual.data_ptr(), y.data_ptr() if y is not None else None, r.data_ptr(),
+            n.data_ptr())
+    return r, n
+
+
+def block_norm_grad(res, d_n, y=None, d_res=None, w_pre=None, w_post=None, gate=None, alpha=1.0, eps=1e-6,
+                    post_norm=True, ws=None):
+    """Gradients of block_norm's inputs (see moeq_block_norm_grad) from those
+    of its outputs r' (d_res, or None) and n (d_n); res is the r' that it
+    returned.  Returns a dict: d_residual, and d_y, d_w_pre, d_w_post (fp32),
+    d_gate (fp32 [H], or [T, H] of the gate's type) for the inputs given.
+    ws: uint8 workspace tensor, or None for one of the call's own."""
+    dev = _res(res, "res")
+    if not isinstance(d_n, torch.Tensor):
+        raise TypeError("d_n must be a CUDA tensor")
+    d = _norm(res, d_n.dtype, y, w_pre, w_post, gate, alpha, eps, post_norm, dev)
+    T, H = res.shape
+    _dense(d_n, res.shape, d_n.dtype, dev, "d_n")
+    if d_res is not None:
+        _dense(d_res, res.shape, res.dtype, dev, "d_res")
+    out = {"d_residual": torch.empty_like(res)}
+    if y is not None:
+        out["d_y"] = torch.empty_like(y)
+    if w_pre is not None:
+        out["d_w_pre"] = torch.empty((H,), dtype=torch.float32, device=res.device)
+    if w_post is not None:
+        out["d_w_post"] = torch.empty((H,), dtype=torch.float32, device=res.device)
+    if gate is not None:
+        out["d_gate"] = torch.empty(gate.shape, dtype=gate.dtype if gate.dim() == 2 else torch.float32, device=res.device)
+    if ws is None:
+        ws = torch.empty((block_norm_grad_workspace_size(T, H),), dtype=torch.uint8, device=res.device)
+    else:
+        _like(ws, (torch.uint8,), 1, dev, "ws")
+    p = lambda t: t.data_ptr() if t is not None else None
+    _launch("moeq_block_norm_grad", dev, d, res.data_ptr(), p(y), p(d_res), d_n.data_ptr(), p(out["d_residual"]),
+            p(out.get("d_y")), p(out.get("d_w_pre")), p(out.get("d_w_post")), p(out.get("d_gate")), ws.data_ptr(),
+            ws.numel())
+    return out
+
+
+def block_norm_grad_workspace_size(T, H):
+    n = ctypes.c_size_t(0)
+    check(lib().moeq_block_norm_grad_workspace_size(T, H, ctypes.byref(n)), "moeq_block_norm_grad_workspace_size")
+    return n.value
+
+
 # ------------------------------------------------------------ profiling
 
 def profile_enable(on=True):

@@ -508,9 +508,8 @@ moeq_status moeq_grouped_wgrad(const moeq_groups *g, const void *dy, int64_t ldd
 
 /*
  * moeq_quantize_i8 — symmetric 8-bit codes of every row, in fp32:
- *   a = max |x|,  scale = a / 127,  code = rint(x * (127 / a))
- * (each quotient and product rounded to fp32, rint = half to even; codes in
- * -127..127).  A row with a < 2^-118 gets codes 0 and scale 1; a row that
+ *   a = max |x|,  scale = a / 127,  code = rint(x / scale)
+ * (each quotient rounded to fp32, rint = half to even; codes in -127..127).  A row with a < 2^-118 gets codes 0 and scale 1; a row that
  * holds an infinity or a NaN gets codes 0 and scale NaN (so that what is
  * computed from it is NaN).
  *   x DEVICE [rows, cols] of dtype MOEQ_F16, MOEQ_BF16 or MOEQ_F32;
@@ -541,6 +540,59 @@ moeq_status moeq_linear_i8_workspace_size(int32_t T, int32_t K, size_t *bytes);
 moeq_status moeq_linear_i8(const moeq_groups *g, const void *x, int64_t ldx, int32_t dtype, const int8_t *wq,
                            int64_t ldw, int64_t stride_w, const float *sw, int32_t N, int32_t K, void *y,
                            int64_t ldy, int32_t y_dtype, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* --------------------------------------------------- norms around a block -- */
+
+/*
+ * What joins one block (an expert layer, say) to the next: the block's
+ * output y is normed, gated and added to the scaled residual, and the sum is
+ * normed for the next block.  Per token, means over its H values:
+ *   p  = w_post * y / sqrt(mean(y^2) + eps)          (p = y if !post_norm)
+ *   r' = alpha * residual + gate * p                 rounded to res_dtype
+ *   n  = w_pre * r' / sqrt(mean(r'^2) + eps)         of the rounded r'
+ * Statistics and sums are fp32, each output rounded once.
+ *   T tokens, H values each (T >= 0, 1 <= H <= 32768); every matrix is
+ *   [T, H], rows one after the other, aligned to its elements.
+ *   dtype: MOEQ_F16, MOEQ_BF16 or MOEQ_F32, of y, n, the weights and the
+ *   gate; res_dtype: of residual and r', dtype or MOEQ_F32.
+ *   w_pre, w_post DEVICE [H] or NULL (ones; w_post only with post_norm);
+ *   gate DEVICE [H], or [T, H] with gate_per_token, or NULL (ones).
+ *   eps > 0; alpha finite.
+ */
+typedef struct {
+  int32_t T, H;
+  int32_t dtype, res_dtype;
+  const void *w_pre, *w_post, *gate;
+  int32_t gate_per_token, post_norm;
+  float alpha, eps;
+} moeq_norm;
+
+/*
+ * moeq_block_norm — r' into res_out and n.  Without a block (y NULL; no
+ * gate, no w_post) r' is the residual itself, which is not written again:
+ * n is its norm, res_out is not used.  res_out may be residual, and n may be
+ * y (in place); no other operands may overlap.
+ */
+moeq_status moeq_block_norm(const moeq_norm *d, const void *residual, const void *y, void *res_out, void *n,
+                            hipStream_t stream);
+
+/*
+ * moeq_block_norm_grad — gradients of all inputs from those of r' (d_res, of
+ * res_dtype, or NULL: zeros) and of n (d_n, of dtype), given the forward's
+ * res = r' and y (NULL without a block).  The rounding of r' passes the
+ * gradient unchanged.
+ *   d_residual DEVICE [T, H] res_dtype; d_y DEVICE [T, H] dtype (with y);
+ *   d_w_pre, d_w_post DEVICE [H] fp32 or NULL (not wanted);
+ *   d_gate (with gate) DEVICE [H] fp32, or [T, H] of dtype for a gate per
+ *   token.  Sums over the tokens are fp32 in a fixed order; zeros for T = 0.
+ *   ws DEVICE, 16-byte aligned, at least
+ *   moeq_block_norm_grad_workspace_size bytes (not needed when no sum over
+ *   the tokens is wanted).  Outputs may not overlap inputs.
+ */
+moeq_status moeq_block_norm_grad_workspace_size(int32_t T, int32_t H, size_t *bytes);
+moeq_status moeq_block_norm_grad(const moeq_norm *d, const void *res, const void *y, const void *d_res,
+                                 const void *d_n, void *d_residual, void *d_y, float *d_w_pre, float *d_w_post,
+                                 void *d_gate, void *ws, size_t ws_bytes, hipStream_t stream);
 
 /* ---------------------------------------------------------- profiling -- */
 

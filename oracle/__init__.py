@@ -16,6 +16,8 @@ Modules
   layer    a lazily quantized layer built from fp16 weights with ``ptq``
   products products of expert-sorted rows with one matrix per expert, their
            gradients, 8-bit codes of rows
+  norms    norms before and after a block with gate and residual scale, and
+           their gradients
 
 Everything is plain numpy in float64, except where the method fixes a storage
 precision (fp16 scales, LUT entries and factors; uint8 codes and zeros) —

@@ -41,7 +41,7 @@ def wgrad(dy, x, offsets, src):
 
 def code_i8(x):
     """(codes int8, scales fp32) of the rows of x (fp32 [rows, cols]): every
-    quotient and product rounded to fp32."""
+    quotient rounded to fp32."""
     x = np.asarray(x, dtype=np.float32)
     codes = np.zeros(x.shape, dtype=np.int8)
     scales = np.ones(x.shape[0], dtype=np.float32)
@@ -51,5 +51,5 @@ def code_i8(x):
             scales[r] = np.nan
         elif a >= np.float32(2.0 ** -118):
             scales[r] = a / np.float32(127)
-            codes[r] = np.rint(x[r] * (np.float32(127) / a)).astype(np.int8)
+            codes[r] = np.rint(x[r] / scales[r]).astype(np.int8)
     return codes, scales

@@ -177,13 +177,28 @@ def test_quantize_i8(rows, cols, dtype):
     if rows > 4:
         x[3, cols // 2], x[4, 0] = float("inf"), float("nan")
     if dtype != F16 and rows > 5:
-        x[5] = 2.0 ** -126     # below what the reciprocal can hold
+        x[5] = 2.0 ** -126     # its scale would be subnormal
         x[6] = 2.0 ** -118
     q, s = moeq.quantize_i8(x)
     with np.errstate(invalid="ignore"):
         qr, sr = products.code_i8(x.to(torch.float32).cpu().numpy())
     assert np.array_equal(q.cpu().numpy(), qr)
     assert np.array_equal(s.cpu().numpy(), sr, equal_nan=True)
+
+
+def test_codes_of_halves():
+    """Rows whose scale is a small integer: values half way between two codes
+    go to the even one."""
+    from bit_quantized_moe_token_amd import moeq
+    s = torch.arange(9, 17, dtype=torch.float32)[:, None]
+    x = (torch.arange(-127, 128, dtype=torch.float32)[None] / 2 * s).cuda()
+    x[:, 0] = 127 * s[:, 0].cuda()
+    for dtype in (F16, BF16, F32):
+        xr = x.to(dtype)
+        q, scale = moeq.quantize_i8(xr)
+        assert torch.equal(scale.cpu(), xr[:, 0].float().cpu() / 127)
+        want = torch.round(xr.double() / scale.double()[:, None])
+        assert torch.equal(q.double(), want)
 
 
 I8_SHAPES = SHAPES + [([201], 1, 1530, 1111), ([16], 1, 4096, 64), ([64], 1, 130, 300), ([4], 1, 16384, 32)]
