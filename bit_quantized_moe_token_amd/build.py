@@ -32,6 +32,9 @@ CFLAGS = [
 FILE_FLAGS = {
     "tiled_gu.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     "tiled_dn.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    "gemm_f16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    "gemm_bf16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    "gemm_i8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
 }
 
 

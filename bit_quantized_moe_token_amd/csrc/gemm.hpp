@@ -301,6 +301,67 @@ __device__ __forceinline__ void store4(const GemmArgs &a, int64_t o, f32x4 v, in
   }
 }
 
+// Output tile of a workgroup, the extent of r and, for the matrices'
+// gradient, the first j; all in scalar registers.
+template <int MODE, int BI, int BJ>
+__device__ __forceinline__ bool pick_tile(const GemmArgs &a, Tile *t, int *nr, int *j0) {
+  Tile v{};
+  int r = a.nr, j = 0;
+  if constexpr (MODE == kMats) {
+    const int n_it = (a.ni + BI - 1) / BI, n_jt = (a.nj + BJ - 1) / BJ, all = a.E * n_it * n_jt;
+    const int per = (all + 7) >> 3, idx = (int)blockIdx.x >> 3, L = ((int)blockIdx.x & 7) * per + idx;
+    if (idx >= per || L >= all) return false;
+    v.e = L / (n_it * n_jt);
+    const int in = L - v.e * n_it * n_jt;
+    j = in / n_it * BJ;
+    v.i0 = in % n_it * BI;
+    int lo, hi;
+    expert_rows(a, v.e, &lo, &hi);
+    v.row = lo;
+    r = hi - lo;
+    v.rows = a.nj - j;
+  } else {
+    if (!find_tile<BJ>(a, BI, &v)) return false;
+  }
+  t->e = __builtin_amdgcn_readfirstlane(v.e);
+  t->row = __builtin_amdgcn_readfirstlane(v.row);
+  t->rows = __builtin_amdgcn_readfirstlane(v.rows);
+  t->i0 = __builtin_amdgcn_readfirstlane(v.i0);
+  *nr = __builtin_amdgcn_readfirstlane(r);
+  *j0 = __builtin_amdgcn_readfirstlane(j);
+  return true;
+}
+
+// Writes the wave's TI x TJ accumulators (tiles of 16 x 16 from ib, jb).
+template <int TY, int MODE, int TI, int TJ>
+__device__ __forceinline__ void write_tile(const GemmArgs &a, const Tile &t, int j0, int ib, int jb,
+                                           const typename Elt<TY>::acc (&acc)[TI][TJ]) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int j = 0; j < TJ; ++j) {
+    const int x = jb + j * 16 + (lane & 15);   // row of the tile
+    if (x >= t.rows) continue;
+    float sc = 1.f;
+    if constexpr (TY == kI8) {
+      const int s = source_row(a, t.row + x);
+      sc = s >= 0 ? a.sj[s] : 0.f;
+    }
+    const int64_t ob = MODE == kMats ? (int64_t)t.e * a.e_out + (int64_t)(j0 + x) * a.ldo : (int64_t)(t.row + x) * a.ldo;
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      const int c = t.i0 + ib + i * 16 + 4 * (lane >> 4);
+      if (c >= a.ni) continue;
+      f32x4 v;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        v[q] = (float)acc[i][j][q];
+        if constexpr (TY == kI8) v[q] = v[q] * sc * (c + q < a.ni ? a.si[(int64_t)t.e * a.ni + c + q] : 0.f);
+      }
+      store4(a, ob + c, v, a.ni - c);
+    }
+  }
+}
+
 // ---- tiled kernel: a workgroup of WI x WJ waves computes BI x BJ outputs.
 template <int TY, int MODE, int BI, int BJ, int WI, int WJ>
 __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_staged_kernel(GemmArgs a) {
@@ -309,29 +370,12 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_staged_kernel(GemmArgs a
   constexpr uint32_t kTileI = BI * kStepBytes, kStage = kTileI + BJ * kStepBytes;
   using Acc = typename Elt<TY>::acc;
   extern __shared__ __attribute__((aligned(1024))) uint8_t gemm_lds[];
-  const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wi = wave % WI, wj = wave / WI;
 
   Tile t;
-  int nr = a.nr, j0 = 0;          // extent of r; first j (kMats)
-  if constexpr (MODE == kMats) {
-    const int n_it = (a.ni + BI - 1) / BI, n_jt = (a.nj + BJ - 1) / BJ;
-    const int per = (a.E * n_it * n_jt + 7) >> 3;
-    const int L = ((int)blockIdx.x & 7) * per + ((int)blockIdx.x >> 3);
-    if (((int)blockIdx.x >> 3) >= per || L >= a.E * n_it * n_jt) return;
-    t.e = L / (n_it * n_jt);
-    const int in = L - t.e * n_it * n_jt;
-    j0 = in / n_it * BJ;
-    t.i0 = in % n_it * BI;
-    int hi;
-    expert_rows(a, t.e, &t.row, &hi);
-    t.row = __builtin_amdgcn_readfirstlane(t.row);
-    nr = __builtin_amdgcn_readfirstlane(hi) - t.row;
-    t.rows = a.nj - j0;
-  } else {
-    if (!find_tile<BJ>(a, BI, &t)) return;
-  }
+  int nr, j0;          // extent of r; first j (kMats)
+  if (!pick_tile<MODE, BI, BJ>(a, &t, &nr, &j0)) return;
 
   StagedOperand<ES, BI, NW, RI> si;
   StagedOperand<ES, BJ, NW, RJ> sj;
@@ -394,29 +438,184 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_staged_kernel(GemmArgs a
     }
   }
 
+  write_tile<TY, MODE, TI, TJ>(a, t, j0, wi * TI * 16, wj * TJ * 16, acc);
+}
+
+// ---- Movement of an operand tile straight into LDS (buffer loads with an
+// LDS destination): the data never occupies registers.  Rows and bases must
+// be 16-byte aligned; what lies behind the buffer resource's range reads
+// zero, which gives the zeros behind the last row and the last r.
+__device__ __forceinline__ const uint8_t *uniform(const uint8_t *p) {   // into scalar registers
+  const uint64_t v = (uint64_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v), hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
+  return (const uint8_t *)(((uint64_t)hi << 32) | lo);
+}
+constexpr uint32_t kNowhere = 0x80000000u;   // an offset behind every range used here
+
+template <int ES, int R, int NW, bool RMAJ>
+struct DmaOperand {
+  static constexpr int NB = R / (8 * NW);   // 1 KiB blocks per wave
+  static_assert(R % (8 * NW) == 0, "blocks per wave");
+  static_assert(!RMAJ || (R % 128 == 0 && ES == 2), "256-byte swizzle groups of 16-bit elements");
+  uint32_t voff[NB];       // lane's offset from the resource's base (kNowhere: no such row)
+  __amdgpu_buffer_rsrc_t rs;
+  const uint8_t *base;     // r as row index: row 0 at the tile's first column
+  uint32_t ld, width;      // r as row index: bytes between rows, bytes of a row from the tile's first column
+  int bytes;               // r contiguous: valid bytes of a row
+
+  __device__ __forceinline__ static int block() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * NB; }
+  // 16-byte piece of the row that the lane moves in block i (r contiguous)
+  __device__ __forceinline__ static uint32_t piece(int i) {
+    const int l = threadIdx.x & 63, x = (block() + i) * 8 + (l >> 3);
+    return 16u * (uint32_t)((l & 7) ^ ((x >> 1) & 7));
+  }
+  // r contiguous: row(x) gives the tile row's offset from `from` or kNowhere
+  template <class RowOff>
+  __device__ __forceinline__ void rows(const uint8_t *from, uint32_t range, int row_bytes, RowOff row) {
+    rs = make_rsrc(uniform(from), __builtin_amdgcn_readfirstlane((int)range));
+    bytes = row_bytes;
 #pragma unroll
-  for (int j = 0; j < TJ; ++j) {
-    const int x = (wj * TJ + j) * 16 + (lane & 15);   // row of the tile
-    if (x >= t.rows) continue;
-    float sc = 1.f;
-    if constexpr (TY == kI8) {
-      const int s = source_row(a, t.row + x);
-      sc = s >= 0 ? a.sj[s] : 0.f;
-    }
-    const int64_t ob = MODE == kMats ? (int64_t)t.e * a.e_out + (int64_t)(j0 + x) * a.ldo : (int64_t)(t.row + x) * a.ldo;
-#pragma unroll
-    for (int i = 0; i < TI; ++i) {
-      const int c = t.i0 + (wi * TI + i) * 16 + 4 * (lane >> 4);
-      if (c >= a.ni) continue;
-      f32x4 v;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        v[q] = (float)acc[i][j][q];
-        if constexpr (TY == kI8) v[q] = v[q] * sc * (c + q < a.ni ? a.si[(int64_t)t.e * a.ni + c + q] : 0.f);
-      }
-      store4(a, ob + c, v, a.ni - c);
+    for (int i = 0; i < NB; ++i) {
+      const uint32_t o = row((block() + i) * 8 + ((int)(threadIdx.x & 63) >> 3));
+      voff[i] = o == kNowhere ? kNowhere : o + piece(i);
     }
   }
+  __device__ __forceinline__ void issue_rows(int t, uint8_t *tile) const {
+    if ((t + 1) * kStepBytes <= bytes) {
+#pragma unroll
+      for (int i = 0; i < NB; ++i) lds_dma_buf<16>(rs, voff[i], (uint32_t)t * kStepBytes, tile + (block() + i) * 1024);
+    } else {                 // the last step of a row that is no multiple of it
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+        lds_dma_buf<16>(rs, (int)piece(i) < bytes - t * kStepBytes ? voff[i] : kNowhere, (uint32_t)t * kStepBytes,
+                        tile + (block() + i) * 1024);
+    }
+  }
+  // r as row index: row of r within the step and byte column that the lane
+  // moves in block i
+  __device__ __forceinline__ static int row_in(int i) { return ((block() + i) * 1024 + (int)(threadIdx.x & 63) * 16) / (2 * R); }
+  __device__ __forceinline__ static uint32_t col_in(int i) {
+    const int o = (block() + i) * 1024 + (int)(threadIdx.x & 63) * 16, s = (o % (2 * R)) / 16;
+    return 16u * (uint32_t)(s ^ (2 * kmaj_swz(o / (2 * R))));
+  }
+  // consecutive rows from `from`
+  __device__ __forceinline__ void cols(const uint8_t *from, int64_t row_stride, int row_bytes) {
+    base = uniform(from);
+    ld = (uint32_t)row_stride;
+    width = (uint32_t)row_bytes;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) voff[i] = (uint32_t)row_in(i) * ld + col_in(i);
+  }
+  __device__ __forceinline__ void issue_cols(int t, int nr, uint8_t *tile) const {
+    const int left = std::min(64, nr - t * 64);
+    const auto r = make_rsrc(uniform(base + (int64_t)t * 64 * ld), (uint32_t)(left - 1) * ld + width);
+#pragma unroll
+    for (int i = 0; i < NB; ++i) lds_dma_buf<16>(r, voff[i], 0, tile + (block() + i) * 1024);
+  }
+  // rows given one by one (gathered): src[i], or negative for a row of zeros
+  __device__ __forceinline__ void gather(const uint8_t *from, uint32_t range, int64_t row_stride) {
+    rs = make_rsrc(uniform(from), __builtin_amdgcn_readfirstlane((int)range));
+    ld = (uint32_t)row_stride;
+  }
+  __device__ __forceinline__ void issue_gather(const int *src, uint8_t *tile) const {
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+      lds_dma_buf<16>(rs, src[i] < 0 ? kNowhere : (uint32_t)src[i] * ld + col_in(i), 0, tile + (block() + i) * 1024);
+  }
+};
+
+// The tiled kernel with both operands moved by DMA.  Two stages: while the
+// waves multiply step k, step k + 1 is on its way; one barrier per step.
+template <int TY, int MODE, int BI, int BJ, int WI, int WJ>
+__global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_dma_kernel(GemmArgs a) {
+  constexpr int ES = Elt<TY>::size, NW = WI * WJ, TI = BI / WI / 16, TJ = BJ / WJ / 16;
+  constexpr bool RI = MODE != kFwd, RJ = MODE == kMats;
+  constexpr uint32_t kTileI = BI * kStepBytes, kStage = kTileI + BJ * kStepBytes;
+  using Acc = typename Elt<TY>::acc;
+  extern __shared__ __attribute__((aligned(1024))) uint8_t gemm_lds[];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wi = wave % WI, wj = wave / WI;
+  Tile t;
+  int nr, j0;
+  if (!pick_tile<MODE, BI, BJ>(a, &t, &nr, &j0)) return;
+
+  using OpI = DmaOperand<ES, BI, NW, RI>;
+  using OpJ = DmaOperand<ES, BJ, NW, RJ>;
+  OpI di;
+  OpJ dj;
+  int src[OpI::NB];        // kMats: source rows of the next step to move
+  auto sources = [&](int k) {
+#pragma unroll
+    for (int i = 0; i < OpI::NB; ++i) {
+      const int r = k * 64 + OpI::row_in(i);
+      src[i] = r < nr ? source_row(a, t.row + r) : -1;
+    }
+  };
+  if constexpr (MODE == kMats) {
+    di.gather(a.I + (int64_t)t.i0 * ES, (uint32_t)(((int64_t)(a.T - 1) * a.ldi + a.ni - t.i0) * ES), a.ldi * ES);
+    dj.cols(a.J + ((int64_t)t.row * a.ldj + j0) * ES, a.ldj * ES, (a.nj - j0) * ES);
+    sources(0);
+  } else {
+    const uint8_t *wmat = a.I + (int64_t)t.e * a.e_i * ES;   // the expert's matrix
+    if constexpr (MODE == kRows) {
+      di.cols(wmat + (int64_t)t.i0 * ES, a.ldi * ES, (a.ni - t.i0) * ES);
+    } else {
+      const int n = std::min(BI, a.ni - t.i0);
+      di.rows(wmat + (int64_t)t.i0 * a.ldi * ES, (uint32_t)(((n - 1) * a.ldi + nr) * ES), nr * ES,
+              [&](int x) { return x < n ? (uint32_t)x * (uint32_t)(a.ldi * ES) : kNowhere; });
+    }
+    if (a.pairs) {
+      dj.rows(a.J, (uint32_t)(((int64_t)(a.T - 1) * a.ldj + nr) * ES), nr * ES, [&](int x) {
+        const int s = x < t.rows ? source_row(a, t.row + x) : -1;
+        return s >= 0 ? (uint32_t)s * (uint32_t)(a.ldj * ES) : kNowhere;
+      });
+    } else {
+      const int n = std::min(BJ, t.rows);
+      dj.rows(a.J + (int64_t)t.row * a.ldj * ES, (uint32_t)(((n - 1) * a.ldj + nr) * ES), nr * ES,
+              [&](int x) { return x < n ? (uint32_t)x * (uint32_t)(a.ldj * ES) : kNowhere; });
+    }
+  }
+  auto issue = [&](int k, uint8_t *st) {
+    if constexpr (MODE == kMats) di.issue_gather(src, st);
+    else if constexpr (MODE == kRows) di.issue_cols(k, nr, st);
+    else di.issue_rows(k, st);
+    if constexpr (RJ) dj.issue_cols(k, nr, st + kTileI);
+    else dj.issue_rows(k, st + kTileI);
+    if constexpr (MODE == kMats) sources(k + 1);
+  };
+
+  Acc acc[TI][TJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) acc[i][j] = Acc{0, 0, 0, 0};
+  const FragReader<BI, RI> fi(0);
+  const FragReader<BJ, RJ> fj(kTileI);
+  const int steps = (int)(((int64_t)nr * ES + kStepBytes - 1) / kStepBytes);
+  if (steps > 0) issue(0, gemm_lds);
+  uint32_t sb = 0;
+#pragma unroll 1
+  for (int k = 0; k < steps; ++k) {
+    vm_wait<0>();
+    __builtin_amdgcn_s_barrier();
+    // every wave has read the other stage (step k - 1) to its end
+    if (k + 1 < steps) issue(k + 1, gemm_lds + (sb ^ kStage));
+    const uint8_t *st = gemm_lds + sb;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      u32x4 x[TI], y[TJ];
+#pragma unroll
+      for (int i = 0; i < TI; ++i) x[i] = fi.read(st, wi * TI + i, s);
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) y[j] = fj.read(st, wj * TJ + j, s);
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) acc[i][j] = Elt<TY>::mma(x[i], y[j], acc[i][j]);
+    }
+    sb ^= kStage;
+  }
+  write_tile<TY, MODE, TI, TJ>(a, t, j0, wi * TI * 16, wj * TJ * 16, acc);
 }
 
 }  // namespace moeq

@@ -4,7 +4,7 @@
 namespace moeq {
 
 moeq_status launch_gemm_i8(const GemmArgs &a, hipStream_t s) {
-  return launch_staged<kI8, kFwd, 128, 128, 2, 2>(a, s, "gemm_i8");
+  return launch_mode<kI8, kFwd>(a, s, "gemm_i8");
 }
 
 }  // namespace moeq

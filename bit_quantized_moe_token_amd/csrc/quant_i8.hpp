@@ -19,11 +19,12 @@ __device__ __forceinline__ RowScale row_scale_of(float top, bool bad) {
 
 // x / scale rounded to the nearest integer, half to even; |x| <= top keeps
 // it within 127.  The quotient is a correctly rounded division: for 16-bit
-// x it then rounds as the exact 127 x / top does.  (With integers X, A < 2^11
-// and powers of two aside, 127 X / A differs from a half (2 n + 1) / 2 by 0
-// or by at least 1 / (2 A), far above the fp32 error; and where it is a
-// half, A is a multiple of 127 and the scale exact.  A product with 127 / top
-// would round some of those halves the wrong way.)
+// x it then rounds as the exact 127 x / top does, but for x = +-top / 2.
+// (With integers X, A < 2^11 and powers of two aside, 127 X / A differs from
+// a half n + 1/2 by 0 or by at least 1 / (2 A), far above the fp32 error;
+// and where it is a half with 2 n + 1 != 127, A is a multiple of 127 and the
+// scale exact.  A product with 127 / top would round some of those halves the
+// wrong way.)
 __device__ __forceinline__ int i8_code(float x, RowScale r) {
   return r.zero ? 0 : (int)__builtin_rintf(x / r.scale);
 }

@@ -74,6 +74,11 @@ SHAPES = [
     ([2] * 70 + [0] * 9 + [31], 8, 136, 72),
     ([1] * 200 + [0] * 56, 2, 64, 64),
     ([700], 1, 1030, 258),
+    ([33, 5], 2, 72, 2000),
+    ([1100, 3, 900, 0], 2, 136, 6664),      # enough tiles for the largest ones
+    ([9, 9, 9], 1, 40, 33),
+    ([50, 0, 70, 33], 1, 2056, 2104),       # and in the matrices' gradient
+    ([600, 2, 811], 2, 200, 6300),
 ]
 
 
@@ -196,9 +201,15 @@ def test_codes_of_halves():
     for dtype in (F16, BF16, F32):
         xr = x.to(dtype)
         q, scale = moeq.quantize_i8(xr)
-        assert torch.equal(scale.cpu(), xr[:, 0].float().cpu() / 127)
-        want = torch.round(xr.double() / scale.double()[:, None])
-        assert torch.equal(q.double(), want)
+        qr, sr = products.code_i8(xr.float().cpu().numpy())
+        assert np.array_equal(q.cpu().numpy(), qr) and np.array_equal(scale.cpu().numpy(), sr)
+        # fp16 and fp32 hold these rows exactly: the scale is s, and the
+        # quotients are exact.  (bf16 rounds 127 s, then s, so that quotients
+        # of x / scale in more bits are no halves any more: the fp32 quotient
+        # above is the definition.)
+        if dtype != BF16:
+            assert torch.equal(scale.cpu(), s[:, 0])
+            assert torch.equal(q.double(), torch.round(x.double() / s.double().cuda()))
 
 
 I8_SHAPES = SHAPES + [([201], 1, 1530, 1111), ([16], 1, 4096, 64), ([64], 1, 130, 300), ([4], 1, 16384, 32)]
