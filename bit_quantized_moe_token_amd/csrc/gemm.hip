@@ -109,9 +109,9 @@ moeq_status run_i8(const moeq_groups *g, const int8_t *xq, int64_t ldx, const fl
   return launch_gemm_i8(a, stream);
 }
 
-// Workspace of moeq_linear_i8: codes with rows padded to whole tile steps,
-// then the scales.
-int64_t code_ld(int32_t K) { return ((int64_t)K + kStepBytes - 1) / kStepBytes * kStepBytes; }
+// Workspace of moeq_linear_i8: codes with rows padded to 128 bytes, then the
+// scales.
+int64_t code_ld(int32_t K) { return ((int64_t)K + 127) / 128 * 128; }
 
 }  // namespace
 

@@ -13,6 +13,7 @@
 // The MFMA takes I as its first operand, so a lane ends with four
 // consecutive i of one j: outputs leave in 8- or 16-byte stores.
 #pragma once
+#include <type_traits>
 #include "common.hpp"
 
 namespace moeq {
@@ -66,9 +67,10 @@ struct Elt<kI8> {
   }
 };
 
-// A tile step covers 128 bytes of every row along r: 64 elements of 16 bits,
-// 128 of 8.  An MFMA consumes 64 of them (16 bytes per lane), two per step.
-constexpr int kStepBytes = 128;
+// A step covers 64 bytes of every row along r (32 elements of 16 bits, 64 of
+// 8): what one MFMA consumes, 16 bytes per lane.
+constexpr int kStepBytes = 64;
+constexpr int kStepRows = 32;    // rows of a step where r is the row index (16-bit elements)
 
 // First and one-past-last sorted row of expert e, within [0, P] whatever the
 // offsets hold.
@@ -162,7 +164,7 @@ __device__ __forceinline__ bool find_tile(const GemmArgs &a, int BI, Tile *t) {
 // 16 bytes at p of which the first n (elements of ES bytes) exist, the rest
 // zero.  p need only be aligned to an element.
 template <int ES>
-__device__ __forceinline__ u32x4 load_piece(const uint8_t *p, int64_t n) {
+__device__ __forceinline__ u32x4 load_piece(const uint8_t *p, int n) {
   u32x4 v = {0u, 0u, 0u, 0u};
   if (n >= 16) {
     struct __attribute__((packed, aligned(ES))) Raw { u32x4 v; };
@@ -179,45 +181,44 @@ __device__ __forceinline__ u32x4 load_piece(const uint8_t *p, int64_t n) {
   return v;
 }
 
-// ---- LDS layout of an operand tile of R rows (i or j) x 128 bytes of r,
-// 128 R bytes, moved in blocks of 1 KiB (16 bytes per lane).
+// ---- LDS layout of an operand tile of R rows (i or j) x 64 bytes of r, 64 R
+// bytes, moved in blocks of 1 KiB (16 bytes per lane).
 //
-// Operand stored with r contiguous: row after row, 128 bytes each; the
-// 16-byte piece c of row x sits in slot c ^ ((x / 2) % 8), so that the 16
+// Operand stored with r contiguous: row after row, 64 bytes each; the
+// 16-byte piece c of row x sits in slot c ^ ((x / 4) % 4), so that the 16
 // rows that an MFMA operand read touches (one piece each) cover all 64 banks
 // once.
 //
-// Operand stored with r as the row index (16-bit only): 64 rows of r, R
+// Operand stored with r as the row index (16-bit only): 32 rows of r, R
 // elements each; 32-byte pieces are permuted within each 256 bytes by
-// XOR with kmaj_swz(r), so that the rows of a transposing read (four of
+// XOR with rmaj_swz(r), so that the rows of a transposing read (four of
 // 32 bytes per 16 lanes) fall into different banks.
-__device__ __forceinline__ int kmaj_swz(int r) { return (r & 3) | ((r >> 1) & 4); }
+__device__ __forceinline__ int rmaj_swz(int r) { return (r & 3) | ((r >> 1) & 4); }
 
 // Fragment reads.  Lane l of an MFMA operand holds element l % 16 of the
-// 16-wide tile and 16 bytes of r (piece l / 16 of the step half s).
+// 16-wide tile and 16 bytes of r (piece l / 16 of the step).
 template <int R, bool RMAJ>
 struct FragReader {
-  uint32_t base[2];
-  __device__ __forceinline__ FragReader(uint32_t tile_base) {
+  uint32_t base;
+  // f0: first 16-wide tile of the wave (a multiple of 8 with RMAJ, so that
+  // tile f of the wave differs from it by an XOR and a multiple of 256 bytes)
+  __device__ __forceinline__ FragReader(uint32_t tile_base, int f0) {
     const int l = threadIdx.x & 63, g = l >> 4, x = l & 15;
     if constexpr (!RMAJ) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s) base[s] = tile_base + x * 128 + 16 * ((4 * s + g) ^ (x >> 1));
+      base = tile_base + (16 * f0 + x) * kStepBytes + 16 * (g ^ (x >> 2));
     } else {
       // lane x of the 16 supplies 8 bytes of row r = 8 g + x / 4 (+ 4 for the
-      // second read, + 32 for s = 1): columns 4 (x % 4) .. + 3 of the tile
+      // second read): columns 4 (x % 4) .. + 3 of the tile
       const int r = 8 * g + (x >> 2);
-      base[0] = tile_base + r * (2 * R) + 8 * (x & 3) + 32 * kmaj_swz(r);
-      base[1] = 0;
+      base = tile_base + r * (2 * R) + (8 * (x & 3) | 32 * ((f0 & 7) ^ rmaj_swz(r))) + (f0 >> 3) * 256;
     }
   }
-  // 16-wide tile f, step half s
-  __device__ __forceinline__ u32x4 read(const uint8_t *lds, int f, int s) const {
+  __device__ __forceinline__ u32x4 read(const uint8_t *lds, int f) const {
     if constexpr (!RMAJ) {
-      return *reinterpret_cast<const u32x4 *>(lds + base[s] + f * 2048);
+      return *reinterpret_cast<const u32x4 *>(lds + base + f * 16 * kStepBytes);
     } else {
       typedef short s16x4 __attribute__((ext_vector_type(4)));
-      const uint32_t o = (base[0] ^ (uint32_t)((f & 7) * 32)) + (f >> 3) * 256 + s * 32 * (2 * R);
+      const uint32_t o = (base ^ (uint32_t)((f & 7) * 32)) + (f >> 3) * 256;
       const auto p = (__attribute__((address_space(3))) s16x4 *)(lds + o);
       const auto q = (__attribute__((address_space(3))) s16x4 *)(lds + o + 4 * (2 * R));
       const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(p));
@@ -227,50 +228,119 @@ struct FragReader {
   }
 };
 
-// ---- Movement of an operand tile into LDS through registers: any element
-// alignment and row stride, 64-bit addresses.
-template <int ES, int R, int NW, bool RMAJ>
-struct StagedOperand {
-  static constexpr int NB = R / (8 * NW);   // 1 KiB blocks per wave
-  static_assert(R % (8 * NW) == 0, "blocks per wave");
+__device__ __forceinline__ const uint8_t *uniform(const uint8_t *p) {   // into scalar registers
+  const uint64_t v = (uint64_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v), hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
+  return (const uint8_t *)(((uint64_t)hi << 32) | lo);
+}
+
+// ---- Movement of an operand's steps into LDS.  A wave moves NB blocks of 1
+// KiB of every step.
+//
+// DMA: buffer loads with an LDS destination; the data never occupies
+// registers.  Bases and rows must be 16-byte aligned; what lies behind the
+// buffer resource's range reads zero, which gives the zeros behind the last
+// row and the last r.
+// Otherwise through registers: any element alignment and row stride, 64-bit
+// addresses; a step is loaded one step before it is stored.
+constexpr uint32_t kNowhere = 0x80000000u;   // an offset behind every range used here
+
+template <int ES, int R, int NW, bool RMAJ, bool DMA>
+struct Operand {
+  static constexpr int NB = R * kStepBytes / (1024 * NW);
+  static_assert(R * kStepBytes % (1024 * NW) == 0, "blocks per wave");
   static_assert(!RMAJ || (R % 128 == 0 && ES == 2), "256-byte swizzle groups of 16-bit elements");
-  const uint8_t *p[NB];    // r contiguous: the row's first byte (null: no such row)
-  int nr;                  // extent of r
-  u32x4 v[NB];
+  static constexpr int kDmaOps = DMA ? NB : 0;
+  __amdgpu_buffer_rsrc_t rs;
+  uint32_t voff[NB];       // DMA: lane's offset from the resource's base (kNowhere: no such row)
+  const uint8_t *p[NB];    // registers, r contiguous: the row's first byte (null: no such row)
+  const uint8_t *base;     // r as row index: the matrix (row 0 of the run) at the tile's first column
+  int64_t ld;              // bytes between rows
+  int nr, width;           // extent of r; bytes of a row: valid ones (r contiguous), or from the tile's first column
+  u32x4 v[NB];             // registers: the step on its way
 
-  __device__ __forceinline__ static int block() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * NB; }
+  __device__ __forceinline__ static int block(int i) { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * NB + i; }
+  // r contiguous: tile row and byte in the step that the lane moves in block i
+  __device__ __forceinline__ static int row_of(int i) { return block(i) * 16 + (int)((threadIdx.x & 63) >> 2); }
+  __device__ __forceinline__ static int piece_of(int i) { return 16 * (int)((threadIdx.x & 3) ^ ((row_of(i) >> 2) & 3)); }
+  // r as row index: row in the step and byte column
+  __device__ __forceinline__ static int r_of(int i) { return (block(i) * 1024 + (int)(threadIdx.x & 63) * 16) / (2 * R); }
+  __device__ __forceinline__ static int col_of(int i) {
+    const int o = block(i) * 1024 + (int)(threadIdx.x & 63) * 16;
+    return 16 * ((o % (2 * R)) / 16 ^ (2 * rmaj_swz(o / (2 * R))));
+  }
 
-  // r contiguous: `row(x)` gives the first byte of tile row x or null
-  template <class RowPtr>
-  __device__ __forceinline__ void rows(RowPtr row, int n_r) {
+  // r contiguous: row x of the tile starts `stride` bytes times index(x)
+  // (negative: a row of zeros) behind `from`; `last` the largest index
+  template <class Index>
+  __device__ __forceinline__ void rows(const uint8_t *from, int64_t stride, int64_t last, int n_r, Index index) {
     nr = n_r;
-#pragma unroll
-    for (int i = 0; i < NB; ++i) p[i] = row((block() + i) * 8 + ((threadIdx.x & 63) >> 3));
-  }
-  __device__ __forceinline__ void fetch_rows(int t) {
+    width = n_r * ES;
+    if constexpr (DMA) rs = make_rsrc(uniform(from), __builtin_amdgcn_readfirstlane((int)(last * stride + width)));
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
-      const int l = threadIdx.x & 63, x = (block() + i) * 8 + (l >> 3);
-      const int64_t o = (int64_t)t * kStepBytes + 16 * ((l & 7) ^ ((x >> 1) & 7));
-      v[i] = load_piece<ES>(p[i] + o, p[i] ? (int64_t)nr * ES - o : 0);
+      const int x = index(row_of(i));
+      if constexpr (DMA) voff[i] = x < 0 ? kNowhere : (uint32_t)x * (uint32_t)stride + (uint32_t)piece_of(i);
+      else p[i] = x < 0 ? nullptr : from + x * stride;
     }
   }
-  // r as row index: `row(r)` gives the first byte of row r (column i0) or null
-  template <class RowPtr>
-  __device__ __forceinline__ void fetch_cols(int t, RowPtr row, int n_cols) {
+  // r as row index: consecutive rows from `from` (at the tile's first column)
+  __device__ __forceinline__ void cols(const uint8_t *from, int64_t stride, int n_r, int row_bytes) {
+    base = uniform(from);
+    ld = stride;
+    nr = n_r;
+    width = row_bytes;
+    if constexpr (DMA) {
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const int l = threadIdx.x & 63, o = (block() + i) * 1024 + l * 16;
-      const int r = o / (2 * R), s = (o % (2 * R)) / 16;
-      const int c = 16 * (s ^ (2 * kmaj_swz(r)));      // byte column of the piece
-      const uint8_t *q = row(t * 64 + r);
-      v[i] = load_piece<ES>(q + c, q ? (int64_t)n_cols * ES - c : 0);
+      for (int i = 0; i < NB; ++i) voff[i] = (uint32_t)r_of(i) * (uint32_t)ld + (uint32_t)col_of(i);
     }
   }
-  __device__ __forceinline__ void store(uint8_t *tile) const {
+  // r as row index: rows given step by step
+  __device__ __forceinline__ void gather(const uint8_t *from, int64_t stride, int64_t last, int n_r, int row_bytes) {
+    cols(from, stride, n_r, row_bytes);
+    if constexpr (DMA) rs = make_rsrc(base, __builtin_amdgcn_readfirstlane((int)(last * stride + width)));
+  }
+
+  // DMA: step t into the tile at `dst` (steps behind the last: zeros)
+  __device__ __forceinline__ void dma_rows(int t, uint8_t *dst) const {
+    const int left = width - t * kStepBytes;
 #pragma unroll
     for (int i = 0; i < NB; ++i)
-      *reinterpret_cast<u32x4 *>(tile + (block() + i) * 1024 + (threadIdx.x & 63) * 16) = v[i];
+      lds_dma_buf<16>(rs, piece_of(i) < left ? voff[i] : kNowhere, (uint32_t)t * kStepBytes, dst + block(i) * 1024);
+  }
+  __device__ __forceinline__ void dma_cols(int t, uint8_t *dst) const {
+    const int left = std::min(kStepRows, nr - t * kStepRows);
+    const auto r = make_rsrc(uniform(base + (int64_t)t * kStepRows * ld), left > 0 ? (uint32_t)(left - 1) * (uint32_t)ld + (uint32_t)width : 0u);
+#pragma unroll
+    for (int i = 0; i < NB; ++i) lds_dma_buf<16>(r, voff[i], 0, dst + block(i) * 1024);
+  }
+  __device__ __forceinline__ void dma_gather(const int *src, uint8_t *dst) const {
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+      lds_dma_buf<16>(rs, src[i] < 0 ? kNowhere : (uint32_t)src[i] * (uint32_t)ld + (uint32_t)col_of(i), 0, dst + block(i) * 1024);
+  }
+  // registers: load step t, store what is loaded
+  __device__ __forceinline__ void load_rows(int t) {
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int o = t * kStepBytes + piece_of(i);
+      v[i] = load_piece<ES>(p[i] + o, p[i] ? width - o : 0);
+    }
+  }
+  __device__ __forceinline__ void load_cols(int t) {
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int r = t * kStepRows + r_of(i);
+      v[i] = load_piece<ES>(base + r * ld + col_of(i), r < nr ? width - col_of(i) : 0);
+    }
+  }
+  __device__ __forceinline__ void load_gather(const int *src) {
+#pragma unroll
+    for (int i = 0; i < NB; ++i) v[i] = load_piece<ES>(base + src[i] * ld + col_of(i), src[i] >= 0 ? width - col_of(i) : 0);
+  }
+  __device__ __forceinline__ void store(uint8_t *dst) const {
+#pragma unroll
+    for (int i = 0; i < NB; ++i) *reinterpret_cast<u32x4 *>(dst + block(i) * 1024 + (threadIdx.x & 63) * 16) = v[i];
   }
 };
 
@@ -362,172 +432,17 @@ __device__ __forceinline__ void write_tile(const GemmArgs &a, const Tile &t, int
   }
 }
 
-// ---- tiled kernel: a workgroup of WI x WJ waves computes BI x BJ outputs.
-template <int TY, int MODE, int BI, int BJ, int WI, int WJ>
-__global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_staged_kernel(GemmArgs a) {
-  constexpr int ES = Elt<TY>::size, NW = WI * WJ, TI = BI / WI / 16, TJ = BJ / WJ / 16;
-  constexpr bool RI = MODE != kFwd, RJ = MODE == kMats;
-  constexpr uint32_t kTileI = BI * kStepBytes, kStage = kTileI + BJ * kStepBytes;
-  using Acc = typename Elt<TY>::acc;
-  extern __shared__ __attribute__((aligned(1024))) uint8_t gemm_lds[];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wi = wave % WI, wj = wave / WI;
+// ---- tiled kernel: a workgroup of WI x WJ waves computes BI x BJ outputs,
+// walking r in steps through a ring of kRing LDS stages.
+//
+// While a wave multiplies step k out of registers it reads the fragments of
+// step k + 1 into a second set, so that the matrix pipe does not wait for LDS.  Steps up to k + 4 are on their way: before step k every
+// wave has taken step k's fragments into registers, which frees its stage.
+// One barrier per step.
+constexpr int kRing = 4;
 
-  Tile t;
-  int nr, j0;          // extent of r; first j (kMats)
-  if (!pick_tile<MODE, BI, BJ>(a, &t, &nr, &j0)) return;
-
-  StagedOperand<ES, BI, NW, RI> si;
-  StagedOperand<ES, BJ, NW, RJ> sj;
-  const uint8_t *wmat = a.I + (int64_t)t.e * a.e_i * ES;   // the expert's matrix (not kMats)
-  if constexpr (!RI) {
-    si.rows([&](int x) { return t.i0 + x < a.ni ? wmat + (int64_t)(t.i0 + x) * a.ldi * ES : nullptr; }, nr);
-  }
-  if constexpr (!RJ) {
-    sj.rows([&](int x) -> const uint8_t * {
-      const int s = x < t.rows ? source_row(a, t.row + x) : -1;
-      return s >= 0 ? a.J + (int64_t)s * a.ldj * ES : nullptr;
-    }, nr);
-  }
-  auto fetch = [&](int k) {
-    if constexpr (!RI) si.fetch_rows(k);
-    else if constexpr (MODE == kRows)
-      si.fetch_cols(k, [&](int r) { return r < nr ? wmat + ((int64_t)r * a.ldi + t.i0) * ES : nullptr; }, a.ni - t.i0);
-    else
-      si.fetch_cols(k, [&](int r) -> const uint8_t * {
-        const int s = r < nr ? source_row(a, t.row + r) : -1;
-        return s >= 0 ? a.I + ((int64_t)s * a.ldi + t.i0) * ES : nullptr;
-      }, a.ni - t.i0);
-    if constexpr (!RJ) sj.fetch_rows(k);
-    else sj.fetch_cols(k, [&](int r) { return r < nr ? a.J + ((int64_t)(t.row + r) * a.ldj + j0) * ES : nullptr; }, a.nj - j0);
-  };
-
-  Acc acc[TI][TJ];
-#pragma unroll
-  for (int i = 0; i < TI; ++i)
-#pragma unroll
-    for (int j = 0; j < TJ; ++j) acc[i][j] = Acc{0, 0, 0, 0};
-  const FragReader<BI, RI> fi(0);
-  const FragReader<BJ, RJ> fj(kTileI);
-  const int steps = (int)(((int64_t)nr * ES + kStepBytes - 1) / kStepBytes);
-  if (steps > 0) {
-    fetch(0);
-    si.store(gemm_lds);
-    sj.store(gemm_lds + kTileI);
-  }
-  for (int k = 0; k < steps; ++k) {
-    if (k + 1 < steps) fetch(k + 1);
-    __syncthreads();
-    const uint8_t *st = gemm_lds + (k & 1) * kStage;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      u32x4 x[TI], y[TJ];
-#pragma unroll
-      for (int i = 0; i < TI; ++i) x[i] = fi.read(st, wi * TI + i, s);
-#pragma unroll
-      for (int j = 0; j < TJ; ++j) y[j] = fj.read(st, wj * TJ + j, s);
-#pragma unroll
-      for (int i = 0; i < TI; ++i)
-#pragma unroll
-        for (int j = 0; j < TJ; ++j) acc[i][j] = Elt<TY>::mma(x[i], y[j], acc[i][j]);
-    }
-    // the other stage was last read before this step's barrier
-    if (k + 1 < steps) {
-      si.store(gemm_lds + ((k + 1) & 1) * kStage);
-      sj.store(gemm_lds + ((k + 1) & 1) * kStage + kTileI);
-    }
-  }
-
-  write_tile<TY, MODE, TI, TJ>(a, t, j0, wi * TI * 16, wj * TJ * 16, acc);
-}
-
-// ---- Movement of an operand tile straight into LDS (buffer loads with an
-// LDS destination): the data never occupies registers.  Rows and bases must
-// be 16-byte aligned; what lies behind the buffer resource's range reads
-// zero, which gives the zeros behind the last row and the last r.
-__device__ __forceinline__ const uint8_t *uniform(const uint8_t *p) {   // into scalar registers
-  const uint64_t v = (uint64_t)p;
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v), hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
-  return (const uint8_t *)(((uint64_t)hi << 32) | lo);
-}
-constexpr uint32_t kNowhere = 0x80000000u;   // an offset behind every range used here
-
-template <int ES, int R, int NW, bool RMAJ>
-struct DmaOperand {
-  static constexpr int NB = R / (8 * NW);   // 1 KiB blocks per wave
-  static_assert(R % (8 * NW) == 0, "blocks per wave");
-  static_assert(!RMAJ || (R % 128 == 0 && ES == 2), "256-byte swizzle groups of 16-bit elements");
-  uint32_t voff[NB];       // lane's offset from the resource's base (kNowhere: no such row)
-  __amdgpu_buffer_rsrc_t rs;
-  const uint8_t *base;     // r as row index: row 0 at the tile's first column
-  uint32_t ld, width;      // r as row index: bytes between rows, bytes of a row from the tile's first column
-  int bytes;               // r contiguous: valid bytes of a row
-
-  __device__ __forceinline__ static int block() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * NB; }
-  // 16-byte piece of the row that the lane moves in block i (r contiguous)
-  __device__ __forceinline__ static uint32_t piece(int i) {
-    const int l = threadIdx.x & 63, x = (block() + i) * 8 + (l >> 3);
-    return 16u * (uint32_t)((l & 7) ^ ((x >> 1) & 7));
-  }
-  // r contiguous: row(x) gives the tile row's offset from `from` or kNowhere
-  template <class RowOff>
-  __device__ __forceinline__ void rows(const uint8_t *from, uint32_t range, int row_bytes, RowOff row) {
-    rs = make_rsrc(uniform(from), __builtin_amdgcn_readfirstlane((int)range));
-    bytes = row_bytes;
-#pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const uint32_t o = row((block() + i) * 8 + ((int)(threadIdx.x & 63) >> 3));
-      voff[i] = o == kNowhere ? kNowhere : o + piece(i);
-    }
-  }
-  __device__ __forceinline__ void issue_rows(int t, uint8_t *tile) const {
-    if ((t + 1) * kStepBytes <= bytes) {
-#pragma unroll
-      for (int i = 0; i < NB; ++i) lds_dma_buf<16>(rs, voff[i], (uint32_t)t * kStepBytes, tile + (block() + i) * 1024);
-    } else {                 // the last step of a row that is no multiple of it
-#pragma unroll
-      for (int i = 0; i < NB; ++i)
-        lds_dma_buf<16>(rs, (int)piece(i) < bytes - t * kStepBytes ? voff[i] : kNowhere, (uint32_t)t * kStepBytes,
-                        tile + (block() + i) * 1024);
-    }
-  }
-  // r as row index: row of r within the step and byte column that the lane
-  // moves in block i
-  __device__ __forceinline__ static int row_in(int i) { return ((block() + i) * 1024 + (int)(threadIdx.x & 63) * 16) / (2 * R); }
-  __device__ __forceinline__ static uint32_t col_in(int i) {
-    const int o = (block() + i) * 1024 + (int)(threadIdx.x & 63) * 16, s = (o % (2 * R)) / 16;
-    return 16u * (uint32_t)(s ^ (2 * kmaj_swz(o / (2 * R))));
-  }
-  // consecutive rows from `from`
-  __device__ __forceinline__ void cols(const uint8_t *from, int64_t row_stride, int row_bytes) {
-    base = uniform(from);
-    ld = (uint32_t)row_stride;
-    width = (uint32_t)row_bytes;
-#pragma unroll
-    for (int i = 0; i < NB; ++i) voff[i] = (uint32_t)row_in(i) * ld + col_in(i);
-  }
-  __device__ __forceinline__ void issue_cols(int t, int nr, uint8_t *tile) const {
-    const int left = std::min(64, nr - t * 64);
-    const auto r = make_rsrc(uniform(base + (int64_t)t * 64 * ld), (uint32_t)(left - 1) * ld + width);
-#pragma unroll
-    for (int i = 0; i < NB; ++i) lds_dma_buf<16>(r, voff[i], 0, tile + (block() + i) * 1024);
-  }
-  // rows given one by one (gathered): src[i], or negative for a row of zeros
-  __device__ __forceinline__ void gather(const uint8_t *from, uint32_t range, int64_t row_stride) {
-    rs = make_rsrc(uniform(from), __builtin_amdgcn_readfirstlane((int)range));
-    ld = (uint32_t)row_stride;
-  }
-  __device__ __forceinline__ void issue_gather(const int *src, uint8_t *tile) const {
-#pragma unroll
-    for (int i = 0; i < NB; ++i)
-      lds_dma_buf<16>(rs, src[i] < 0 ? kNowhere : (uint32_t)src[i] * ld + col_in(i), 0, tile + (block() + i) * 1024);
-  }
-};
-
-// The tiled kernel with both operands moved by DMA.  Two stages: while the
-// waves multiply step k, step k + 1 is on its way; one barrier per step.
-template <int TY, int MODE, int BI, int BJ, int WI, int WJ>
-__global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_dma_kernel(GemmArgs a) {
+template <int TY, int MODE, int BI, int BJ, int WI, int WJ, bool DI, bool DJ>
+__global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) {
   constexpr int ES = Elt<TY>::size, NW = WI * WJ, TI = BI / WI / 16, TJ = BJ / WJ / 16;
   constexpr bool RI = MODE != kFwd, RJ = MODE == kMats;
   constexpr uint32_t kTileI = BI * kStepBytes, kStage = kTileI + BJ * kStepBytes;
@@ -539,81 +454,136 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_dma_kernel(GemmArgs a) {
   int nr, j0;
   if (!pick_tile<MODE, BI, BJ>(a, &t, &nr, &j0)) return;
 
-  using OpI = DmaOperand<ES, BI, NW, RI>;
-  using OpJ = DmaOperand<ES, BJ, NW, RJ>;
+  using OpI = Operand<ES, BI, NW, RI, DI>;
+  using OpJ = Operand<ES, BJ, NW, RJ, DJ>;
   OpI di;
   OpJ dj;
   int src[OpI::NB];        // kMats: source rows of the next step to move
   auto sources = [&](int k) {
 #pragma unroll
     for (int i = 0; i < OpI::NB; ++i) {
-      const int r = k * 64 + OpI::row_in(i);
+      const int r = k * kStepRows + OpI::r_of(i);
       src[i] = r < nr ? source_row(a, t.row + r) : -1;
     }
   };
+  const int64_t si = a.ldi * ES, sj = a.ldj * ES;
   if constexpr (MODE == kMats) {
-    di.gather(a.I + (int64_t)t.i0 * ES, (uint32_t)(((int64_t)(a.T - 1) * a.ldi + a.ni - t.i0) * ES), a.ldi * ES);
-    dj.cols(a.J + ((int64_t)t.row * a.ldj + j0) * ES, a.ldj * ES, (a.nj - j0) * ES);
+    di.gather(a.I + (int64_t)t.i0 * ES, si, a.T - 1, nr, (a.ni - t.i0) * ES);
+    dj.cols(a.J + (int64_t)t.row * sj + (int64_t)j0 * ES, sj, nr, (a.nj - j0) * ES);
     sources(0);
   } else {
     const uint8_t *wmat = a.I + (int64_t)t.e * a.e_i * ES;   // the expert's matrix
     if constexpr (MODE == kRows) {
-      di.cols(wmat + (int64_t)t.i0 * ES, a.ldi * ES, (a.ni - t.i0) * ES);
+      di.cols(wmat + (int64_t)t.i0 * ES, si, nr, (a.ni - t.i0) * ES);
     } else {
       const int n = std::min(BI, a.ni - t.i0);
-      di.rows(wmat + (int64_t)t.i0 * a.ldi * ES, (uint32_t)(((n - 1) * a.ldi + nr) * ES), nr * ES,
-              [&](int x) { return x < n ? (uint32_t)x * (uint32_t)(a.ldi * ES) : kNowhere; });
+      di.rows(wmat + t.i0 * si, si, n - 1, nr, [&](int x) { return x < n ? x : -1; });
     }
     if (a.pairs) {
-      dj.rows(a.J, (uint32_t)(((int64_t)(a.T - 1) * a.ldj + nr) * ES), nr * ES, [&](int x) {
-        const int s = x < t.rows ? source_row(a, t.row + x) : -1;
-        return s >= 0 ? (uint32_t)s * (uint32_t)(a.ldj * ES) : kNowhere;
-      });
+      dj.rows(a.J, sj, a.T - 1, nr, [&](int x) { return x < t.rows ? source_row(a, t.row + x) : -1; });
     } else {
       const int n = std::min(BJ, t.rows);
-      dj.rows(a.J + (int64_t)t.row * a.ldj * ES, (uint32_t)(((n - 1) * a.ldj + nr) * ES), nr * ES,
-              [&](int x) { return x < n ? (uint32_t)x * (uint32_t)(a.ldj * ES) : kNowhere; });
+      dj.rows(a.J + t.row * sj, sj, n - 1, nr, [&](int x) { return x < n ? x : -1; });
     }
   }
-  auto issue = [&](int k, uint8_t *st) {
-    if constexpr (MODE == kMats) di.issue_gather(src, st);
-    else if constexpr (MODE == kRows) di.issue_cols(k, nr, st);
-    else di.issue_rows(k, st);
-    if constexpr (RJ) dj.issue_cols(k, nr, st + kTileI);
-    else dj.issue_rows(k, st + kTileI);
-    if constexpr (MODE == kMats) sources(k + 1);
+  // Registers: the step loaded last goes into its stage, step k is loaded.
+  // DMA: step k goes into stage `st` on its own.
+  auto move = [&](int k, uint8_t *st) {
+    if constexpr (DI) {
+      if constexpr (MODE == kMats) di.dma_gather(src, st);
+      else if constexpr (MODE == kRows) di.dma_cols(k, st);
+      else di.dma_rows(k, st);
+    }
+    if constexpr (DJ) {
+      if constexpr (RJ) dj.dma_cols(k, st + kTileI);
+      else dj.dma_rows(k, st + kTileI);
+    }
+    if constexpr (MODE == kMats && DI) sources(k + 1);
   };
+  auto load = [&](int k) {
+    if constexpr (!DI) {
+      if constexpr (MODE == kMats) di.load_gather(src), sources(k + 1);
+      else if constexpr (MODE == kRows) di.load_cols(k);
+      else di.load_rows(k);
+    }
+    if constexpr (!DJ) {
+      if constexpr (RJ) dj.load_cols(k);
+      else dj.load_rows(k);
+    }
+  };
+  auto store = [&](uint8_t *st) {
+    if constexpr (!DI) di.store(st);
+    if constexpr (!DJ) dj.store(st + kTileI);
+  };
+  constexpr bool kRegs = !DI || !DJ;
+  constexpr int kOps = OpI::kDmaOps + OpJ::kDmaOps;
 
   Acc acc[TI][TJ];
 #pragma unroll
   for (int i = 0; i < TI; ++i)
 #pragma unroll
     for (int j = 0; j < TJ; ++j) acc[i][j] = Acc{0, 0, 0, 0};
-  const FragReader<BI, RI> fi(0);
-  const FragReader<BJ, RJ> fj(kTileI);
+  const FragReader<BI, RI> fi(0, wi * TI);
+  const FragReader<BJ, RJ> fj(kTileI, wj * TJ);
   const int steps = (int)(((int64_t)nr * ES + kStepBytes - 1) / kStepBytes);
-  if (steps > 0) issue(0, gemm_lds);
-  uint32_t sb = 0;
-#pragma unroll 1
-  for (int k = 0; k < steps; ++k) {
-    vm_wait<0>();
+  if (steps > 0) {
+#pragma unroll
+    for (int k = 0; k < kRing; ++k) {
+      if (kRegs && k < kRing - 1) {
+        load(k);
+        store(gemm_lds + k * kStage);
+      }
+      move(k, gemm_lds + k * kStage);
+    }
+    if (kRegs) load(kRing - 1);
+    lgkm_vm_wait<(kRing - 1) * kOps>();
     __builtin_amdgcn_s_barrier();
-    // every wave has read the other stage (step k - 1) to its end
-    if (k + 1 < steps) issue(k + 1, gemm_lds + (sb ^ kStage));
-    const uint8_t *st = gemm_lds + sb;
+    u32x4 x[2][TI], y[2][TJ];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      u32x4 x[TI], y[TJ];
+    for (int i = 0; i < TI; ++i) x[0][i] = fi.read(gemm_lds, i);
 #pragma unroll
-      for (int i = 0; i < TI; ++i) x[i] = fi.read(st, wi * TI + i, s);
+    for (int j = 0; j < TJ; ++j) y[0][j] = fj.read(gemm_lds, j);
+    uint32_t sb = 0;         // stage of step k
+    // step k, its fragments in set c
+    auto step = [&](int k, auto c) {
+      constexpr int C = decltype(c)::value, N = 1 - C;
+      lgkm_vm_wait<(kRing - 2) * kOps>();
+      __builtin_amdgcn_s_barrier();
+      const uint32_t sn = sb == (kRing - 1) * kStage ? 0u : sb + kStage;
+      // registers: step k + 3 goes behind the ring's newest stage
+      if constexpr (kRegs) store(gemm_lds + (sb == 0 ? (kRing - 1) * kStage : sb - kStage));
+      move(k + kRing, gemm_lds + sb);
+      if constexpr (kRegs) load(k + kRing);
+      __builtin_amdgcn_sched_barrier(0);
+      const uint8_t *st = gemm_lds + sn;
 #pragma unroll
-      for (int j = 0; j < TJ; ++j) y[j] = fj.read(st, wj * TJ + j, s);
+      for (int j = 0; j < TJ; ++j) y[N][j] = fj.read(st, j);
+#pragma unroll
+      for (int i = 0; i < TI; ++i) x[N][i] = fi.read(st, i);
 #pragma unroll
       for (int i = 0; i < TI; ++i)
 #pragma unroll
-        for (int j = 0; j < TJ; ++j) acc[i][j] = Elt<TY>::mma(x[i], y[j], acc[i][j]);
+        for (int j = 0; j < TJ; ++j) acc[i][j] = Elt<TY>::mma(x[C][i], y[C][j], acc[i][j]);
+      // the reads between the first three quarters of the MFMAs, so that the
+      // last quarter covers their latency
+      constexpr int kReads = TI * (RI ? 2 : 1) + TJ * (RJ ? 2 : 1), kPer = std::max(1, TI * TJ * 3 / 4 / kReads);
+#pragma unroll
+      for (int q = 0; q < kReads; ++q) {
+        __builtin_amdgcn_sched_group_barrier(0x008, kPer, 0);   // MFMA
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);      // LDS read
+      }
+      __builtin_amdgcn_sched_group_barrier(0x008, TI * TJ, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      sb = sn;
+    };
+    int k = 0;
+#pragma unroll 1
+    for (; k + 1 < steps; k += 2) {
+      step(k, std::integral_constant<int, 0>{});
+      step(k + 1, std::integral_constant<int, 1>{});
     }
-    sb ^= kStage;
+    if (k < steps) step(k, std::integral_constant<int, 0>{});
+    vm_wait<0>();            // (the zeros of steps behind the last are still on their way)
   }
   write_tile<TY, MODE, TI, TJ>(a, t, j0, wi * TI * 16, wj * TJ * 16, acc);
 }

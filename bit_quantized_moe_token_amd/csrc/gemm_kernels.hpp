@@ -22,11 +22,9 @@ template <int TY, int MODE, int BI, int BJ, int WI, int WJ, bool DMA>
 moeq_status launch_tiles(const GemmArgs &a, hipStream_t s, const char *name) {
   const int64_t grid = tile_grid<MODE, BI, BJ>(a);
   if (grid > kMaxGrid) return fail(MOEQ_ERR_UNSUPPORTED, "%s: too many tiles", name);
-  const dim3 g((unsigned)grid), b(64 * WI * WJ);
-  constexpr size_t lds = 2 * (BI + BJ) * kStepBytes;
   prof_begin(name, s);
-  if constexpr (DMA) hipLaunchKernelGGL((gemm_dma_kernel<TY, MODE, BI, BJ, WI, WJ>), g, b, lds, s, a);
-  else hipLaunchKernelGGL((gemm_staged_kernel<TY, MODE, BI, BJ, WI, WJ>), g, b, lds, s, a);
+  hipLaunchKernelGGL((gemm_tile_kernel<TY, MODE, BI, BJ, WI, WJ, DMA, DMA>), dim3((unsigned)grid), dim3(64 * WI * WJ),
+                     kRing * (BI + BJ) * kStepBytes, s, a);
   prof_end(name, s);
   return check_launch(name);
 }
