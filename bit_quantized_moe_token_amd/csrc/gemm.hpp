@@ -185,14 +185,18 @@ __device__ __forceinline__ u32x4 load_piece(const uint8_t *p, int n) {
 // bytes, moved in blocks of 1 KiB (16 bytes per lane).
 //
 // Operand stored with r contiguous: row after row, 64 bytes each; the
-// 16-byte piece c of row x sits in slot c ^ ((x / 4) % 4), so that the 16
-// rows that an MFMA operand read touches (one piece each) cover all 64 banks
-// once.
+// 16-byte piece c of row x sits in slot c ^ kmaj_swz(x).  A 16-byte read of a
+// wave goes through LDS in four passes of 16 lanes: lanes 0-3, 12-15, 20-27,
+// the other 16 of the first 32, and the same of the last 32.  An MFMA
+// operand read has row l % 16, piece l / 16 in lane l; with s(q) = 0, 2, 3, 1
+// for rows 4 q .. 4 q + 3 each pass covers all 64 banks once (s(q) = q gives
+// two-way conflicts, half of the LDS cycles by SQ_LDS_BANK_CONFLICT).
 //
 // Operand stored with r as the row index (16-bit only): 32 rows of r, R
 // elements each; 32-byte pieces are permuted within each 256 bytes by
 // XOR with rmaj_swz(r), so that the rows of a transposing read (four of
 // 32 bytes per 16 lanes) fall into different banks.
+__device__ __forceinline__ int kmaj_swz(int x) { return (x >> 1 & 2) ^ (x >> 3 & 1) * 3; }
 __device__ __forceinline__ int rmaj_swz(int r) { return (r & 3) | ((r >> 1) & 4); }
 
 // Fragment reads.  Lane l of an MFMA operand holds element l % 16 of the
@@ -205,7 +209,7 @@ struct FragReader {
   __device__ __forceinline__ FragReader(uint32_t tile_base, int f0) {
     const int l = threadIdx.x & 63, g = l >> 4, x = l & 15;
     if constexpr (!RMAJ) {
-      base = tile_base + (16 * f0 + x) * kStepBytes + 16 * (g ^ (x >> 2));
+      base = tile_base + (16 * f0 + x) * kStepBytes + 16 * (g ^ kmaj_swz(x));
     } else {
       // lane x of the 16 supplies 8 bytes of row r = 8 g + x / 4 (+ 4 for the
       // second read): columns 4 (x % 4) .. + 3 of the tile
@@ -262,7 +266,7 @@ struct Operand {
   __device__ __forceinline__ static int block(int i) { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * NB + i; }
   // r contiguous: tile row and byte in the step that the lane moves in block i
   __device__ __forceinline__ static int row_of(int i) { return block(i) * 16 + (int)((threadIdx.x & 63) >> 2); }
-  __device__ __forceinline__ static int piece_of(int i) { return 16 * (int)((threadIdx.x & 3) ^ ((row_of(i) >> 2) & 3)); }
+  __device__ __forceinline__ static int piece_of(int i) { return 16 * ((int)(threadIdx.x & 3) ^ kmaj_swz(row_of(i))); }
   // r as row index: row in the step and byte column
   __device__ __forceinline__ static int r_of(int i) { return (block(i) * 1024 + (int)(threadIdx.x & 63) * 16) / (2 * R); }
   __device__ __forceinline__ static int col_of(int i) {
@@ -301,23 +305,18 @@ struct Operand {
     if constexpr (DMA) rs = make_rsrc(base, __builtin_amdgcn_readfirstlane((int)(last * stride + width)));
   }
 
-  // DMA: step t into the tile at `dst` (steps behind the last: zeros)
-  __device__ __forceinline__ void dma_rows(int t, uint8_t *dst) const {
-    const int left = width - t * kStepBytes;
-#pragma unroll
-    for (int i = 0; i < NB; ++i)
-      lds_dma_buf<16>(rs, piece_of(i) < left ? voff[i] : kNowhere, (uint32_t)t * kStepBytes, dst + block(i) * 1024);
+  // DMA: block i of step t into the tile at `dst` (steps behind the last:
+  // zeros)
+  __device__ __forceinline__ void dma_rows(int i, int t, uint8_t *dst) const {
+    lds_dma_buf<16>(rs, piece_of(i) < width - t * kStepBytes ? voff[i] : kNowhere, (uint32_t)t * kStepBytes, dst + block(i) * 1024);
   }
-  __device__ __forceinline__ void dma_cols(int t, uint8_t *dst) const {
+  __device__ __forceinline__ void dma_cols(int i, int t, uint8_t *dst) const {
     const int left = std::min(kStepRows, nr - t * kStepRows);
     const auto r = make_rsrc(uniform(base + (int64_t)t * kStepRows * ld), left > 0 ? (uint32_t)(left - 1) * (uint32_t)ld + (uint32_t)width : 0u);
-#pragma unroll
-    for (int i = 0; i < NB; ++i) lds_dma_buf<16>(r, voff[i], 0, dst + block(i) * 1024);
+    lds_dma_buf<16>(r, voff[i], 0, dst + block(i) * 1024);
   }
-  __device__ __forceinline__ void dma_gather(const int *src, uint8_t *dst) const {
-#pragma unroll
-    for (int i = 0; i < NB; ++i)
-      lds_dma_buf<16>(rs, src[i] < 0 ? kNowhere : (uint32_t)src[i] * (uint32_t)ld + (uint32_t)col_of(i), 0, dst + block(i) * 1024);
+  __device__ __forceinline__ void dma_gather(int i, int src, uint8_t *dst) const {
+    lds_dma_buf<16>(rs, src < 0 ? kNowhere : (uint32_t)src * (uint32_t)ld + (uint32_t)col_of(i), 0, dst + block(i) * 1024);
   }
   // registers: load step t, store what is loaded
   __device__ __forceinline__ void load_rows(int t) {
@@ -488,17 +487,25 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) 
   }
   // Registers: the step loaded last goes into its stage, step k is loaded.
   // DMA: step k goes into stage `st` on its own.
-  auto move = [&](int k, uint8_t *st) {
+  constexpr int kOps = OpI::kDmaOps + OpJ::kDmaOps;
+  auto move = [&](int q, int k, uint8_t *st) {   // q-th DMA of step k
     if constexpr (DI) {
-      if constexpr (MODE == kMats) di.dma_gather(src, st);
-      else if constexpr (MODE == kRows) di.dma_cols(k, st);
-      else di.dma_rows(k, st);
+      if (q < OpI::NB) {
+        if constexpr (MODE == kMats) di.dma_gather(q, src[q], st);
+        else if constexpr (MODE == kRows) di.dma_cols(q, k, st);
+        else di.dma_rows(q, k, st);
+      }
     }
     if constexpr (DJ) {
-      if constexpr (RJ) dj.dma_cols(k, st + kTileI);
-      else dj.dma_rows(k, st + kTileI);
+      const int j = q - OpI::kDmaOps;
+      if (j >= 0 && j < OpJ::NB) {
+        if constexpr (RJ) dj.dma_cols(j, k, st + kTileI);
+        else dj.dma_rows(j, k, st + kTileI);
+      }
     }
-    if constexpr (MODE == kMats && DI) sources(k + 1);
+    if constexpr (MODE == kMats && DI) {
+      if (q == kOps - 1) sources(k + 1);
+    }
   };
   auto load = [&](int k) {
     if constexpr (!DI) {
@@ -516,7 +523,6 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) 
     if constexpr (!DJ) dj.store(st + kTileI);
   };
   constexpr bool kRegs = !DI || !DJ;
-  constexpr int kOps = OpI::kDmaOps + OpJ::kDmaOps;
 
   Acc acc[TI][TJ];
 #pragma unroll
@@ -533,7 +539,8 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) 
         load(k);
         store(gemm_lds + k * kStage);
       }
-      move(k, gemm_lds + k * kStage);
+#pragma unroll
+      for (int q = 0; q < kOps; ++q) move(q, k, gemm_lds + k * kStage);
     }
     if (kRegs) load(kRing - 1);
     lgkm_vm_wait<(kRing - 1) * kOps>();
@@ -552,28 +559,42 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) 
       const uint32_t sn = sb == (kRing - 1) * kStage ? 0u : sb + kStage;
       // registers: step k + 3 goes behind the ring's newest stage
       if constexpr (kRegs) store(gemm_lds + (sb == 0 ? (kRing - 1) * kStage : sb - kStage));
-      move(k + kRing, gemm_lds + sb);
       if constexpr (kRegs) load(k + kRing);
       __builtin_amdgcn_sched_barrier(0);
       const uint8_t *st = gemm_lds + sn;
+      // The MFMAs in kSeg parts.  A part starts with its share of the DMA
+      // operations (all at once after the barrier, they hold the waves up: a
+      // CU takes one in about 16 cycles) and has its share of the next step's
+      // fragment reads between its MFMAs; the last part has none, so that
+      // its MFMAs cover their latency.
+      constexpr int kSeg = TI < 4 ? TI : 4, kRd = kSeg > 1 ? kSeg - 1 : 1, IS = TI / kSeg;
+      constexpr int kReads = TI + TJ, kInsI = RI ? 2 : 1, kInsJ = RJ ? 2 : 1;
 #pragma unroll
-      for (int j = 0; j < TJ; ++j) y[N][j] = fj.read(st, j);
+      for (int g = 0; g < kSeg; ++g) {
 #pragma unroll
-      for (int i = 0; i < TI; ++i) x[N][i] = fi.read(st, i);
+        for (int q = 0; q < kOps; ++q)
+          if (q * kSeg / std::max(kOps, 1) == g) move(q, k + kRing, gemm_lds + sb);
+        int ins = 0;
 #pragma unroll
-      for (int i = 0; i < TI; ++i)
+        for (int f = 0; f < kReads; ++f)
+          if (f * kRd / kReads == g) {
+            if (f < TJ) y[N][f] = fj.read(st, f), ins += kInsJ;
+            else x[N][f - TJ] = fi.read(st, f - TJ), ins += kInsI;
+          }
 #pragma unroll
-        for (int j = 0; j < TJ; ++j) acc[i][j] = Elt<TY>::mma(x[C][i], y[C][j], acc[i][j]);
-      // the reads between the first three quarters of the MFMAs, so that the
-      // last quarter covers their latency
-      constexpr int kReads = TI * (RI ? 2 : 1) + TJ * (RJ ? 2 : 1), kPer = std::max(1, TI * TJ * 3 / 4 / kReads);
+        for (int i = g * IS; i < (g + 1) * IS; ++i)
 #pragma unroll
-      for (int q = 0; q < kReads; ++q) {
-        __builtin_amdgcn_sched_group_barrier(0x008, kPer, 0);   // MFMA
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);      // LDS read
+          for (int j = 0; j < TJ; ++j) acc[i][j] = Elt<TY>::mma(x[C][i], y[C][j], acc[i][j]);
+#pragma unroll
+        for (int f = 0; f < kReads * 2; ++f) {
+          if (f < ins) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // MFMA
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // LDS read
+          }
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, TI * TJ, 0);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      __builtin_amdgcn_sched_group_barrier(0x008, TI * TJ, 0);
-      __builtin_amdgcn_sched_barrier(0);
       sb = sn;
     };
     int k = 0;
