@@ -70,6 +70,12 @@ GemmArgs base_args(const moeq_groups *g) {
   a.P = g->P;
   a.T = g->T;
   a.kdiv = g->pairs ? (uint32_t)g->k : 1u;
+  if (a.kdiv > 1) {     // see pair_row
+    int L = 1;
+    while ((1ull << L) < a.kdiv) ++L;
+    a.kmul = (uint32_t)((1ull << (31 + L)) / a.kdiv + 1);
+    a.kshift = L - 1;
+  }
   return a;
 }
 

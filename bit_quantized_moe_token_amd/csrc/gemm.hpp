@@ -34,7 +34,8 @@ struct GemmArgs {
   int64_t ldi, ldj, ldo;     // elements between rows of I, J and out
   int64_t e_i, e_out;        // elements between experts' matrices in I and (gradient) in out
   int32_t E, P, T;           // experts, sorted rows, source rows
-  uint32_t kdiv;
+  uint32_t kdiv, kmul;       // pair / kdiv = mulhi(pair, kmul) >> kshift for 0 <= pair < 2^31, kdiv > 1
+  int32_t kshift;
   int32_t ni, nj, nr;        // extents of i, j (kMats only) and r (not kMats)
   int32_t out_type;          // moeq_dtype
   int32_t out_vec;           // out rows and base allow stores of four elements
@@ -85,14 +86,18 @@ __device__ __forceinline__ void expert_rows(const GemmArgs &a, int e, int *lo, i
   *hi = std::min(std::max(a.off[e + 1], l), a.P);
 }
 
-// Source row of sorted row r; -1 (a row of zeros) when it lies outside [0, T).
+// Source row of pair id p; -1 (a row of zeros) when it lies outside [0, T).
+// The quotient: with kmul = floor(2^(31+L) / k) + 1 and 2^L >= k, the product
+// exceeds p / k by less than 1 / k for p < 2^31.
+__device__ __forceinline__ int pair_row(const GemmArgs &a, int p) {
+  uint32_t s = (uint32_t)p;
+  if (a.kdiv != 1) s = __umulhi(s, a.kmul) >> a.kshift;
+  return p >= 0 && s < (uint32_t)a.T ? (int)s : -1;
+}
+// Source row of sorted row r.
 __device__ __forceinline__ int source_row(const GemmArgs &a, int r) {
-  uint32_t s = (uint32_t)r;
-  if (a.pairs) {
-    s = (uint32_t)a.pairs[r];
-    if (a.kdiv != 1) s /= a.kdiv;
-  }
-  return s < (uint32_t)a.T ? (int)s : -1;
+  if (a.pairs) return pair_row(a, a.pairs[r]);
+  return r < a.T ? r : -1;
 }
 
 // Output tile of a workgroup: expert, first sorted row and rows left in the
@@ -238,6 +243,29 @@ __device__ __forceinline__ const uint8_t *uniform(const uint8_t *p) {   // into 
   return (const uint8_t *)(((uint64_t)hi << 32) | lo);
 }
 
+// Buffer -> LDS transfer of SIZE (4 or 16) bytes per lane, as lds_dma_buf but
+// unknown to the compiler (rs: the four words of the buffer resource): it
+// puts a wait for all transfers before every transposing LDS read
+// otherwise.  The kernel waits by count before the step that reads the
+// data; the instruction has no register output.  m0 holds the LDS address.
+// (s_nop 4: five wait states between a VALU write of a scalar register, as
+// v_readfirstlane makes for rs, and a memory instruction that reads it; the
+// compiler does not look into the asm for that.)
+template <int SIZE>
+__device__ __forceinline__ void lds_dma_raw(i32x4 rs, uint32_t voff, uint32_t soff, const uint8_t *lds) {
+  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t *)lds;
+  if constexpr (SIZE == 16)
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                 :: "v"(voff), "s"(rs), "s"(soff), "s"(at) : "m0", "memory");
+  else
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 4\n\tbuffer_load_dword %0, %1, %2 offen lds"
+                 :: "v"(voff), "s"(rs), "s"(soff), "s"(at) : "m0", "memory");
+}
+__device__ __forceinline__ i32x4 raw_rsrc(const uint8_t *base, uint32_t bytes) {   // both uniform
+  const uint64_t v = (uint64_t)uniform(base);
+  return i32x4{(int)(uint32_t)v, (int)((uint32_t)(v >> 32) & 0xffffu), __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
+}
+
 // ---- Movement of an operand's steps into LDS.  A wave moves NB blocks of 1
 // KiB of every step.
 //
@@ -255,7 +283,7 @@ struct Operand {
   static_assert(R * kStepBytes % (1024 * NW) == 0, "blocks per wave");
   static_assert(!RMAJ || (R % 128 == 0 && ES == 2), "256-byte swizzle groups of 16-bit elements");
   static constexpr int kDmaOps = DMA ? NB : 0;
-  __amdgpu_buffer_rsrc_t rs;
+  i32x4 rs;
   uint32_t voff[NB];       // DMA: lane's offset from the resource's base (kNowhere: no such row)
   const uint8_t *p[NB];    // registers, r contiguous: the row's first byte (null: no such row)
   const uint8_t *base;     // r as row index: the matrix (row 0 of the run) at the tile's first column
@@ -263,13 +291,16 @@ struct Operand {
   int nr, width;           // extent of r; bytes of a row: valid ones (r contiguous), or from the tile's first column
   u32x4 v[NB];             // registers: the step on its way
 
-  __device__ __forceinline__ static int block(int i) { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * NB + i; }
+  int first;               // the wave's first block
+
+  __device__ __forceinline__ explicit Operand(int wave) : first(wave * NB) {}
+  __device__ __forceinline__ int block(int i) const { return first + i; }
   // r contiguous: tile row and byte in the step that the lane moves in block i
-  __device__ __forceinline__ static int row_of(int i) { return block(i) * 16 + (int)((threadIdx.x & 63) >> 2); }
-  __device__ __forceinline__ static int piece_of(int i) { return 16 * ((int)(threadIdx.x & 3) ^ kmaj_swz(row_of(i))); }
+  __device__ __forceinline__ int row_of(int i) const { return block(i) * 16 + (int)((threadIdx.x & 63) >> 2); }
+  __device__ __forceinline__ int piece_of(int i) const { return 16 * ((int)(threadIdx.x & 3) ^ kmaj_swz(row_of(i))); }
   // r as row index: row in the step and byte column
-  __device__ __forceinline__ static int r_of(int i) { return (block(i) * 1024 + (int)(threadIdx.x & 63) * 16) / (2 * R); }
-  __device__ __forceinline__ static int col_of(int i) {
+  __device__ __forceinline__ int r_of(int i) const { return (block(i) * 1024 + (int)(threadIdx.x & 63) * 16) / (2 * R); }
+  __device__ __forceinline__ int col_of(int i) const {
     const int o = block(i) * 1024 + (int)(threadIdx.x & 63) * 16;
     return 16 * ((o % (2 * R)) / 16 ^ (2 * rmaj_swz(o / (2 * R))));
   }
@@ -280,7 +311,7 @@ struct Operand {
   __device__ __forceinline__ void rows(const uint8_t *from, int64_t stride, int64_t last, int n_r, Index index) {
     nr = n_r;
     width = n_r * ES;
-    if constexpr (DMA) rs = make_rsrc(uniform(from), __builtin_amdgcn_readfirstlane((int)(last * stride + width)));
+    if constexpr (DMA) rs = raw_rsrc(from, (uint32_t)(last * stride + width));
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
       const int x = index(row_of(i));
@@ -302,21 +333,21 @@ struct Operand {
   // r as row index: rows given step by step
   __device__ __forceinline__ void gather(const uint8_t *from, int64_t stride, int64_t last, int n_r, int row_bytes) {
     cols(from, stride, n_r, row_bytes);
-    if constexpr (DMA) rs = make_rsrc(base, __builtin_amdgcn_readfirstlane((int)(last * stride + width)));
+    if constexpr (DMA) rs = raw_rsrc(base, (uint32_t)(last * stride + width));
   }
 
   // DMA: block i of step t into the tile at `dst` (steps behind the last:
   // zeros)
   __device__ __forceinline__ void dma_rows(int i, int t, uint8_t *dst) const {
-    lds_dma_buf<16>(rs, piece_of(i) < width - t * kStepBytes ? voff[i] : kNowhere, (uint32_t)t * kStepBytes, dst + block(i) * 1024);
+    lds_dma_raw<16>(rs, piece_of(i) < width - t * kStepBytes ? voff[i] : kNowhere, (uint32_t)t * kStepBytes, dst + block(i) * 1024);
   }
   __device__ __forceinline__ void dma_cols(int i, int t, uint8_t *dst) const {
     const int left = std::min(kStepRows, nr - t * kStepRows);
-    const auto r = make_rsrc(uniform(base + (int64_t)t * kStepRows * ld), left > 0 ? (uint32_t)(left - 1) * (uint32_t)ld + (uint32_t)width : 0u);
-    lds_dma_buf<16>(r, voff[i], 0, dst + block(i) * 1024);
+    const i32x4 r = raw_rsrc(base + (int64_t)t * kStepRows * ld, left > 0 ? (uint32_t)(left - 1) * (uint32_t)ld + (uint32_t)width : 0u);
+    lds_dma_raw<16>(r, voff[i], 0, dst + block(i) * 1024);
   }
   __device__ __forceinline__ void dma_gather(int i, int src, uint8_t *dst) const {
-    lds_dma_buf<16>(rs, src < 0 ? kNowhere : (uint32_t)src * (uint32_t)ld + (uint32_t)col_of(i), 0, dst + block(i) * 1024);
+    lds_dma_raw<16>(rs, src < 0 ? kNowhere : (uint32_t)src * (uint32_t)ld + (uint32_t)col_of(i), 0, dst + block(i) * 1024);
   }
   // registers: load step t, store what is loaded
   __device__ __forceinline__ void load_rows(int t) {
@@ -439,6 +470,11 @@ __device__ __forceinline__ void write_tile(const GemmArgs &a, const Tile &t, int
 // wave has taken step k's fragments into registers, which frees its stage.
 // One barrier per step.
 constexpr int kRing = 4;
+// LDS of a workgroup: the ring, and the pair ids of kMats.
+template <int MODE, int BI, int BJ, int NW, bool DI>
+constexpr size_t tile_lds() {
+  return kRing * (BI + BJ) * kStepBytes + (MODE == kMats && DI ? kRing * NW * (BI * kStepBytes / (1024 * NW)) * 256 : 0);
+}
 
 template <int TY, int MODE, int BI, int BJ, int WI, int WJ, bool DI, bool DJ>
 __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) {
@@ -455,21 +491,43 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) 
 
   using OpI = Operand<ES, BI, NW, RI, DI>;
   using OpJ = Operand<ES, BJ, NW, RJ, DJ>;
-  OpI di;
-  OpJ dj;
-  int src[OpI::NB];        // kMats: source rows of the next step to move
-  auto sources = [&](int k) {
-#pragma unroll
-    for (int i = 0; i < OpI::NB; ++i) {
-      const int r = k * kStepRows + OpI::r_of(i);
-      src[i] = r < nr ? source_row(a, t.row + r) : -1;
+  OpI di(wave);
+  OpJ dj(wave);
+  // kMats with pairs: the pair ids of the rows that this wave moves come by
+  // DMA too, three steps before they are needed (a load into registers would
+  // make the wave wait for every transfer before it).  Step k's are in slot
+  // k % kRing, one dword per lane and block.
+  constexpr bool kIdx = MODE == kMats && DI;
+  i32x4 prs{};
+  auto idx_at = [&](int q, int k) {
+    return gemm_lds + kRing * kStage + (((k & (kRing - 1)) * NW + wave) * OpI::NB + q) * 256;
+  };
+  auto fetch_idx = [&](int q, int k) {
+    const int r = k * kStepRows + di.r_of(q);
+    lds_dma_raw<4>(prs, r < nr ? (uint32_t)r * 4u : kNowhere, 0, idx_at(q, k));
+  };
+  auto source = [&](int q, int k) {      // source row of the lane's row in block q of step k
+    const int r = k * kStepRows + di.r_of(q);
+    if (r >= nr) return -1;
+    if constexpr (kIdx) {
+      if (a.pairs) return pair_row(a, *reinterpret_cast<const int *>(idx_at(q, k) + (threadIdx.x & 63) * 4));
     }
+    return source_row(a, t.row + r);
   };
   const int64_t si = a.ldi * ES, sj = a.ldj * ES;
   if constexpr (MODE == kMats) {
     di.gather(a.I + (int64_t)t.i0 * ES, si, a.T - 1, nr, (a.ni - t.i0) * ES);
     dj.cols(a.J + (int64_t)t.row * sj + (int64_t)j0 * ES, sj, nr, (a.nj - j0) * ES);
-    sources(0);
+    if constexpr (kIdx) {
+      if (a.pairs) {
+        prs = raw_rsrc((const uint8_t *)(a.pairs + t.row), (uint32_t)nr * 4u);
+#pragma unroll
+        for (int k = 0; k < kRing; ++k)
+#pragma unroll
+          for (int q = 0; q < OpI::NB; ++q) fetch_idx(q, k);
+        vm_wait<0>();
+      }
+    }
   } else {
     const uint8_t *wmat = a.I + (int64_t)t.e * a.e_i * ES;   // the expert's matrix
     if constexpr (MODE == kRows) {
@@ -491,7 +549,7 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) 
   auto move = [&](int q, int k, uint8_t *st) {   // q-th DMA of step k
     if constexpr (DI) {
       if (q < OpI::NB) {
-        if constexpr (MODE == kMats) di.dma_gather(q, src[q], st);
+        if constexpr (MODE == kMats) di.dma_gather(q, source(q, k), st);
         else if constexpr (MODE == kRows) di.dma_cols(q, k, st);
         else di.dma_rows(q, k, st);
       }
@@ -503,13 +561,18 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) 
         else dj.dma_rows(j, k, st + kTileI);
       }
     }
-    if constexpr (MODE == kMats && DI) {
-      if (q == kOps - 1) sources(k + 1);
+    if constexpr (kIdx) {
+      if (a.pairs && q < OpI::NB) fetch_idx(q, k + kRing - 1);
     }
   };
   auto load = [&](int k) {
     if constexpr (!DI) {
-      if constexpr (MODE == kMats) di.load_gather(src), sources(k + 1);
+      if constexpr (MODE == kMats) {
+        int src[OpI::NB];
+#pragma unroll
+        for (int q = 0; q < OpI::NB; ++q) src[q] = source(q, k);
+        di.load_gather(src);
+      }
       else if constexpr (MODE == kRows) di.load_cols(k);
       else di.load_rows(k);
     }
@@ -543,7 +606,7 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) 
       for (int q = 0; q < kOps; ++q) move(q, k, gemm_lds + k * kStage);
     }
     if (kRegs) load(kRing - 1);
-    lgkm_vm_wait<(kRing - 1) * kOps>();
+    lgkm_vm_wait<(kRing - 1) * kOps>();    // (kMats' pair ids only make it stricter)
     __builtin_amdgcn_s_barrier();
     u32x4 x[2][TI], y[2][TJ];
 #pragma unroll
@@ -554,7 +617,8 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) 
     // step k, its fragments in set c
     auto step = [&](int k, auto c) {
       constexpr int C = decltype(c)::value, N = 1 - C;
-      lgkm_vm_wait<(kRing - 2) * kOps>();
+      if (kIdx && a.pairs) lgkm_vm_wait<(kRing - 2) * (kOps + OpI::NB)>();
+      else lgkm_vm_wait<(kRing - 2) * kOps>();
       __builtin_amdgcn_s_barrier();
       const uint32_t sn = sb == (kRing - 1) * kStage ? 0u : sb + kStage;
       // registers: step k + 3 goes behind the ring's newest stage

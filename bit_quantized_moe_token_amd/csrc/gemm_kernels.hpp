@@ -24,7 +24,7 @@ moeq_status launch_tiles(const GemmArgs &a, hipStream_t s, const char *name) {
   if (grid > kMaxGrid) return fail(MOEQ_ERR_UNSUPPORTED, "%s: too many tiles", name);
   prof_begin(name, s);
   hipLaunchKernelGGL((gemm_tile_kernel<TY, MODE, BI, BJ, WI, WJ, DMA, DMA>), dim3((unsigned)grid), dim3(64 * WI * WJ),
-                     kRing * (BI + BJ) * kStepBytes, s, a);
+                     (tile_lds<MODE, BI, BJ, WI * WJ, DMA>()), s, a);
   prof_end(name, s);
   return check_launch(name);
 }
