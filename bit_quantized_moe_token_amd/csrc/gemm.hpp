@@ -68,10 +68,12 @@ struct Elt<kI8> {
   }
 };
 
-// A step covers 64 bytes of every row along r (32 elements of 16 bits, 64 of
-// 8): what one MFMA consumes, 16 bytes per lane.
-constexpr int kStepBytes = 64;
-constexpr int kStepRows = 32;    // rows of a step where r is the row index (16-bit elements)
+// A stage covers 128 bytes of every row along r (64 elements of 16 bits, 128
+// of 8), a cache line: 64-byte stages, which would leave room for a deeper
+// ring, measured 10% slower on matrices with r contiguous.  An MFMA consumes
+// half a stage, 16 bytes per lane.
+constexpr int kStageBytes = 128;
+constexpr int kStageRows = 64;   // rows of a stage where r is the row index (16-bit elements)
 
 // First and one-past-last sorted row of expert e, within [0, P] whatever the
 // offsets hold.
@@ -186,35 +188,34 @@ __device__ __forceinline__ u32x4 load_piece(const uint8_t *p, int n) {
   return v;
 }
 
-// ---- LDS layout of an operand tile of R rows (i or j) x 64 bytes of r, 64 R
-// bytes, moved in blocks of 1 KiB (16 bytes per lane).
+// ---- LDS layout of an operand tile of R rows (i or j) x 128 bytes of r,
+// 128 R bytes, moved in blocks of 1 KiB (16 bytes per lane).
 //
-// Operand stored with r contiguous: row after row, 64 bytes each; the
+// Operand stored with r contiguous: row after row, 128 bytes each; the
 // 16-byte piece c of row x sits in slot c ^ kmaj_swz(x).  A 16-byte read of a
 // wave goes through LDS in four passes of 16 lanes: lanes 0-3, 12-15, 20-27,
 // the other 16 of the first 32, and the same of the last 32.  An MFMA
-// operand read has row l % 16, piece l / 16 in lane l; with s(q) = 0, 2, 3, 1
-// for rows 4 q .. 4 q + 3 each pass covers all 64 banks once (s(q) = q gives
-// two-way conflicts, half of the LDS cycles by SQ_LDS_BANK_CONFLICT).
+// operand read has row l % 16, piece l / 16 (+ 4 in the second half) in lane
+// l: with this swizzle each pass covers all 64 banks once
+// (SQ_LDS_BANK_CONFLICT is 0).
 //
-// Operand stored with r as the row index (16-bit only): 32 rows of r, R
+// Operand stored with r as the row index (16-bit only): 64 rows of r, R
 // elements each; 32-byte pieces are permuted within each 256 bytes by
 // XOR with rmaj_swz(r), so that the rows of a transposing read (four of
 // 32 bytes per 16 lanes) fall into different banks.
-__device__ __forceinline__ int kmaj_swz(int x) { return (x >> 1 & 2) ^ (x >> 3 & 1) * 3; }
+__device__ __forceinline__ int kmaj_swz(int x) { return x >> 1 & 7; }
 __device__ __forceinline__ int rmaj_swz(int r) { return (r & 3) | ((r >> 1) & 4); }
 
 // Fragment reads.  Lane l of an MFMA operand holds element l % 16 of the
-// 16-wide tile and 16 bytes of r (piece l / 16 of the step).
+// 16-wide tile and 16 bytes of r (piece l / 16 of the half h of the stage).
 template <int R, bool RMAJ>
 struct FragReader {
   uint32_t base;
-  // f0: first 16-wide tile of the wave (a multiple of 8 with RMAJ, so that
-  // tile f of the wave differs from it by an XOR and a multiple of 256 bytes)
+  // f0: first 16-wide tile of the wave
   __device__ __forceinline__ FragReader(uint32_t tile_base, int f0) {
     const int l = threadIdx.x & 63, g = l >> 4, x = l & 15;
     if constexpr (!RMAJ) {
-      base = tile_base + (16 * f0 + x) * kStepBytes + 16 * (g ^ kmaj_swz(x));
+      base = tile_base + (16 * f0 + x) * kStageBytes + 16 * (g ^ kmaj_swz(x));
     } else {
       // lane x of the 16 supplies 8 bytes of row r = 8 g + x / 4 (+ 4 for the
       // second read): columns 4 (x % 4) .. + 3 of the tile
@@ -222,12 +223,12 @@ struct FragReader {
       base = tile_base + r * (2 * R) + (8 * (x & 3) | 32 * ((f0 & 7) ^ rmaj_swz(r))) + (f0 >> 3) * 256;
     }
   }
-  __device__ __forceinline__ u32x4 read(const uint8_t *lds, int f) const {
+  __device__ __forceinline__ u32x4 read(const uint8_t *lds, int f, int h) const {
     if constexpr (!RMAJ) {
-      return *reinterpret_cast<const u32x4 *>(lds + base + f * 16 * kStepBytes);
+      return *reinterpret_cast<const u32x4 *>(lds + (base ^ (uint32_t)(64 * h)) + f * 16 * kStageBytes);
     } else {
       typedef short s16x4 __attribute__((ext_vector_type(4)));
-      const uint32_t o = (base ^ (uint32_t)((f & 7) * 32)) + (f >> 3) * 256;
+      const uint32_t o = (base ^ (uint32_t)((f & 7) * 32)) + (f >> 3) * 256 + h * (kStageRows / 2) * (2 * R);
       const auto p = (__attribute__((address_space(3))) s16x4 *)(lds + o);
       const auto q = (__attribute__((address_space(3))) s16x4 *)(lds + o + 4 * (2 * R));
       const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(p));
@@ -266,21 +267,21 @@ __device__ __forceinline__ i32x4 raw_rsrc(const uint8_t *base, uint32_t bytes) {
   return i32x4{(int)(uint32_t)v, (int)((uint32_t)(v >> 32) & 0xffffu), __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
 }
 
-// ---- Movement of an operand's steps into LDS.  A wave moves NB blocks of 1
-// KiB of every step.
+// ---- Movement of an operand's stages into LDS.  A wave moves NB blocks of 1
+// KiB of every stage.
 //
 // DMA: buffer loads with an LDS destination; the data never occupies
 // registers.  Bases and rows must be 16-byte aligned; what lies behind the
 // buffer resource's range reads zero, which gives the zeros behind the last
 // row and the last r.
 // Otherwise through registers: any element alignment and row stride, 64-bit
-// addresses; a step is loaded one step before it is stored.
+// addresses; a stage is loaded one stage before it is stored.
 constexpr uint32_t kNowhere = 0x80000000u;   // an offset behind every range used here
 
 template <int ES, int R, int NW, bool RMAJ, bool DMA>
 struct Operand {
-  static constexpr int NB = R * kStepBytes / (1024 * NW);
-  static_assert(R * kStepBytes % (1024 * NW) == 0, "blocks per wave");
+  static constexpr int NB = R * kStageBytes / (1024 * NW);
+  static_assert(R * kStageBytes % (1024 * NW) == 0, "blocks per wave");
   static_assert(!RMAJ || (R % 128 == 0 && ES == 2), "256-byte swizzle groups of 16-bit elements");
   static constexpr int kDmaOps = DMA ? NB : 0;
   i32x4 rs;
@@ -289,16 +290,16 @@ struct Operand {
   const uint8_t *base;     // r as row index: the matrix (row 0 of the run) at the tile's first column
   int64_t ld;              // bytes between rows
   int nr, width;           // extent of r; bytes of a row: valid ones (r contiguous), or from the tile's first column
-  u32x4 v[NB];             // registers: the step on its way
+  u32x4 v[NB];             // registers: the stage on its way
 
   int first;               // the wave's first block
 
   __device__ __forceinline__ explicit Operand(int wave) : first(wave * NB) {}
   __device__ __forceinline__ int block(int i) const { return first + i; }
-  // r contiguous: tile row and byte in the step that the lane moves in block i
-  __device__ __forceinline__ int row_of(int i) const { return block(i) * 16 + (int)((threadIdx.x & 63) >> 2); }
-  __device__ __forceinline__ int piece_of(int i) const { return 16 * ((int)(threadIdx.x & 3) ^ kmaj_swz(row_of(i))); }
-  // r as row index: row in the step and byte column
+  // r contiguous: tile row and byte in the stage that the lane moves in block i
+  __device__ __forceinline__ int row_of(int i) const { return block(i) * 8 + (int)((threadIdx.x & 63) >> 3); }
+  __device__ __forceinline__ int piece_of(int i) const { return 16 * ((int)(threadIdx.x & 7) ^ kmaj_swz(row_of(i))); }
+  // r as row index: row in the stage and byte column
   __device__ __forceinline__ int r_of(int i) const { return (block(i) * 1024 + (int)(threadIdx.x & 63) * 16) / (2 * R); }
   __device__ __forceinline__ int col_of(int i) const {
     const int o = block(i) * 1024 + (int)(threadIdx.x & 63) * 16;
@@ -330,37 +331,37 @@ struct Operand {
       for (int i = 0; i < NB; ++i) voff[i] = (uint32_t)r_of(i) * (uint32_t)ld + (uint32_t)col_of(i);
     }
   }
-  // r as row index: rows given step by step
+  // r as row index: rows given stage by stage
   __device__ __forceinline__ void gather(const uint8_t *from, int64_t stride, int64_t last, int n_r, int row_bytes) {
     cols(from, stride, n_r, row_bytes);
     if constexpr (DMA) rs = raw_rsrc(base, (uint32_t)(last * stride + width));
   }
 
-  // DMA: block i of step t into the tile at `dst` (steps behind the last:
+  // DMA: block i of stage t into the tile at `dst` (stages behind the last:
   // zeros)
   __device__ __forceinline__ void dma_rows(int i, int t, uint8_t *dst) const {
-    lds_dma_raw<16>(rs, piece_of(i) < width - t * kStepBytes ? voff[i] : kNowhere, (uint32_t)t * kStepBytes, dst + block(i) * 1024);
+    lds_dma_raw<16>(rs, piece_of(i) < width - t * kStageBytes ? voff[i] : kNowhere, (uint32_t)t * kStageBytes, dst + block(i) * 1024);
   }
   __device__ __forceinline__ void dma_cols(int i, int t, uint8_t *dst) const {
-    const int left = std::min(kStepRows, nr - t * kStepRows);
-    const i32x4 r = raw_rsrc(base + (int64_t)t * kStepRows * ld, left > 0 ? (uint32_t)(left - 1) * (uint32_t)ld + (uint32_t)width : 0u);
+    const int left = std::min(kStageRows, nr - t * kStageRows);
+    const i32x4 r = raw_rsrc(base + (int64_t)t * kStageRows * ld, left > 0 ? (uint32_t)(left - 1) * (uint32_t)ld + (uint32_t)width : 0u);
     lds_dma_raw<16>(r, voff[i], 0, dst + block(i) * 1024);
   }
   __device__ __forceinline__ void dma_gather(int i, int src, uint8_t *dst) const {
     lds_dma_raw<16>(rs, src < 0 ? kNowhere : (uint32_t)src * (uint32_t)ld + (uint32_t)col_of(i), 0, dst + block(i) * 1024);
   }
-  // registers: load step t, store what is loaded
+  // registers: load stage t, store what is loaded
   __device__ __forceinline__ void load_rows(int t) {
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
-      const int o = t * kStepBytes + piece_of(i);
+      const int o = t * kStageBytes + piece_of(i);
       v[i] = load_piece<ES>(p[i] + o, p[i] ? width - o : 0);
     }
   }
   __device__ __forceinline__ void load_cols(int t) {
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
-      const int r = t * kStepRows + r_of(i);
+      const int r = t * kStageRows + r_of(i);
       v[i] = load_piece<ES>(base + r * ld + col_of(i), r < nr ? width - col_of(i) : 0);
     }
   }
@@ -463,24 +464,25 @@ __device__ __forceinline__ void write_tile(const GemmArgs &a, const Tile &t, int
 }
 
 // ---- tiled kernel: a workgroup of WI x WJ waves computes BI x BJ outputs,
-// walking r in steps through a ring of kRing LDS stages.
+// walking r through two LDS stages.
 //
-// While a wave multiplies step k out of registers it reads the fragments of
-// step k + 1 into a second set, so that the matrix pipe does not wait for LDS.  Steps up to k + 4 are on their way: before step k every
-// wave has taken step k's fragments into registers, which frees its stage.
-// One barrier per step.
-constexpr int kRing = 4;
-// LDS of a workgroup: the ring, and the pair ids of kMats.
+// A wave multiplies half a stage out of registers while it reads the
+// fragments of the next half into a second set, so that the matrix pipe does
+// not wait for LDS.  Before the second half of stage p every wave has taken
+// it into registers, which frees the stage for p + 2; stage p + 1 has to be
+// there by then, for its first fragments: one wait and one barrier per stage.
+//
+// LDS of a workgroup: the stages, and the pair ids of kMats.
 template <int MODE, int BI, int BJ, int NW, bool DI>
 constexpr size_t tile_lds() {
-  return kRing * (BI + BJ) * kStepBytes + (MODE == kMats && DI ? kRing * NW * (BI * kStepBytes / (1024 * NW)) * 256 : 0);
+  return 2 * (BI + BJ) * kStageBytes + (MODE == kMats && DI ? 2 * (BI * kStageBytes / 1024) * 256 : 0);
 }
 
 template <int TY, int MODE, int BI, int BJ, int WI, int WJ, bool DI, bool DJ>
 __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) {
   constexpr int ES = Elt<TY>::size, NW = WI * WJ, TI = BI / WI / 16, TJ = BJ / WJ / 16;
   constexpr bool RI = MODE != kFwd, RJ = MODE == kMats;
-  constexpr uint32_t kTileI = BI * kStepBytes, kStage = kTileI + BJ * kStepBytes;
+  constexpr uint32_t kTileI = BI * kStageBytes, kStage = kTileI + BJ * kStageBytes;
   using Acc = typename Elt<TY>::acc;
   extern __shared__ __attribute__((aligned(1024))) uint8_t gemm_lds[];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -494,20 +496,18 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) 
   OpI di(wave);
   OpJ dj(wave);
   // kMats with pairs: the pair ids of the rows that this wave moves come by
-  // DMA too, three steps before they are needed (a load into registers would
-  // make the wave wait for every transfer before it).  Step k's are in slot
-  // k % kRing, one dword per lane and block.
+  // DMA too, one stage before they are needed (a load into registers would
+  // make the wave wait for every transfer before it).  Stage k's are in slot
+  // k % 2, one dword per lane and block.
   constexpr bool kIdx = MODE == kMats && DI;
   i32x4 prs{};
-  auto idx_at = [&](int q, int k) {
-    return gemm_lds + kRing * kStage + (((k & (kRing - 1)) * NW + wave) * OpI::NB + q) * 256;
-  };
+  auto idx_at = [&](int q, int k) { return gemm_lds + 2 * kStage + (((k & 1) * NW + wave) * OpI::NB + q) * 256; };
   auto fetch_idx = [&](int q, int k) {
-    const int r = k * kStepRows + di.r_of(q);
+    const int r = k * kStageRows + di.r_of(q);
     lds_dma_raw<4>(prs, r < nr ? (uint32_t)r * 4u : kNowhere, 0, idx_at(q, k));
   };
-  auto source = [&](int q, int k) {      // source row of the lane's row in block q of step k
-    const int r = k * kStepRows + di.r_of(q);
+  auto source = [&](int q, int k) {      // source row of the lane's row in block q of stage k
+    const int r = k * kStageRows + di.r_of(q);
     if (r >= nr) return -1;
     if constexpr (kIdx) {
       if (a.pairs) return pair_row(a, *reinterpret_cast<const int *>(idx_at(q, k) + (threadIdx.x & 63) * 4));
@@ -522,9 +522,7 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) 
       if (a.pairs) {
         prs = raw_rsrc((const uint8_t *)(a.pairs + t.row), (uint32_t)nr * 4u);
 #pragma unroll
-        for (int k = 0; k < kRing; ++k)
-#pragma unroll
-          for (int q = 0; q < OpI::NB; ++q) fetch_idx(q, k);
+        for (int q = 0; q < OpI::NB; ++q) fetch_idx(q, 0), fetch_idx(q, 1);
         vm_wait<0>();
       }
     }
@@ -543,10 +541,8 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) 
       dj.rows(a.J + t.row * sj, sj, n - 1, nr, [&](int x) { return x < n ? x : -1; });
     }
   }
-  // Registers: the step loaded last goes into its stage, step k is loaded.
-  // DMA: step k goes into stage `st` on its own.
   constexpr int kOps = OpI::kDmaOps + OpJ::kDmaOps;
-  auto move = [&](int q, int k, uint8_t *st) {   // q-th DMA of step k
+  auto move = [&](int q, int k, uint8_t *st) {   // q-th DMA of stage k
     if constexpr (DI) {
       if (q < OpI::NB) {
         if constexpr (MODE == kMats) di.dma_gather(q, source(q, k), st);
@@ -560,9 +556,6 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) 
         if constexpr (RJ) dj.dma_cols(j, k, st + kTileI);
         else dj.dma_rows(j, k, st + kTileI);
       }
-    }
-    if constexpr (kIdx) {
-      if (a.pairs && q < OpI::NB) fetch_idx(q, k + kRing - 1);
     }
   };
   auto load = [&](int k) {
@@ -594,56 +587,54 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) 
     for (int j = 0; j < TJ; ++j) acc[i][j] = Acc{0, 0, 0, 0};
   const FragReader<BI, RI> fi(0, wi * TI);
   const FragReader<BJ, RJ> fj(kTileI, wj * TJ);
-  const int steps = (int)(((int64_t)nr * ES + kStepBytes - 1) / kStepBytes);
-  if (steps > 0) {
+  const int stages = (int)(((int64_t)nr * ES + kStageBytes - 1) / kStageBytes);
+  if (stages > 0) {
 #pragma unroll
-    for (int k = 0; k < kRing; ++k) {
-      if (kRegs && k < kRing - 1) {
+    for (int k = 0; k < 2; ++k) {
+      if (kRegs) {
         load(k);
         store(gemm_lds + k * kStage);
       }
 #pragma unroll
       for (int q = 0; q < kOps; ++q) move(q, k, gemm_lds + k * kStage);
     }
-    if (kRegs) load(kRing - 1);
-    lgkm_vm_wait<(kRing - 1) * kOps>();    // (kMats' pair ids only make it stricter)
+    if (kRegs) load(2);
+    lgkm_vm_wait<kRegs ? 0 : kOps>();
+    if constexpr (kIdx) {    // (both stages' ids have been read)
+      if (a.pairs) {
+#pragma unroll
+        for (int q = 0; q < OpI::NB; ++q) fetch_idx(q, 2);
+      }
+    }
     __builtin_amdgcn_s_barrier();
     u32x4 x[2][TI], y[2][TJ];
 #pragma unroll
-    for (int i = 0; i < TI; ++i) x[0][i] = fi.read(gemm_lds, i);
+    for (int i = 0; i < TI; ++i) x[0][i] = fi.read(gemm_lds, i, 0);
 #pragma unroll
-    for (int j = 0; j < TJ; ++j) y[0][j] = fj.read(gemm_lds, j);
-    uint32_t sb = 0;         // stage of step k
-    // step k, its fragments in set c
-    auto step = [&](int k, auto c) {
+    for (int j = 0; j < TJ; ++j) y[0][j] = fj.read(gemm_lds, j, 0);
+    // The MFMAs of a half stage (set C), with the reads of the next one
+    // (half 1 - C of the stage at st) between them, in kSeg parts.  In the
+    // second half a part starts with its share of the DMA operations of
+    // stage k (all at once after the barrier they hold the waves up: a CU
+    // takes one in about 16 cycles).  The last part has no reads, so that its
+    // MFMAs cover their latency.
+    auto half = [&](auto c, const uint8_t *st, int k, uint8_t *to) {
       constexpr int C = decltype(c)::value, N = 1 - C;
-      if (kIdx && a.pairs) lgkm_vm_wait<(kRing - 2) * (kOps + OpI::NB)>();
-      else lgkm_vm_wait<(kRing - 2) * kOps>();
-      __builtin_amdgcn_s_barrier();
-      const uint32_t sn = sb == (kRing - 1) * kStage ? 0u : sb + kStage;
-      // registers: step k + 3 goes behind the ring's newest stage
-      if constexpr (kRegs) store(gemm_lds + (sb == 0 ? (kRing - 1) * kStage : sb - kStage));
-      if constexpr (kRegs) load(k + kRing);
-      __builtin_amdgcn_sched_barrier(0);
-      const uint8_t *st = gemm_lds + sn;
-      // The MFMAs in kSeg parts.  A part starts with its share of the DMA
-      // operations (all at once after the barrier, they hold the waves up: a
-      // CU takes one in about 16 cycles) and has its share of the next step's
-      // fragment reads between its MFMAs; the last part has none, so that
-      // its MFMAs cover their latency.
       constexpr int kSeg = TI < 4 ? TI : 4, kRd = kSeg > 1 ? kSeg - 1 : 1, IS = TI / kSeg;
       constexpr int kReads = TI + TJ, kInsI = RI ? 2 : 1, kInsJ = RJ ? 2 : 1;
 #pragma unroll
       for (int g = 0; g < kSeg; ++g) {
+        if constexpr (C == 1) {
 #pragma unroll
-        for (int q = 0; q < kOps; ++q)
-          if (q * kSeg / std::max(kOps, 1) == g) move(q, k + kRing, gemm_lds + sb);
+          for (int q = 0; q < kOps; ++q)
+            if (q * kSeg / std::max(kOps, 1) == g) move(q, k, to);
+        }
         int ins = 0;
 #pragma unroll
         for (int f = 0; f < kReads; ++f)
           if (f * kRd / kReads == g) {
-            if (f < TJ) y[N][f] = fj.read(st, f), ins += kInsJ;
-            else x[N][f - TJ] = fi.read(st, f - TJ), ins += kInsI;
+            if (f < TJ) y[N][f] = fj.read(st, f, N), ins += kInsJ;
+            else x[N][f - TJ] = fi.read(st, f - TJ, N), ins += kInsI;
           }
 #pragma unroll
         for (int i = g * IS; i < (g + 1) * IS; ++i)
@@ -659,16 +650,28 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) 
         __builtin_amdgcn_sched_group_barrier(0x008, TI * TJ, 0);
         __builtin_amdgcn_sched_barrier(0);
       }
-      sb = sn;
     };
-    int k = 0;
+    uint32_t sb = 0;         // where stage k is
 #pragma unroll 1
-    for (; k + 1 < steps; k += 2) {
-      step(k, std::integral_constant<int, 0>{});
-      step(k + 1, std::integral_constant<int, 1>{});
+    for (int k = 0; k < stages; ++k) {
+      half(std::integral_constant<int, 0>{}, gemm_lds + sb, 0, nullptr);
+      lgkm_vm_wait<0>();
+      __builtin_amdgcn_s_barrier();
+      if constexpr (kRegs) {
+        store(gemm_lds + sb);
+        load(k + 3);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      half(std::integral_constant<int, 1>{}, gemm_lds + (sb ^ kStage), k + 2, gemm_lds + sb);
+      if constexpr (kIdx) {
+        if (a.pairs) {
+#pragma unroll
+          for (int q = 0; q < OpI::NB; ++q) fetch_idx(q, k + 3);
+        }
+      }
+      sb ^= kStage;
     }
-    if (k < steps) step(k, std::integral_constant<int, 0>{});
-    vm_wait<0>();            // (the zeros of steps behind the last are still on their way)
+    vm_wait<0>();            // (the zeros of stages behind the last are still on their way)
   }
   write_tile<TY, MODE, TI, TJ>(a, t, j0, wi * TI * 16, wj * TJ * 16, acc);
 }
