@@ -55,11 +55,6 @@ moeq_status check_stride(const char *who, const char *name, int64_t stride, int6
 bool ok16(int dtype) { return dtype == MOEQ_F16 || dtype == MOEQ_BF16; }
 bool okout(int dtype) { return ok16(dtype) || dtype == MOEQ_F32; }
 
-bool vec_out(const void *p, int64_t ld, int64_t stride, int dtype) {
-  const int es = elt_size(dtype);
-  return ((uintptr_t)p % (4 * es)) == 0 && ld % 4 == 0 && stride % 4 == 0;
-}
-
 #define MOEQ_TRY(e) do { const moeq_status st_ = (e); if (st_ != MOEQ_OK) return st_; } while (0)
 
 GemmArgs base_args(const moeq_groups *g) {
@@ -111,7 +106,6 @@ moeq_status run_i8(const moeq_groups *g, const int8_t *xq, int64_t ldx, const fl
   a.ni = N;
   a.nr = K;
   a.out_type = y_dtype;
-  a.out_vec = vec_out(y, ldy, 0, y_dtype);
   return launch_gemm_i8(a, stream);
 }
 
@@ -147,7 +141,6 @@ MOEQ_API moeq_status moeq_grouped_gemm(const moeq_groups *g, const void *x, int6
   a.ni = N;
   a.nr = K;
   a.out_type = y_dtype;
-  a.out_vec = vec_out(y, ldy, 0, y_dtype);
   const GemmMode mode = trans ? kRows : kFwd;
   return dtype == MOEQ_F16 ? launch_gemm_f16(a, mode, stream) : launch_gemm_bf16(a, mode, stream);
 }
@@ -178,7 +171,6 @@ MOEQ_API moeq_status moeq_grouped_wgrad(const moeq_groups *g, const void *dy, in
   a.ni = K;
   a.nj = N;
   a.out_type = dw_dtype;
-  a.out_vec = vec_out(dw, lddw, g->E > 1 ? stride_dw : 0, dw_dtype);
   return dtype == MOEQ_F16 ? launch_gemm_f16(a, kMats, stream) : launch_gemm_bf16(a, kMats, stream);
 }
 

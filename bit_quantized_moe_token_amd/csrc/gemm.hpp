@@ -38,7 +38,6 @@ struct GemmArgs {
   int32_t kshift;
   int32_t ni, nj, nr;        // extents of i, j (kMats only) and r (not kMats)
   int32_t out_type;          // moeq_dtype
-  int32_t out_vec;           // out rows and base allow stores of four elements
 };
 
 template <int TY>
@@ -115,55 +114,52 @@ struct Tile {
 // numbering, for its own L2.  The count of row tiles is known only on the
 // device: workgroups beyond it return false.
 constexpr int kBand = 8;
+constexpr int kMaxExperts = 256;
 template <int BJ>
 __device__ __forceinline__ bool find_tile(const GemmArgs &a, int BI, Tile *t) {
+  constexpr int NB = kMaxExperts / kWave;     // experts per lane
   const int lane = threadIdx.x & 63;
   const int n_it = (a.ni + BI - 1) / BI;
-  int total = 0;   // row tiles of all experts
-  for (int b = 0; b < a.E; b += kWave) {
-    int nc = 0, lo, hi;
-    if (b + lane < a.E) {
-      expert_rows(a, b + lane, &lo, &hi);
-      nc = (hi - lo + BJ - 1) / BJ;
-    }
+  int lo[NB], hi[NB], nc[NB], end[NB];        // rows, row tiles, row tiles up to and with the expert
+  int total = 0;
 #pragma unroll
-    for (int o = 32; o; o >>= 1) nc += __shfl_xor(nc, o, kWave);
-    total += nc;
+  for (int b = 0; b < NB; ++b) {
+    if (b * kWave >= a.E) break;
+    lo[b] = hi[b] = 0;
+    if (b * kWave + lane < a.E) expert_rows(a, b * kWave + lane, &lo[b], &hi[b]);
+    nc[b] = end[b] = (hi[b] - lo[b] + BJ - 1) / BJ;
+  }
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    if (b * kWave >= a.E) break;
+    const int last = std::min(kWave, a.E - b * kWave);
+    for (int o = 1; o < last; o <<= 1) {
+      const int v = __shfl_up(end[b], o, kWave);
+      if (lane >= o) end[b] += v;
+    }
+    end[b] += total;
+    total = __builtin_amdgcn_readlane(end[b], last - 1);
   }
   const int all = total * n_it, per = (all + 7) >> 3;
   const int idx = (int)blockIdx.x >> 3, L = ((int)blockIdx.x & 7) * per + idx;
   if (idx >= per || L >= all) return false;
-  int carry = 0;
-  for (int b = 0; b < a.E; b += kWave) {
-    int nc = 0, lo = 0, hi = 0;
-    if (b + lane < a.E) {
-      expert_rows(a, b + lane, &lo, &hi);
-      nc = (hi - lo + BJ - 1) / BJ;
-    }
-    int incl = nc;
 #pragma unroll
-    for (int o = 1; o < kWave; o <<= 1) {
-      const int v = __shfl_up(incl, o, kWave);
-      if (lane >= o) incl += v;
-    }
-    const int excl = carry + incl - nc;
-    const uint64_t hit = __ballot(L >= excl * n_it && L < (excl + nc) * n_it);
+  for (int b = 0; b < NB; ++b) {
+    if (b * kWave >= a.E) break;
+    const uint64_t hit = __ballot(L >= (end[b] - nc[b]) * n_it && L < end[b] * n_it);
     if (hit) {
       const int src = __builtin_ctzll(hit);
-      const int ex = __builtin_amdgcn_readfirstlane(__shfl(excl, src, kWave));
-      const int n = __builtin_amdgcn_readfirstlane(__shfl(nc, src, kWave));
-      const int l = __builtin_amdgcn_readfirstlane(__shfl(lo, src, kWave));
-      const int h = __builtin_amdgcn_readfirstlane(__shfl(hi, src, kWave));
+      const int n = __builtin_amdgcn_readlane(nc[b], src), ex = __builtin_amdgcn_readlane(end[b], src) - n;
+      const int l = __builtin_amdgcn_readlane(lo[b], src), h = __builtin_amdgcn_readlane(hi[b], src);
       const int local = L - ex * n_it, band = local / (kBand * n_it);
       const int in = local - band * kBand * n_it, width = std::min(kBand, n - band * kBand);
       const int jt = band * kBand + in % width;
-      t->e = b + src;
+      t->e = b * kWave + src;
       t->row = l + jt * BJ;
       t->rows = h - t->row;
       t->i0 = in / width * BI;
       return true;
     }
-    carry += __builtin_amdgcn_readfirstlane(__shfl(incl, 63, kWave));
   }
   return false;
 }
@@ -283,7 +279,6 @@ struct Operand {
   static constexpr int NB = R * kStageBytes / (1024 * NW);
   static_assert(R * kStageBytes % (1024 * NW) == 0, "blocks per wave");
   static_assert(!RMAJ || (R % 128 == 0 && ES == 2), "256-byte swizzle groups of 16-bit elements");
-  static constexpr int kDmaOps = DMA ? NB : 0;
   i32x4 rs;
   uint32_t voff[NB];       // DMA: lane's offset from the resource's base (kNowhere: no such row)
   const uint8_t *p[NB];    // registers, r contiguous: the row's first byte (null: no such row)
@@ -379,14 +374,17 @@ struct Operand {
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 __device__ __forceinline__ uint16_t f16_bits(float v) { return __builtin_bit_cast(uint16_t, (f16)v); }
 
+typedef f32x4 f32x4_a4 __attribute__((aligned(4)));   // at the alignment of an element
+typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+
 // Four consecutive elements at index o of which n exist, each rounded once.
 __device__ __forceinline__ void store4(const GemmArgs &a, int64_t o, f32x4 v, int n) {
   if (a.out_type == MOEQ_F32) {
     float *p = (float *)a.out + o;
-    if (a.out_vec && n >= 4) *reinterpret_cast<f32x4 *>(p) = v;
+    if (n >= 4) *(__attribute__((address_space(1))) f32x4_a4 *)p = v;
     else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) if (i < n) p[i] = v[i];
+      for (int i = 0; i < 3; ++i) if (i < n) p[i] = v[i];
     }
     return;
   }
@@ -394,11 +392,12 @@ __device__ __forceinline__ void store4(const GemmArgs &a, int64_t o, f32x4 v, in
 #pragma unroll
   for (int i = 0; i < 4; ++i) h[i] = a.out_type == MOEQ_BF16 ? bf16_bits(v[i]) : f16_bits(v[i]);
   uint16_t *p = (uint16_t *)a.out + o;
-  if (a.out_vec && n >= 4) {
-    *reinterpret_cast<u32x2 *>(p) = u32x2{(uint32_t)h[0] | ((uint32_t)h[1] << 16), (uint32_t)h[2] | ((uint32_t)h[3] << 16)};
+  if (n >= 4) {
+    *(__attribute__((address_space(1))) u32x2_a2 *)p =
+        u32x2{(uint32_t)h[0] | ((uint32_t)h[1] << 16), (uint32_t)h[2] | ((uint32_t)h[3] << 16)};
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) if (i < n) p[i] = h[i];
+    for (int i = 0; i < 3; ++i) if (i < n) p[i] = h[i];
   }
 }
 
@@ -464,21 +463,21 @@ __device__ __forceinline__ void write_tile(const GemmArgs &a, const Tile &t, int
 }
 
 // ---- tiled kernel: a workgroup of WI x WJ waves computes BI x BJ outputs,
-// walking r through two LDS stages.
+// walking r through a ring of RING LDS stages.
 //
 // A wave multiplies half a stage out of registers while it reads the
 // fragments of the next half into a second set, so that the matrix pipe does
 // not wait for LDS.  Before the second half of stage p every wave has taken
-// it into registers, which frees the stage for p + 2; stage p + 1 has to be
+// it into registers, which frees the stage for p + RING; stage p + 1 has to be
 // there by then, for its first fragments: one wait and one barrier per stage.
 //
 // LDS of a workgroup: the stages, and the pair ids of kMats.
-template <int MODE, int BI, int BJ, int NW, bool DI>
+template <int MODE, int BI, int BJ, bool DMA, int RING>
 constexpr size_t tile_lds() {
-  return 2 * (BI + BJ) * kStageBytes + (MODE == kMats && DI ? 2 * (BI * kStageBytes / 1024) * 256 : 0);
+  return RING * (BI + BJ) * kStageBytes + (MODE == kMats && DMA ? 2 * (BI * kStageBytes / 1024) * 256 : 0);
 }
 
-template <int TY, int MODE, int BI, int BJ, int WI, int WJ, bool DI, bool DJ>
+template <int TY, int MODE, int BI, int BJ, int WI, int WJ, int RING, bool DMA>
 __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) {
   constexpr int ES = Elt<TY>::size, NW = WI * WJ, TI = BI / WI / 16, TJ = BJ / WJ / 16;
   constexpr bool RI = MODE != kFwd, RJ = MODE == kMats;
@@ -491,17 +490,17 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) 
   int nr, j0;
   if (!pick_tile<MODE, BI, BJ>(a, &t, &nr, &j0)) return;
 
-  using OpI = Operand<ES, BI, NW, RI, DI>;
-  using OpJ = Operand<ES, BJ, NW, RJ, DJ>;
+  using OpI = Operand<ES, BI, NW, RI, DMA>;
+  using OpJ = Operand<ES, BJ, NW, RJ, DMA>;
   OpI di(wave);
   OpJ dj(wave);
   // kMats with pairs: the pair ids of the rows that this wave moves come by
   // DMA too, one stage before they are needed (a load into registers would
   // make the wave wait for every transfer before it).  Stage k's are in slot
   // k % 2, one dword per lane and block.
-  constexpr bool kIdx = MODE == kMats && DI;
+  constexpr bool kIdx = MODE == kMats && DMA;
   i32x4 prs{};
-  auto idx_at = [&](int q, int k) { return gemm_lds + 2 * kStage + (((k & 1) * NW + wave) * OpI::NB + q) * 256; };
+  auto idx_at = [&](int q, int k) { return gemm_lds + RING * kStage + (((k & 1) * NW + wave) * OpI::NB + q) * 256; };
   auto fetch_idx = [&](int q, int k) {
     const int r = k * kStageRows + di.r_of(q);
     lds_dma_raw<4>(prs, r < nr ? (uint32_t)r * 4u : kNowhere, 0, idx_at(q, k));
@@ -541,44 +540,42 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) 
       dj.rows(a.J + t.row * sj, sj, n - 1, nr, [&](int x) { return x < n ? x : -1; });
     }
   }
-  constexpr int kOps = OpI::kDmaOps + OpJ::kDmaOps;
+  constexpr int kOps = DMA ? OpI::NB + OpJ::NB : 0;
   auto move = [&](int q, int k, uint8_t *st) {   // q-th DMA of stage k
-    if constexpr (DI) {
+    if constexpr (DMA) {
       if (q < OpI::NB) {
         if constexpr (MODE == kMats) di.dma_gather(q, source(q, k), st);
         else if constexpr (MODE == kRows) di.dma_cols(q, k, st);
         else di.dma_rows(q, k, st);
-      }
-    }
-    if constexpr (DJ) {
-      const int j = q - OpI::kDmaOps;
-      if (j >= 0 && j < OpJ::NB) {
-        if constexpr (RJ) dj.dma_cols(j, k, st + kTileI);
-        else dj.dma_rows(j, k, st + kTileI);
+      } else {
+        if constexpr (RJ) dj.dma_cols(q - OpI::NB, k, st + kTileI);
+        else dj.dma_rows(q - OpI::NB, k, st + kTileI);
       }
     }
   };
-  auto load = [&](int k) {
-    if constexpr (!DI) {
+  auto load = [&](int k) {                       // stage k into registers
+    if constexpr (!DMA) {
       if constexpr (MODE == kMats) {
         int src[OpI::NB];
 #pragma unroll
         for (int q = 0; q < OpI::NB; ++q) src[q] = source(q, k);
         di.load_gather(src);
+      } else if constexpr (MODE == kRows) {
+        di.load_cols(k);
+      } else {
+        di.load_rows(k);
       }
-      else if constexpr (MODE == kRows) di.load_cols(k);
-      else di.load_rows(k);
-    }
-    if constexpr (!DJ) {
       if constexpr (RJ) dj.load_cols(k);
       else dj.load_rows(k);
     }
   };
-  auto store = [&](uint8_t *st) {
-    if constexpr (!DI) di.store(st);
-    if constexpr (!DJ) dj.store(st + kTileI);
+  auto store = [&](uint8_t *st) {                // and from there into its place
+    if constexpr (!DMA) {
+      di.store(st);
+      dj.store(st + kTileI);
+    }
   };
-  constexpr bool kRegs = !DI || !DJ;
+  static_assert(RING == 2 || (DMA && MODE != kMats), "longer rings count DMA operations only");
 
   Acc acc[TI][TJ];
 #pragma unroll
@@ -590,16 +587,16 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) 
   const int stages = (int)(((int64_t)nr * ES + kStageBytes - 1) / kStageBytes);
   if (stages > 0) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (kRegs) {
+    for (int k = 0; k < RING; ++k) {
+      if (!DMA) {
         load(k);
         store(gemm_lds + k * kStage);
       }
 #pragma unroll
       for (int q = 0; q < kOps; ++q) move(q, k, gemm_lds + k * kStage);
     }
-    if (kRegs) load(2);
-    lgkm_vm_wait<kRegs ? 0 : kOps>();
+    if (!DMA) load(2);
+    lgkm_vm_wait<(RING - 1) * kOps>();
     if constexpr (kIdx) {    // (both stages' ids have been read)
       if (a.pairs) {
 #pragma unroll
@@ -652,24 +649,46 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) 
       }
     };
     uint32_t sb = 0;         // where stage k is
-#pragma unroll 1
-    for (int k = 0; k < stages; ++k) {
-      half(std::integral_constant<int, 0>{}, gemm_lds + sb, 0, nullptr);
-      lgkm_vm_wait<0>();
+    // the wait and the barrier before the second half of stage k; where
+    // stage k + 1 is
+    auto turn = [&](int k) {
+      lgkm_vm_wait<(RING - 2) * kOps>();
       __builtin_amdgcn_s_barrier();
-      if constexpr (kRegs) {
+      if constexpr (!DMA) {
         store(gemm_lds + sb);
         load(k + 3);
       }
       __builtin_amdgcn_sched_barrier(0);
-      half(std::integral_constant<int, 1>{}, gemm_lds + (sb ^ kStage), k + 2, gemm_lds + sb);
+      return sb == (RING - 1) * kStage ? 0u : sb + kStage;
+    };
+    auto ids = [&](int k) {
       if constexpr (kIdx) {
         if (a.pairs) {
 #pragma unroll
-          for (int q = 0; q < OpI::NB; ++q) fetch_idx(q, k + 3);
+          for (int q = 0; q < OpI::NB; ++q) fetch_idx(q, k);
         }
       }
-      sb ^= kStage;
+    };
+    // a wave whose outputs do not exist (behind the expert's last row, or the
+    // last i) only moves operands
+    if (wj * TJ * 16 < t.rows && t.i0 + wi * TI * 16 < a.ni) {
+#pragma unroll 1
+      for (int k = 0; k < stages; ++k) {
+        half(std::integral_constant<int, 0>{}, gemm_lds + sb, 0, nullptr);
+        const uint32_t sn = turn(k);
+        half(std::integral_constant<int, 1>{}, gemm_lds + sn, k + RING, gemm_lds + sb);
+        ids(k + 3);
+        sb = sn;
+      }
+    } else {
+#pragma unroll 1
+      for (int k = 0; k < stages; ++k) {
+        const uint32_t sn = turn(k);
+#pragma unroll
+        for (int q = 0; q < kOps; ++q) move(q, k + RING, gemm_lds + sb);
+        ids(k + 3);
+        sb = sn;
+      }
     }
     vm_wait<0>();            // (the zeros of stages behind the last are still on their way)
   }

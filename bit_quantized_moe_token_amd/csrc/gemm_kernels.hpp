@@ -10,21 +10,21 @@ moeq_status launch_gemm_i8(const GemmArgs &a, hipStream_t s);
 
 // Workgroups of a launch with tiles of BI x BJ: row tiles are bounded by one
 // partial tile per expert that has rows.
-template <int MODE, int BI, int BJ>
-int64_t tile_grid(const GemmArgs &a) {
+template <int MODE>
+int64_t tile_grid(const GemmArgs &a, int BI, int BJ) {
   const int64_t n_it = (a.ni + BI - 1) / BI;
   const int64_t n_jt = MODE == kMats ? (int64_t)a.E * ((a.nj + BJ - 1) / BJ) : a.P / BJ + std::min(a.E, a.P);
   return (n_it * n_jt + 7) / 8 * 8;
 }
 constexpr int64_t kMaxGrid = 0x7fffff00 / 512;   // (threads of a launch fit 32 bits)
 
-template <int TY, int MODE, int BI, int BJ, int WI, int WJ, bool DMA>
+template <int TY, int MODE, int BI, int BJ, int WI, int WJ, int RING, bool DMA>
 moeq_status launch_tiles(const GemmArgs &a, hipStream_t s, const char *name) {
-  const int64_t grid = tile_grid<MODE, BI, BJ>(a);
+  const int64_t grid = tile_grid<MODE>(a, BI, BJ);
   if (grid > kMaxGrid) return fail(MOEQ_ERR_UNSUPPORTED, "%s: too many tiles", name);
   prof_begin(name, s);
-  hipLaunchKernelGGL((gemm_tile_kernel<TY, MODE, BI, BJ, WI, WJ, DMA, DMA>), dim3((unsigned)grid), dim3(64 * WI * WJ),
-                     (tile_lds<MODE, BI, BJ, WI * WJ, DMA>()), s, a);
+  hipLaunchKernelGGL((gemm_tile_kernel<TY, MODE, BI, BJ, WI, WJ, RING, DMA>), dim3((unsigned)grid), dim3(64 * WI * WJ),
+                     (tile_lds<MODE, BI, BJ, DMA, RING>()), s, a);
   prof_end(name, s);
   return check_launch(name);
 }
@@ -45,11 +45,55 @@ bool dma_ok(const GemmArgs &a) {
   return !a.pairs || (int64_t)a.T * a.ldj * ES <= lim;
 }
 
+// The tile: as large as the mean rows of an expert fill and as leaves about
+// one workgroup per CU.  Larger tiles read the operands less often (8 experts
+// of 1000 rows, K 4096, N 14336, bf16: 256 x 256 716 us, 128 x 128 989, 128
+// x 64 1323, 64 x 64 1629), smaller ones spend less on rows that do not
+// exist and spread few rows over more CUs (one matrix of 4096 x 4096: 200
+// rows 64 x 32 22 us, 128 x 128 30; 64 rows of each expert above: 128 x 64
+// 176, 128 x 128 183, 256 x 256 220).  Small tiles take a longer ring where
+// rows are long, so that a workgroup alone on its CU does not wait for every
+// stage (one row, one matrix of 4096 x 4096: 16 us with four stages, 30 with
+// two); for short rows more workgroups per CU are better (128 experts of 512
+// x 768, one row each: 20 and 18 us).
+// Through registers (rows that are not 16-byte aligned) the largest tile has
+// no room: 128 x 128 at most.
+constexpr int kFewTiles = 200;
+constexpr int kLongRow = 4096;     // bytes
+
 template <int TY, int MODE>
 moeq_status launch_mode(const GemmArgs &a, hipStream_t s, const char *name) {
-  if (!dma_ok<TY, MODE>(a)) return launch_tiles<TY, MODE, 128, 128, 2, 2, false>(a, s, name);
-  if (tile_grid<MODE, 256, 256>(a) >= 256) return launch_tiles<TY, MODE, 256, 256, 2, 4, true>(a, s, name);
-  return launch_tiles<TY, MODE, 128, 128, 2, 2, true>(a, s, name);
+  const int rows = a.P / a.E + (a.P % a.E != 0);       // mean rows per expert
+  const bool wide = MODE == kMats || (rows >= 80 && tile_grid<MODE>(a, 128, 128) >= kFewTiles);
+  if (!dma_ok<TY, MODE>(a)) {
+    if (wide) return launch_tiles<TY, MODE, 128, 128, 4, 2, 2, false>(a, s, name);
+    if constexpr (MODE == kRows) return launch_tiles<TY, MODE, 128, 64, 4, 2, 2, false>(a, s, name);
+    if constexpr (MODE == kFwd) {
+      if (rows >= 16 && tile_grid<MODE>(a, 128, 64) >= kFewTiles) return launch_tiles<TY, MODE, 128, 64, 4, 2, 2, false>(a, s, name);
+      return launch_tiles<TY, MODE, 64, 32, 4, 1, 2, false>(a, s, name);
+    }
+  }
+  if constexpr (MODE == kMats) {
+    // (here the outputs are most of the traffic: the larger tile is never
+    // worse but where an extent does not fill it)
+    if (std::min(a.ni, a.nj) > 128) return launch_tiles<TY, MODE, 256, 256, 2, 4, 2, true>(a, s, name);
+    return launch_tiles<TY, MODE, 128, 128, 4, 2, 2, true>(a, s, name);
+  } else {
+    constexpr int BI = MODE == kRows ? 128 : 64;       // (transposing reads need 128 columns)
+    const bool deep = (int64_t)a.nr * Elt<TY>::size >= kLongRow;
+    if (rows >= 160 && tile_grid<MODE>(a, 256, 256) >= kFewTiles)
+      return launch_tiles<TY, MODE, 256, 256, 2, 4, 2, true>(a, s, name);
+    if (wide) {
+      if (deep) return launch_tiles<TY, MODE, 128, 128, 4, 2, 3, true>(a, s, name);
+      return launch_tiles<TY, MODE, 128, 128, 4, 2, 2, true>(a, s, name);
+    }
+    if (rows >= 40 && tile_grid<MODE>(a, 128, 64) >= kFewTiles) {
+      if (deep) return launch_tiles<TY, MODE, 128, 64, 4, 2, 3, true>(a, s, name);
+      return launch_tiles<TY, MODE, 128, 64, 4, 2, 2, true>(a, s, name);
+    }
+    if (deep) return launch_tiles<TY, MODE, BI, 32, 4, 1, 4, true>(a, s, name);
+    return launch_tiles<TY, MODE, BI, 32, 4, 1, 2, true>(a, s, name);
+  }
 }
 
 template <int TY>

@@ -29,6 +29,29 @@ __device__ __forceinline__ int i8_code(float x, RowScale r) {
   return r.zero ? 0 : (int)__builtin_rintf(x / r.scale);
 }
 
+// The codes of eight values, a byte each.  x * (1 / scale) is within 3
+// roundings (2^-24 of at most 127 each) of the quotient: only next to a half
+// (here 2^-14) can it round otherwise, and the division is made.
+__device__ __forceinline__ u32x2 i8_codes(const float *x, RowScale r) {
+  const float inv = r.zero ? 0.f : 1.f / r.scale;
+  float q[8];
+  bool near = false;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float t = x[j] * inv;
+    q[j] = __builtin_rintf(t);
+    near |= __builtin_fabsf(__builtin_fabsf(t - q[j]) - 0.5f) < 0x1p-14f;
+  }
+  if (near) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = (float)i8_code(x[j], r);
+  }
+  u32x2 c = {0u, 0u};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) c[j / 4] |= (r.zero ? 0u : (uint32_t)(int)q[j] & 0xffu) << (8 * (j & 3));
+  return c;
+}
+
 // row_scale_of for a workgroup of NW waves that each hold part of one row
 // (s_top: NW floats; the result is the same in every thread).
 template <int NW>
@@ -36,6 +59,7 @@ __device__ __forceinline__ RowScale row_scale(float top, bool bad, float *s_top)
   if (bad) top = __builtin_inff();
 #pragma unroll
   for (int o = 32; o; o >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, o, kWave));
+  if constexpr (NW == 1) return row_scale_of(top, top == __builtin_inff());
   if ((threadIdx.x & 63) == 0) s_top[threadIdx.x >> 6] = top;
   __syncthreads();
 #pragma unroll
