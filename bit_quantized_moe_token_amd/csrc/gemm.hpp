@@ -463,25 +463,32 @@ __device__ __forceinline__ void write_tile(const GemmArgs &a, const Tile &t, int
 }
 
 // ---- tiled kernel: a workgroup of WI x WJ waves computes BI x BJ outputs,
-// walking r through a ring of RING LDS stages.
+// walking r through LDS rings of RI stages of I and RJ (RI or one less) of J.
 //
 // A wave multiplies half a stage out of registers while it reads the
 // fragments of the next half into a second set, so that the matrix pipe does
-// not wait for LDS.  Before the second half of stage p every wave has taken
-// it into registers, which frees the stage for p + RING; stage p + 1 has to be
-// there by then, for its first fragments: one wait and one barrier per stage.
+// not wait for LDS.  Before the second half of stage k every wave has taken
+// it into registers, which frees its places for stage k + RI of I and k + RJ
+// of J; stage k + 1 has to be there by then, for its first fragments: one
+// wait and one barrier per stage.
 //
-// LDS of a workgroup: the stages, and the pair ids of kMats.
-template <int MODE, int BI, int BJ, bool DMA, int RING>
+// With tiles of 256 x 256 the rings are the kernel's bound: without the DMA
+// operations 1024 tiles of r 5632 take 541 us, without the MFMAs 640 (417
+// when all of them hit the L2), with both 777 at two stages each.  The third
+// stage of I, which is the matrices and comes from HBM, fills the LDS.
+//
+// LDS of a workgroup: the rings, and the pair ids of kMats.
+template <int MODE, int BI, int BJ, int RI, int RJ, bool DMA>
 constexpr size_t tile_lds() {
-  return RING * (BI + BJ) * kStageBytes + (MODE == kMats && DMA ? 2 * (BI * kStageBytes / 1024) * 256 : 0);
+  return (RI * BI + RJ * BJ) * kStageBytes + (MODE == kMats && DMA ? 2 * (BI * kStageBytes / 1024) * 256 : 0);
 }
 
-template <int TY, int MODE, int BI, int BJ, int WI, int WJ, int RING, bool DMA>
+template <int TY, int MODE, int BI, int BJ, int WI, int WJ, int RI, int RJ, bool DMA>
 __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) {
   constexpr int ES = Elt<TY>::size, NW = WI * WJ, TI = BI / WI / 16, TJ = BJ / WJ / 16;
-  constexpr bool RI = MODE != kFwd, RJ = MODE == kMats;
-  constexpr uint32_t kTileI = BI * kStageBytes, kStage = kTileI + BJ * kStageBytes;
+  constexpr bool XI = MODE != kFwd, XJ = MODE == kMats;      // r is the row index of the operand
+  constexpr uint32_t kTileI = BI * kStageBytes, kTileJ = BJ * kStageBytes, kJ = RI * kTileI;   // J's ring
+  static_assert(RI == RJ || RI == RJ + 1, "see the wait counts");
   using Acc = typename Elt<TY>::acc;
   extern __shared__ __attribute__((aligned(1024))) uint8_t gemm_lds[];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -490,8 +497,8 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) 
   int nr, j0;
   if (!pick_tile<MODE, BI, BJ>(a, &t, &nr, &j0)) return;
 
-  using OpI = Operand<ES, BI, NW, RI, DMA>;
-  using OpJ = Operand<ES, BJ, NW, RJ, DMA>;
+  using OpI = Operand<ES, BI, NW, XI, DMA>;
+  using OpJ = Operand<ES, BJ, NW, XJ, DMA>;
   OpI di(wave);
   OpJ dj(wave);
   // kMats with pairs: the pair ids of the rows that this wave moves come by
@@ -500,7 +507,7 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) 
   // k % 2, one dword per lane and block.
   constexpr bool kIdx = MODE == kMats && DMA;
   i32x4 prs{};
-  auto idx_at = [&](int q, int k) { return gemm_lds + RING * kStage + (((k & 1) * NW + wave) * OpI::NB + q) * 256; };
+  auto idx_at = [&](int q, int k) { return gemm_lds + kJ + RJ * kTileJ + (((k & 1) * NW + wave) * OpI::NB + q) * 256; };
   auto fetch_idx = [&](int q, int k) {
     const int r = k * kStageRows + di.r_of(q);
     lds_dma_raw<4>(prs, r < nr ? (uint32_t)r * 4u : kNowhere, 0, idx_at(q, k));
@@ -541,15 +548,18 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) 
     }
   }
   constexpr int kOps = DMA ? OpI::NB + OpJ::NB : 0;
-  auto move = [&](int q, int k, uint8_t *st) {   // q-th DMA of stage k
+  // DMA operations of a stage, J's first: q-th of stage kj of J to toj, or of
+  // stage ki of I to toi
+  auto move = [&](int q, int kj, uint8_t *toj, int ki, uint8_t *toi) {
     if constexpr (DMA) {
-      if (q < OpI::NB) {
-        if constexpr (MODE == kMats) di.dma_gather(q, source(q, k), st);
-        else if constexpr (MODE == kRows) di.dma_cols(q, k, st);
-        else di.dma_rows(q, k, st);
+      if (q < OpJ::NB) {
+        if constexpr (XJ) dj.dma_cols(q, kj, toj);
+        else dj.dma_rows(q, kj, toj);
       } else {
-        if constexpr (RJ) dj.dma_cols(q - OpI::NB, k, st + kTileI);
-        else dj.dma_rows(q - OpI::NB, k, st + kTileI);
+        const int i = q - OpJ::NB;
+        if constexpr (MODE == kMats) di.dma_gather(i, source(i, ki), toi);
+        else if constexpr (MODE == kRows) di.dma_cols(i, ki, toi);
+        else di.dma_rows(i, ki, toi);
       }
     }
   };
@@ -565,38 +575,40 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) 
       } else {
         di.load_rows(k);
       }
-      if constexpr (RJ) dj.load_cols(k);
+      if constexpr (XJ) dj.load_cols(k);
       else dj.load_rows(k);
     }
   };
-  auto store = [&](uint8_t *st) {                // and from there into its place
+  auto store = [&](uint8_t *toj, uint8_t *toi) {   // and from there into its place
     if constexpr (!DMA) {
-      di.store(st);
-      dj.store(st + kTileI);
+      di.store(toi);
+      dj.store(toj);
     }
   };
-  static_assert(RING == 2 || (DMA && MODE != kMats), "longer rings count DMA operations only");
+  static_assert(RI == 2 || (DMA && MODE != kMats), "longer rings count DMA operations only");
 
   Acc acc[TI][TJ];
 #pragma unroll
   for (int i = 0; i < TI; ++i)
 #pragma unroll
     for (int j = 0; j < TJ; ++j) acc[i][j] = Acc{0, 0, 0, 0};
-  const FragReader<BI, RI> fi(0, wi * TI);
-  const FragReader<BJ, RJ> fj(kTileI, wj * TJ);
+  const FragReader<BI, XI> fi(0, wi * TI);
+  const FragReader<BJ, XJ> fj(kJ, wj * TJ);
   const int stages = (int)(((int64_t)nr * ES + kStageBytes - 1) / kStageBytes);
   if (stages > 0) {
 #pragma unroll
-    for (int k = 0; k < RING; ++k) {
+    for (int k = 0; k < RI; ++k) {
+      uint8_t *toj = gemm_lds + kJ + k * kTileJ, *toi = gemm_lds + k * kTileI;
       if (!DMA) {
         load(k);
-        store(gemm_lds + k * kStage);
+        store(toj, toi);
       }
 #pragma unroll
-      for (int q = 0; q < kOps; ++q) move(q, k, gemm_lds + k * kStage);
+      for (int q = 0; q < kOps; ++q)
+        if (k < RJ || q >= OpJ::NB) move(q, k, toj, k, toi);
     }
     if (!DMA) load(2);
-    lgkm_vm_wait<(RING - 1) * kOps>();
+    lgkm_vm_wait<DMA ? (RJ - 1) * OpJ::NB + (RI - 1) * OpI::NB : 0>();
     if constexpr (kIdx) {    // (both stages' ids have been read)
       if (a.pairs) {
 #pragma unroll
@@ -610,28 +622,27 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) 
 #pragma unroll
     for (int j = 0; j < TJ; ++j) y[0][j] = fj.read(gemm_lds, j, 0);
     // The MFMAs of a half stage (set C), with the reads of the next one
-    // (half 1 - C of the stage at st) between them, in kSeg parts.  In the
-    // second half a part starts with its share of the DMA operations of
-    // stage k (all at once after the barrier they hold the waves up: a CU
+    // (half 1 - C of the stage at sti, stj) between them, in kSeg parts.  In the
+    // second half a part starts with its share of the DMA operations (all at once after the barrier they hold the waves up: a CU
     // takes one in about 16 cycles).  The last part has no reads, so that its
     // MFMAs cover their latency.
-    auto half = [&](auto c, const uint8_t *st, int k, uint8_t *to) {
+    auto half = [&](auto c, const uint8_t *sti, const uint8_t *stj, int k, uint8_t *toi, uint8_t *toj) {
       constexpr int C = decltype(c)::value, N = 1 - C;
       constexpr int kSeg = TI < 4 ? TI : 4, kRd = kSeg > 1 ? kSeg - 1 : 1, IS = TI / kSeg;
-      constexpr int kReads = TI + TJ, kInsI = RI ? 2 : 1, kInsJ = RJ ? 2 : 1;
+      constexpr int kReads = TI + TJ, kInsI = XI ? 2 : 1, kInsJ = XJ ? 2 : 1;
 #pragma unroll
       for (int g = 0; g < kSeg; ++g) {
         if constexpr (C == 1) {
 #pragma unroll
           for (int q = 0; q < kOps; ++q)
-            if (q * kSeg / std::max(kOps, 1) == g) move(q, k, to);
+            if (q * kSeg / std::max(kOps, 1) == g) move(q, k + RJ, toj, k + RI, toi);
         }
         int ins = 0;
 #pragma unroll
         for (int f = 0; f < kReads; ++f)
           if (f * kRd / kReads == g) {
-            if (f < TJ) y[N][f] = fj.read(st, f, N), ins += kInsJ;
-            else x[N][f - TJ] = fi.read(st, f - TJ, N), ins += kInsI;
+            if (f < TJ) y[N][f] = fj.read(stj, f, N), ins += kInsJ;
+            else x[N][f - TJ] = fi.read(sti, f - TJ, N), ins += kInsI;
           }
 #pragma unroll
         for (int i = g * IS; i < (g + 1) * IS; ++i)
@@ -648,18 +659,16 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) 
         __builtin_amdgcn_sched_barrier(0);
       }
     };
-    uint32_t sb = 0;         // where stage k is
-    // the wait and the barrier before the second half of stage k; where
-    // stage k + 1 is
+    uint32_t ai = 0, aj = 0; // where stage k is in the rings
+    // the wait and the barrier before the second half of stage k
     auto turn = [&](int k) {
-      lgkm_vm_wait<(RING - 2) * kOps>();
+      lgkm_vm_wait<DMA ? (RJ - 2) * kOps + (RI - RJ) * OpI::NB : 0>();
       __builtin_amdgcn_s_barrier();
       if constexpr (!DMA) {
-        store(gemm_lds + sb);
+        store(gemm_lds + kJ + aj, gemm_lds + ai);
         load(k + 3);
       }
       __builtin_amdgcn_sched_barrier(0);
-      return sb == (RING - 1) * kStage ? 0u : sb + kStage;
     };
     auto ids = [&](int k) {
       if constexpr (kIdx) {
@@ -669,25 +678,31 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) 
         }
       }
     };
+    auto next = [&](uint32_t *n, uint32_t v, uint32_t tile, int ring) { *n = v == (ring - 1) * tile ? 0u : v + tile; };
     // a wave whose outputs do not exist (behind the expert's last row, or the
     // last i) only moves operands
     if (wj * TJ * 16 < t.rows && t.i0 + wi * TI * 16 < a.ni) {
 #pragma unroll 1
       for (int k = 0; k < stages; ++k) {
-        half(std::integral_constant<int, 0>{}, gemm_lds + sb, 0, nullptr);
-        const uint32_t sn = turn(k);
-        half(std::integral_constant<int, 1>{}, gemm_lds + sn, k + RING, gemm_lds + sb);
+        half(std::integral_constant<int, 0>{}, gemm_lds + ai, gemm_lds + aj, 0, nullptr, nullptr);
+        turn(k);
+        uint32_t ni, nj;
+        next(&ni, ai, kTileI, RI);
+        next(&nj, aj, kTileJ, RJ);
+        half(std::integral_constant<int, 1>{}, gemm_lds + ni, gemm_lds + nj, k, gemm_lds + ai, gemm_lds + kJ + aj);
         ids(k + 3);
-        sb = sn;
+        ai = ni;
+        aj = nj;
       }
     } else {
 #pragma unroll 1
       for (int k = 0; k < stages; ++k) {
-        const uint32_t sn = turn(k);
+        turn(k);
 #pragma unroll
-        for (int q = 0; q < kOps; ++q) move(q, k + RING, gemm_lds + sb);
+        for (int q = 0; q < kOps; ++q) move(q, k + RJ, gemm_lds + kJ + aj, k + RI, gemm_lds + ai);
         ids(k + 3);
-        sb = sn;
+        next(&ai, ai, kTileI, RI);
+        next(&aj, aj, kTileJ, RJ);
       }
     }
     vm_wait<0>();            // (the zeros of stages behind the last are still on their way)

@@ -18,13 +18,13 @@ int64_t tile_grid(const GemmArgs &a, int BI, int BJ) {
 }
 constexpr int64_t kMaxGrid = 0x7fffff00 / 512;   // (threads of a launch fit 32 bits)
 
-template <int TY, int MODE, int BI, int BJ, int WI, int WJ, int RING, bool DMA>
+template <int TY, int MODE, int BI, int BJ, int WI, int WJ, int RI, int RJ, bool DMA>
 moeq_status launch_tiles(const GemmArgs &a, hipStream_t s, const char *name) {
   const int64_t grid = tile_grid<MODE>(a, BI, BJ);
   if (grid > kMaxGrid) return fail(MOEQ_ERR_UNSUPPORTED, "%s: too many tiles", name);
   prof_begin(name, s);
-  hipLaunchKernelGGL((gemm_tile_kernel<TY, MODE, BI, BJ, WI, WJ, RING, DMA>), dim3((unsigned)grid), dim3(64 * WI * WJ),
-                     (tile_lds<MODE, BI, BJ, DMA, RING>()), s, a);
+  hipLaunchKernelGGL((gemm_tile_kernel<TY, MODE, BI, BJ, WI, WJ, RI, RJ, DMA>), dim3((unsigned)grid), dim3(64 * WI * WJ),
+                     (tile_lds<MODE, BI, BJ, RI, RJ, DMA>()), s, a);
   prof_end(name, s);
   return check_launch(name);
 }
@@ -66,33 +66,33 @@ moeq_status launch_mode(const GemmArgs &a, hipStream_t s, const char *name) {
   const int rows = a.P / a.E + (a.P % a.E != 0);       // mean rows per expert
   const bool wide = MODE == kMats || (rows >= 80 && tile_grid<MODE>(a, 128, 128) >= kFewTiles);
   if (!dma_ok<TY, MODE>(a)) {
-    if (wide) return launch_tiles<TY, MODE, 128, 128, 4, 2, 2, false>(a, s, name);
-    if constexpr (MODE == kRows) return launch_tiles<TY, MODE, 128, 64, 4, 2, 2, false>(a, s, name);
+    if (wide) return launch_tiles<TY, MODE, 128, 128, 4, 2, 2, 2, false>(a, s, name);
+    if constexpr (MODE == kRows) return launch_tiles<TY, MODE, 128, 64, 4, 2, 2, 2, false>(a, s, name);
     if constexpr (MODE == kFwd) {
-      if (rows >= 16 && tile_grid<MODE>(a, 128, 64) >= kFewTiles) return launch_tiles<TY, MODE, 128, 64, 4, 2, 2, false>(a, s, name);
-      return launch_tiles<TY, MODE, 64, 32, 4, 1, 2, false>(a, s, name);
+      if (rows >= 16 && tile_grid<MODE>(a, 128, 64) >= kFewTiles) return launch_tiles<TY, MODE, 128, 64, 4, 2, 2, 2, false>(a, s, name);
+      return launch_tiles<TY, MODE, 64, 32, 4, 1, 2, 2, false>(a, s, name);
     }
   }
   if constexpr (MODE == kMats) {
     // (here the outputs are most of the traffic: the larger tile is never
     // worse but where an extent does not fill it)
-    if (std::min(a.ni, a.nj) > 128) return launch_tiles<TY, MODE, 256, 256, 2, 4, 2, true>(a, s, name);
-    return launch_tiles<TY, MODE, 128, 128, 4, 2, 2, true>(a, s, name);
+    if (std::min(a.ni, a.nj) > 128) return launch_tiles<TY, MODE, 256, 256, 2, 4, 2, 2, true>(a, s, name);
+    return launch_tiles<TY, MODE, 128, 128, 4, 2, 2, 2, true>(a, s, name);
   } else {
     constexpr int BI = MODE == kRows ? 128 : 64;       // (transposing reads need 128 columns)
     const bool deep = (int64_t)a.nr * Elt<TY>::size >= kLongRow;
     if (rows >= 160 && tile_grid<MODE>(a, 256, 256) >= kFewTiles)
-      return launch_tiles<TY, MODE, 256, 256, 2, 4, 2, true>(a, s, name);
+      return launch_tiles<TY, MODE, 256, 256, 2, 4, 3, 2, true>(a, s, name);
     if (wide) {
-      if (deep) return launch_tiles<TY, MODE, 128, 128, 4, 2, 3, true>(a, s, name);
-      return launch_tiles<TY, MODE, 128, 128, 4, 2, 2, true>(a, s, name);
+      if (deep) return launch_tiles<TY, MODE, 128, 128, 4, 2, 3, 3, true>(a, s, name);
+      return launch_tiles<TY, MODE, 128, 128, 4, 2, 2, 2, true>(a, s, name);
     }
     if (rows >= 40 && tile_grid<MODE>(a, 128, 64) >= kFewTiles) {
-      if (deep) return launch_tiles<TY, MODE, 128, 64, 4, 2, 3, true>(a, s, name);
-      return launch_tiles<TY, MODE, 128, 64, 4, 2, 2, true>(a, s, name);
+      if (deep) return launch_tiles<TY, MODE, 128, 64, 4, 2, 3, 3, true>(a, s, name);
+      return launch_tiles<TY, MODE, 128, 64, 4, 2, 2, 2, true>(a, s, name);
     }
-    if (deep) return launch_tiles<TY, MODE, BI, 32, 4, 1, 4, true>(a, s, name);
-    return launch_tiles<TY, MODE, BI, 32, 4, 1, 2, true>(a, s, name);
+    if (deep) return launch_tiles<TY, MODE, BI, 32, 4, 1, 4, 4, true>(a, s, name);
+    return launch_tiles<TY, MODE, BI, 32, 4, 1, 2, 2, true>(a, s, name);
   }
 }
 
