@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(norm_block(NT)) block_norm_kernel(NormArgs a) 
 // column sums in registers; they leave once, as one row of a.part per
 // workgroup, for the summing kernel below (no atomics: the order is fixed).
 template <int TY, int TR, int NT, int CH>
-__global__ void __launch_bounds__(norm_block(NT)) block_norm_grad_kernel(NormArgs a) {
+__global__ void __launch_bounds__(norm_block(NT), CH == 1 ? 4 : 1) block_norm_grad_kernel(NormArgs a) {
   constexpr int RW = norm_block(NT) / NT;   // rows at a time
   __shared__ float s[2 * 3 * 16];
   const int t = threadIdx.x % NT;
@@ -149,6 +149,20 @@ __global__ void __launch_bounds__(norm_block(NT)) block_norm_grad_kernel(NormArg
     for (int c = 0; c < CH; ++c)
 #pragma unroll
       for (int j = 0; j < 8; ++j) sums[q][c][j] = 0.f;
+  // the rows' weights as stored; opaque to the compiler in every row, which
+  // would keep their fp32 values in registers otherwise
+  Oct<TY> wq[CH], wp[CH], gt[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int i = (c * NT + t) * 8;
+    if (a.w_pre) wq[c].load(a.w_pre, i, a.H - i);
+    else wq[c].fill(1.f);
+    if (a.w_post) wp[c].load(a.w_post, i, a.H - i);
+    else wp[c].fill(1.f);
+    if (a.gate && !a.ld_gate) gt[c].load(a.gate, i, a.H - i);
+    else gt[c].fill(1.f);
+  }
+  const bool tok = a.gate && a.ld_gate;     // a gate row per token
   for (int64_t row = lo; row < hi; ++row) {
     const int64_t at = row * a.H;
     Oct<TR> r[CH], dr[CH];
@@ -160,76 +174,71 @@ __global__ void __launch_bounds__(norm_block(NT)) block_norm_grad_kernel(NormArg
       r[c].load(a.res, at + i, a.H - i);
       dn[c].load(a.d_n, at + i, a.H - i);
       if (a.d_res) dr[c].load(a.d_res, at + i, a.H - i);
+      else dr[c].fill(0.f);
       if (a.y) x[c].load(a.y, at + i, a.H - i);
+      else x[c].fill(0.f);
+      if (tok) gt[c].load(a.gate, at + i, a.H - i);
+      wq[c].opaque();
+      wp[c].opaque();
+      gt[c].opaque();
     }
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int i = (c * NT + t) * 8;
-      Oct<TY> w;
-      if (a.w_pre) w.load(a.w_pre, i, a.H - i);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float g = a.w_pre ? dn[c][j] * w[j] : dn[c][j];
+        const float g = dn[c][j] * wq[c][j];
         q3[0] += r[c][j] * r[c][j];
         q3[1] += g * r[c][j];
-        if (a.y && a.post) q3[2] += x[c][j] * x[c][j];
+        q3[2] += x[c][j] * x[c][j];
       }
     }
     row_sum<NT, 3>(q3, s, 0);
     const float k = 1.f / __builtin_sqrtf(q3[0] * rh + a.eps);
-    const float m = q3[1] * k * rh;          // mean(g u)
+    const float m = q3[1] * k * rh;         // mean(g u)
     const float b = a.post ? 1.f / __builtin_sqrtf(q3[2] * rh + a.eps) : 1.f;
-    float d[CH][8], z[1] = {0.f};           // dr, sum of c v
+    const float al = a.y ? a.alpha : 1.f;
+    float d[CH][8], z[1] = {0.f};           // c, sum of c v
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int i = (c * NT + t) * 8;
-      Oct<TY> w, g, wp, o;
-      Oct<TR> out;
       float ov[8], dv[8];
-      if (a.w_pre) w.load(a.w_pre, i, a.H - i);
-      if (a.y && a.w_post) wp.load(a.w_post, i, a.H - i);
-      if (a.y && a.gate) g.load(a.gate, row * a.ld_gate + i, a.H - i);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float gg = a.w_pre ? dn[c][j] * w[j] : dn[c][j], u = r[c][j] * k;
-        float e = k * (gg - u * m);
-        if (a.d_res) e += dr[c][j];
+        const float u = r[c][j] * k;
+        const float e = k * (dn[c][j] * wq[c][j] - u * m) + dr[c][j];
         sums[0][c][j] += dn[c][j] * u;
-        ov[j] = a.y ? a.alpha * e : e;
-        dv[j] = 0.f;
-        if (a.y) {
-          const float q = x[c][j] * b, p = a.w_post ? q * wp[j] : q;
-          const float eg = a.gate ? e * g[j] : e;
-          sums[1][c][j] += eg * q;
-          if (a.gate) {
-            if (a.ld_gate) dv[j] = e * p;
-            else sums[2][c][j] += e * p;
-          }
-          d[c][j] = a.w_post ? eg * wp[j] : eg;
-          z[0] += d[c][j] * q;
-        }
+        ov[j] = al * e;
+        const float v = x[c][j] * b, eg = e * gt[c][j];
+        sums[1][c][j] += eg * v;
+        dv[j] = e * v * wp[c][j];
+        sums[2][c][j] += dv[j];
+        d[c][j] = eg * wp[c][j];
+        z[0] += d[c][j] * v;
       }
+      Oct<TR> out;
       out.pack(ov);
       out.store(a.d_r, at + i, a.H - i);
-      if (a.y && a.gate && a.ld_gate) o.pack(dv), o.store(a.d_gate, at + i, a.H - i);
+      if (tok) {
+        Oct<TY> o;
+        o.pack(dv);
+        o.store(a.d_gate, at + i, a.H - i);
+      }
     }
+    // (also a barrier between this row's sums in s and the next one's)
+    row_sum<NT, 1>(z, s, 1);
     if (a.y) {
-      if (a.post) row_sum<NT, 1>(z, s, 1);
-      const float mz = z[0] * rh;
+      const float mz = a.post ? z[0] * rh : 0.f;
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const int i = (c * NT + t) * 8;
         Oct<TY> o;
         float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = a.post ? b * (d[c][j] - x[c][j] * b * mz) : d[c][j];
+        for (int j = 0; j < 8; ++j) v[j] = b * (d[c][j] - x[c][j] * b * mz);
         o.pack(v);
         o.store(a.d_y, at + i, a.H - i);
       }
-    } else if (NT > 64) {
-      __syncthreads();        // s is written again by the next row's first reduction
     }
-    if (a.y && !a.post && NT > 64) __syncthreads();
   }
   if (!a.cols) return;
 #pragma unroll
@@ -243,58 +252,77 @@ __global__ void __launch_bounds__(norm_block(NT)) block_norm_grad_kernel(NormArg
     }
 }
 
-// Column sums of the units' partial sums: 64 columns per workgroup, 16
+// Column sums of the units' partial sums: 32 columns per workgroup, 32
 // threads a column, joined in a fixed order.
 __global__ void __launch_bounds__(1024) norm_columns_kernel(const float *__restrict__ part, int32_t units, int32_t H,
                                                             float *d_w_pre, float *d_w_post, float *d_gate) {
-  __shared__ float s[16][64];
-  const int q = blockIdx.y, c = blockIdx.x * 64 + (threadIdx.x & 63), w = threadIdx.x >> 6;
+  __shared__ float s[32][33];
+  const int q = blockIdx.y, x = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
   float *out = q == 0 ? d_w_pre : q == 1 ? d_w_post : d_gate;
   if (!out) return;
   float v = 0.f;
-  if (c < H)
-    for (int u = w; u < units; u += 16) v += part[((int64_t)u * 3 + q) * H + c];
-  s[w][threadIdx.x & 63] = v;
+  if (c < H) {
+#pragma unroll 8
+    for (int u = w; u < units; u += 32) v += part[((int64_t)u * 3 + q) * H + c];
+  }
+  s[w][x] = v;
   __syncthreads();
   if (w == 0 && c < H) {
     v = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v += s[i][threadIdx.x];
+    for (int i = 0; i < 32; ++i) v += s[i][x];
     out[c] = v;
   }
 }
 
 constexpr int kNormMaxH = 32768;
-constexpr int kGradGroups = 512;   // most workgroups of the gradient kernel
 
-// Threads per row for rows of H.
-static int norm_threads(int H) { return H <= 1024 ? 64 : H <= 4096 ? 256 : H <= 8192 ? 512 : 1024; }
+// Threads per row of the gradient kernel for rows of H: one piece of eight a
+// thread as far as 1024 threads go, so that the column sums and a row in
+// flight stay within 128 registers and a CU holds 16 waves.
+static int grad_threads(int H) { return H <= 512 ? 64 : H <= 1024 ? 128 : H <= 2048 ? 256 : H <= 4096 ? 512 : 1024; }
 
-// Units (rows in flight) of the gradient kernel.
+// Units (rows in flight) of the gradient kernel: 1024 threads per CU, each
+// unit leaving one row of partial column sums.
 static int grad_units(int T, int H) {
-  const int rw = norm_threads(H) == 64 ? 4 : 1;
-  const int groups = std::min((T + rw - 1) / rw, kGradGroups);
+  const int nt = grad_threads(H), rw = nt == 64 ? 4 : 1;
+  const int groups = std::min((T + rw - 1) / rw, 256 * 1024 / (nt * rw));
   return groups * rw;
 }
 
 template <int TY, int TR, int NT, int CH>
-static void launch_norm(const NormArgs &a, bool grad, hipStream_t s) {
+static void launch_norm(const NormArgs &a, hipStream_t s) {
   constexpr int RW = norm_block(NT) / NT;
-  if (grad)
-    hipLaunchKernelGGL((block_norm_grad_kernel<TY, TR, NT, CH>), dim3(grad_units(a.T, a.H) / RW), dim3(norm_block(NT)), 0, s, a);
-  else
-    hipLaunchKernelGGL((block_norm_kernel<TY, TR, NT, CH>), dim3((a.T + RW - 1) / RW), dim3(norm_block(NT)), 0, s, a);
+  hipLaunchKernelGGL((block_norm_kernel<TY, TR, NT, CH>), dim3((a.T + RW - 1) / RW), dim3(norm_block(NT)), 0, s, a);
+}
+
+template <int TY, int TR, int NT, int CH>
+static void launch_grad(const NormArgs &a, hipStream_t s) {
+  constexpr int RW = norm_block(NT) / NT;
+  hipLaunchKernelGGL((block_norm_grad_kernel<TY, TR, NT, CH>), dim3(grad_units(a.T, a.H) / RW), dim3(norm_block(NT)), 0, s, a);
 }
 
 template <int TY, int TR>
 static void launch_norm_h(const NormArgs &a, bool grad, hipStream_t s) {
-  if (a.H <= 512) launch_norm<TY, TR, 64, 1>(a, grad, s);
-  else if (a.H <= 1024) launch_norm<TY, TR, 64, 2>(a, grad, s);
-  else if (a.H <= 2048) launch_norm<TY, TR, 256, 1>(a, grad, s);
-  else if (a.H <= 4096) launch_norm<TY, TR, 256, 2>(a, grad, s);
-  else if (a.H <= 8192) launch_norm<TY, TR, 512, 2>(a, grad, s);
-  else if (a.H <= 16384) launch_norm<TY, TR, 1024, 2>(a, grad, s);
-  else launch_norm<TY, TR, 1024, 4>(a, grad, s);
+  if (grad) {
+    if (a.H <= 512) launch_grad<TY, TR, 64, 1>(a, s);
+    else if (a.H <= 1024) launch_grad<TY, TR, 128, 1>(a, s);
+    else if (a.H <= 2048) launch_grad<TY, TR, 256, 1>(a, s);
+    else if (a.H <= 4096) launch_grad<TY, TR, 512, 1>(a, s);
+    else if (a.H <= 8192) launch_grad<TY, TR, 1024, 1>(a, s);
+    else if (a.H <= 16384) launch_grad<TY, TR, 1024, 2>(a, s);
+    else launch_grad<TY, TR, 1024, 4>(a, s);
+    return;
+  }
+  if (a.H <= 512) launch_norm<TY, TR, 64, 1>(a, s);
+  else if (a.H <= 1024) launch_norm<TY, TR, 64, 2>(a, s);
+  else if (a.H <= 2048) launch_norm<TY, TR, 256, 1>(a, s);
+  else if (a.H <= 4096 && a.T <= 256) launch_norm<TY, TR, 512, 1>(a, s);   // (few rows: for latency)
+  else if (a.H <= 4096) launch_norm<TY, TR, 256, 2>(a, s);
+  else if (a.H <= 8192 && a.T <= 256) launch_norm<TY, TR, 1024, 1>(a, s);
+  else if (a.H <= 8192) launch_norm<TY, TR, 512, 2>(a, s);
+  else if (a.H <= 16384) launch_norm<TY, TR, 1024, 2>(a, s);
+  else launch_norm<TY, TR, 1024, 4>(a, s);
 }
 
 static void launch_norm_types(const NormArgs &a, int ty, int tr, bool grad, hipStream_t s) {
@@ -425,7 +453,7 @@ MOEQ_API moeq_status moeq_block_norm_grad(const moeq_norm *d, const void *res, c
   }
   if (cols) {
     prof_begin("norm_columns", stream);
-    hipLaunchKernelGGL(norm_columns_kernel, dim3((d->H + 63) / 64, 3), dim3(1024), 0, stream, (const float *)ws, units,
+    hipLaunchKernelGGL(norm_columns_kernel, dim3((d->H + 31) / 32, 3), dim3(1024), 0, stream, (const float *)ws, units,
                        d->H, d_w_pre, d_w_post, g_cols);
     prof_end("norm_columns", stream);
     MOEQ_TRY(check_launch("norm_columns"));

@@ -60,6 +60,16 @@ struct Oct {
     if constexpr (TY == MOEQ_F32) return Val<TY>::get(w[j]);
     else return Val<TY>::get((w[j / 2] >> (16 * (j & 1))) & 0xffffu);
   }
+  __device__ __forceinline__ void fill(float v) {
+    const uint32_t b = Val<TY>::put(v);
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[j] = TY == MOEQ_F32 ? b : b | (b << 16);
+  }
+  // the same bits, which the compiler takes for new ones
+  __device__ __forceinline__ void opaque() {
+#pragma unroll
+    for (int j = 0; j < W; ++j) asm volatile("" : "+v"(w[j]));
+  }
   __device__ __forceinline__ void pack(const float *v) {
 #pragma unroll
     for (int j = 0; j < W; ++j) {

@@ -6,6 +6,7 @@ the library filled.  No arithmetic of the method happens here.
 """
 
 import ctypes
+import functools
 from ctypes import c_void_p
 
 import numpy as np
@@ -364,12 +365,17 @@ _16BIT = (torch.float16, torch.bfloat16)
 def _like(t, dtypes, ndim, dev, name):
     """Checks a strided operand: on device index `dev`, one of `dtypes`,
     `ndim` dimensions, the last one contiguous."""
+    try:
+        if t.dtype in dtypes and t.dim() == ndim and t.get_device() == dev and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on another device than the other tensors")
     if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be one of {dtypes}, got {t.dtype}")
+        raise TypeError(f"{name} must be one of {tuple(dtypes)}, got {t.dtype}")
     if t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dimensions, got shape {tuple(t.shape)}")
     if t.stride(-1) != 1 and t.shape[-1] > 1:
@@ -402,24 +408,30 @@ def _groups(T, E, offsets, pairs, k, dev):
                        pairs.data_ptr() if pairs is not None else None, E, P, T, k), P
 
 
-def _out(out, shape, dtype, dtypes, dev, name="out"):
+def _out(out, shape, dtype, dtypes, dev, like, name="out"):
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+        return like.new_empty(shape, dtype=dtype)
     _like(out, dtypes, len(shape), dev, name)
     if tuple(out.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(out.shape)}")
     return out
 
 
+_FUNCS = {}
+
+
 def _launch(name, dev, *args):
     """Calls entry point `name` on the current stream of device `dev`."""
-    f = getattr(lib(), name)
+    f = _FUNCS.get(name)
+    if f is None:
+        f = _FUNCS[name] = getattr(lib(), name)
     if torch._C._cuda_getDevice() == dev:
         st = f(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
             st = f(*args, torch._C._cuda_getCurrentRawStream(dev))
-    check(st, name)
+    if st:
+        check(st, name)
 
 
 def grouped_gemm(x, w, offsets, pairs=None, k=1, trans=False, out=None, out_dtype=None):
@@ -439,7 +451,7 @@ def grouped_gemm(x, w, offsets, pairs=None, k=1, trans=False, out=None, out_dtyp
     if Kw != K:
         raise ValueError(f"x has {K} columns, w {Kw}")
     g, P = _groups(T, E, offsets, pairs, k, dev)
-    out = _out(out, (P, N), out_dtype or x.dtype, (x.dtype, torch.float32), dev)
+    out = _out(out, (P, N), out_dtype or x.dtype, (x.dtype, torch.float32), dev, x)
     _launch("moeq_grouped_gemm", dev, g, x.data_ptr(), _ld(x), w.data_ptr(), _ld(w), w.stride(0), int(trans), N, K,
             _DTYPE[x.dtype], out.data_ptr(), _ld(out), _DTYPE[out.dtype])
     return out
@@ -458,7 +470,7 @@ def grouped_wgrad(dy, x, offsets, pairs=None, k=1, out=None, out_dtype=torch.flo
     g, P = _groups(T, E, offsets, pairs, k, dev)
     if P != dy.shape[0]:
         raise ValueError(f"dy has {dy.shape[0]} rows for {P} sorted rows")
-    out = _out(out, (E, N, K), out_dtype, (dy.dtype, torch.float32), dev)
+    out = _out(out, (E, N, K), out_dtype, (dy.dtype, torch.float32), dev, dy)
     _launch("moeq_grouped_wgrad", dev, g, dy.data_ptr(), _ld(dy), x.data_ptr(), _ld(x), N, K, _DTYPE[dy.dtype],
             out.data_ptr(), _ld(out), out.stride(0), _DTYPE[out.dtype])
     return out
@@ -472,7 +484,7 @@ def quantize_i8(x):
     if isinstance(x, torch.Tensor) and x.dim() == 3:
         q, s = quantize_i8(x.reshape(-1, x.shape[-1]))
         return q.view(x.shape), s.view(x.shape[:2])
-    _like(x, tuple(_DTYPE), 2, dev, "x")
+    _like(x, _DTYPE, 2, dev, "x")
     q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
     s = torch.empty((x.shape[0],), dtype=torch.float32, device=x.device)
     _launch("moeq_quantize_i8", dev, x.data_ptr(), _ld(x), x.shape[0], x.shape[1], _DTYPE[x.dtype], q.data_ptr(),
@@ -504,7 +516,7 @@ def gemm_i8(xq, sx, wq, sw, offsets=None, pairs=None, k=1, out=None, out_dtype=t
     _flat(sx, T, torch.float32, dev, "sx")
     E, N, ldw, stride_w = _i8_weights(xq, wq, sw, dev)
     g, P = _groups(T, E, offsets, pairs, k, dev)
-    out = _out(out, (P, N), out_dtype, tuple(_DTYPE), dev)
+    out = _out(out, (P, N), out_dtype, _DTYPE, dev, xq)
     _launch("moeq_gemm_i8", dev, g, xq.data_ptr(), _ld(xq), sx.data_ptr(), wq.data_ptr(), ldw, stride_w, sw.data_ptr(),
             N, K, out.data_ptr(), _ld(out), _DTYPE[out.dtype])
     return out
@@ -515,13 +527,13 @@ def linear_i8(x, wq, sw, offsets=None, pairs=None, k=1, out=None, out_dtype=None
     quantize_i8 (see moeq_linear_i8).  ws: uint8 workspace tensor, or None
     for one of the call's own.  Returns [P, N] of out_dtype (x's type)."""
     dev = x.get_device() if isinstance(x, torch.Tensor) else -1
-    _like(x, tuple(_DTYPE), 2, dev, "x")
+    _like(x, _DTYPE, 2, dev, "x")
     T, K = x.shape
     E, N, ldw, stride_w = _i8_weights(x, wq, sw, dev)
     g, P = _groups(T, E, offsets, pairs, k, dev)
-    out = _out(out, (P, N), out_dtype or x.dtype, tuple(_DTYPE), dev)
+    out = _out(out, (P, N), out_dtype or x.dtype, _DTYPE, dev, x)
     if ws is None:
-        ws = torch.empty((linear_i8_workspace_size(T, K),), dtype=torch.uint8, device=x.device)
+        ws = x.new_empty((linear_i8_workspace_size(T, K),), dtype=torch.uint8)
     else:
         _like(ws, (torch.uint8,), 1, dev, "ws")
     _launch("moeq_linear_i8", dev, g, x.data_ptr(), _ld(x), _DTYPE[x.dtype], wq.data_ptr(), ldw, stride_w, sw.data_ptr(),
@@ -529,6 +541,7 @@ def linear_i8(x, wq, sw, offsets=None, pairs=None, k=1, out=None, out_dtype=None
     return out
 
 
+@functools.lru_cache(maxsize=1024)
 def linear_i8_workspace_size(T, K):
     n = ctypes.c_size_t(0)
     check(lib().moeq_linear_i8_workspace_size(T, K, ctypes.byref(n)), "moeq_linear_i8_workspace_size")
@@ -538,6 +551,11 @@ def linear_i8_workspace_size(T, K):
 # ------------------------------------------------ norms around a block
 
 def _dense(t, shape, dtype, dev, name):
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.get_device() != dev:
@@ -546,8 +564,11 @@ def _dense(t, shape, dtype, dev, name):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _addr(t):
+    return t.data_ptr() if t is not None else None
 
 
 def _norm(res, dtype, y, w_pre, w_post, gate, alpha, eps, post_norm, dev):
@@ -565,19 +586,19 @@ def _norm(res, dtype, y, w_pre, w_post, gate, alpha, eps, post_norm, dev):
     per_token = gate is not None and gate.dim() == 2
     if gate is not None:
         _dense(gate, res.shape if per_token else vec, dtype, dev, "gate")
-    p = lambda t: t.data_ptr() if t is not None else None
-    return _lib.Norm(T, H, _DTYPE[dtype], _DTYPE[res.dtype], p(w_pre), p(w_post), p(gate), int(per_token),
-                     int(bool(post_norm)), alpha, eps)
+    return _lib.Norm(T, H, _DTYPE[dtype], _DTYPE[res.dtype], _addr(w_pre), _addr(w_post), _addr(gate), per_token,
+                     bool(post_norm), alpha, eps)
 
 
 def _res(res, name):
-    dev = res.get_device() if isinstance(res, torch.Tensor) else -1
-    if dev < 0:
+    """Device index of a residual [T, H]."""
+    if not isinstance(res, torch.Tensor) or not res.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if res.dim() != 2 or res.dtype not in _DTYPE:
         raise TypeError(f"{name} must be [T, H] of fp16, bf16 or fp32, got {tuple(res.shape)} {res.dtype}")
-    _dense(res, res.shape, res.dtype, dev, name)
-    return dev
+    if not res.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return res.get_device()
 
 
 def block_norm(residual, y=None, w_pre=None, w_post=None, gate=None, alpha=1.0, eps=1e-6, post_norm=True,
@@ -603,12 +624,11 @@ def block_norm(residual, y=None, w_pre=None, w_post=None, gate=None, alpha=1.0, 
         r = res_out
         _dense(r, residual.shape, residual.dtype, dev, "res_out")
     if n_out is None:
-        n = torch.empty(residual.shape, dtype=dtype, device=residual.device)
+        n = torch.empty_like(residual if y is None else y, dtype=dtype)
     else:
         n = n_out
         _dense(n, residual.shape, dtype, dev, "n_out")
-    _launch("moeq_block_norm", dev, d, residual.data_ptr(), y.data_ptr() if y is not None else None, r.data_ptr(),
-            n.data_ptr())
+    _launch("moeq_block_norm", dev, d, residual.data_ptr(), _addr(y), r.data_ptr(), n.data_ptr())
     return r, n
 
 
@@ -637,16 +657,16 @@ def block_norm_grad(res, d_n, y=None, d_res=None, w_pre=None, w_post=None, gate=
     if gate is not None:
         out["d_gate"] = torch.empty(gate.shape, dtype=gate.dtype if gate.dim() == 2 else torch.float32, device=res.device)
     if ws is None:
-        ws = torch.empty((block_norm_grad_workspace_size(T, H),), dtype=torch.uint8, device=res.device)
+        ws = res.new_empty((block_norm_grad_workspace_size(T, H),), dtype=torch.uint8)
     else:
         _like(ws, (torch.uint8,), 1, dev, "ws")
-    p = lambda t: t.data_ptr() if t is not None else None
-    _launch("moeq_block_norm_grad", dev, d, res.data_ptr(), p(y), p(d_res), d_n.data_ptr(), p(out["d_residual"]),
-            p(out.get("d_y")), p(out.get("d_w_pre")), p(out.get("d_w_post")), p(out.get("d_gate")), ws.data_ptr(),
-            ws.numel())
+    _launch("moeq_block_norm_grad", dev, d, res.data_ptr(), _addr(y), _addr(d_res), d_n.data_ptr(),
+            _addr(out["d_residual"]), _addr(out.get("d_y")), _addr(out.get("d_w_pre")), _addr(out.get("d_w_post")),
+            _addr(out.get("d_gate")), ws.data_ptr(), ws.numel())
     return out
 
 
+@functools.lru_cache(maxsize=1024)
 def block_norm_grad_workspace_size(T, H):
     n = ctypes.c_size_t(0)
     check(lib().moeq_block_norm_grad_workspace_size(T, H, ctypes.byref(n)), "moeq_block_norm_grad_workspace_size")
