@@ -366,7 +366,7 @@ def _like(t, dtypes, ndim, dev, name):
     """Checks a strided operand: on device index `dev`, one of `dtypes`,
     `ndim` dimensions, the last one contiguous."""
     try:
-        if t.dtype in dtypes and t.dim() == ndim and t.get_device() == dev and t.is_contiguous():
+        if t.dtype in dtypes and t.dim() == ndim and t.get_device() == dev >= 0 and t.is_contiguous():
             return
     except AttributeError:
         pass
@@ -552,7 +552,7 @@ def linear_i8_workspace_size(T, K):
 
 def _dense(t, shape, dtype, dev, name):
     try:
-        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev >= 0 and t.is_contiguous():
             return
     except AttributeError:
         pass

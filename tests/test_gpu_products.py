@@ -79,6 +79,17 @@ SHAPES = [
     ([9, 9, 9], 1, 40, 33),
     ([50, 0, 70, 33], 1, 2056, 2104),       # and in the matrices' gradient
     ([600, 2, 811], 2, 200, 6300),
+    # each tile of the aligned and, at odd indices, of the unaligned path; rows
+    # of 4096 bytes and more take longer rings
+    ([90] * 15 + [91], 2, 136, 1000),
+    ([90] * 15 + [91], 2, 135, 1001),
+    ([50] * 16, 2, 136, 1000),
+    ([50] * 16, 2, 133, 1003),
+    ([90] * 16, 2, 2048, 1000),
+    ([7, 0, 3], 1, 2100, 50),
+    ([50] * 16, 2, 2048, 1000),
+    ([3] * 5, 1, 77, 130),
+    ([3, 9, 1], 2, 4096, 200),
 ]
 
 
@@ -212,7 +223,8 @@ def test_codes_of_halves():
             assert torch.equal(q.double(), torch.round(x.double() / s.double().cuda()))
 
 
-I8_SHAPES = SHAPES + [([201], 1, 1530, 1111), ([16], 1, 4096, 64), ([64], 1, 130, 300), ([4], 1, 16384, 32)]
+I8_SHAPES = SHAPES + [([201], 1, 1530, 1111), ([16], 1, 4096, 64), ([64], 1, 130, 300), ([4], 1, 16384, 32),
+                      ([0, 1], 1, 33, 5), ([90] * 16, 2, 4096, 1000), ([1], 1, 20001, 40), ([50] * 16, 2, 4096, 1000)]
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16, F32], ids=["f16", "bf16", "f32"])
@@ -307,3 +319,94 @@ def test_graph_stream_and_repeat():
         other = step()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(other, eager))
+
+
+def test_refusals():
+    from bit_quantized_moe_token_amd import moeq
+    x, w = torch.zeros(4, 64, dtype=F16, device="cuda"), torch.zeros(2, 32, 64, dtype=F16, device="cuda")
+    off, pairs = torch.tensor([0, 2, 4], dtype=torch.int32).cuda(), torch.zeros(4, dtype=torch.int32).cuda()
+    ok = moeq.grouped_gemm(x, w, off, pairs=pairs, k=1)
+    assert ok.shape == (4, 32)
+    for bad, err in (((x.cpu(), w, off), TypeError), ((x.float(), w, off), TypeError), ((x, w.bfloat16(), off), TypeError),
+                     ((x, w[0], off), ValueError), ((x[:, :63], w, off), ValueError), ((x.T, w, off), ValueError),
+                     ((x, w, off[:2]), ValueError), ((x, w, off.long()), TypeError), ((x, w, None), ValueError)):
+        with pytest.raises(err):
+            moeq.grouped_gemm(*bad)
+    with pytest.raises(TypeError):
+        moeq.grouped_gemm(x, w, off, out=torch.zeros(4, 32, dtype=BF16, device="cuda"))
+    with pytest.raises(ValueError):
+        moeq.grouped_gemm(x, w, off, out=torch.zeros(4, 31, dtype=F16, device="cuda"))
+    with pytest.raises(ValueError):
+        moeq.grouped_gemm(x, w, off, trans=True)                     # 64 columns against 32
+    with pytest.raises(moeq.MoeqError):
+        moeq.grouped_gemm(x, w, off, pairs=pairs, k=0)
+    with pytest.raises(moeq.MoeqError):
+        moeq.grouped_gemm(x[:1].expand(4, 64), w, off)               # rows that lie on each other
+    with pytest.raises(ValueError):
+        moeq.grouped_wgrad(x, x, off, pairs=pairs[:3])
+    with pytest.raises(moeq.MoeqError):
+        moeq.grouped_wgrad(x, x, off, out=torch.zeros(1, 64, 64, device="cuda").expand(2, 64, 64))
+    wq, sw = torch.zeros(32, 64, dtype=torch.int8, device="cuda"), torch.ones(32, device="cuda")
+    for bad, err in (((x, wq.float(), sw), TypeError), ((x, wq[:, :63], sw), ValueError), ((x, wq, sw[:31]), ValueError),
+                     ((x, wq, sw.half()), TypeError), ((x.double(), wq, sw), TypeError)):
+        with pytest.raises(err):
+            moeq.linear_i8(*bad)
+    with pytest.raises(moeq.MoeqError) as e:
+        moeq.linear_i8(x, wq, sw, ws=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == 3
+
+
+def test_equal_inputs_and_shared_matrices():
+    """The same source row at several places gives equal rows; experts may
+    share one matrix (stride 0); outputs may be a view with gaps."""
+    from bit_quantized_moe_token_amd import moeq
+    rng = np.random.default_rng(12)
+    x, w = _rows(rng, (3, 80), BF16), _rows(rng, (1, 48, 80), BF16)
+    off = torch.tensor([0, 70, 70, 200], dtype=torch.int32).cuda()
+    pairs = torch.from_numpy((np.arange(200) % 3 * 2).astype(np.int32)).cuda()
+    buf = torch.full((200, 61), 5.0, dtype=BF16, device="cuda")
+    y = moeq.grouped_gemm(x, w.expand(3, 48, 80), off, pairs=pairs, k=2, out=buf[:, :48])
+    one = moeq.grouped_gemm(x, w, torch.tensor([0, 3], dtype=torch.int32).cuda())
+    assert torch.equal(y, one[torch.arange(200, device="cuda") % 3])
+    assert bool((buf[:, 48:] == 5).all())
+
+
+def test_two_streams_and_two_graphs():
+    """Two captured passes and eager ones on two streams, each with outputs
+    and workspaces of its own, do not disturb each other."""
+    from bit_quantized_moe_token_amd import moeq
+    rng = np.random.default_rng(13)
+    passes = []
+    for n in (300, 40):
+        off, pairs = _routing(rng, [n, 5, n // 2], 2, 64)
+        x, w = _rows(rng, (64, 512), F16), _rows(rng, (3, 256, 512), F16)
+        wq, sw = moeq.quantize_i8(w)
+        passes.append((torch.from_numpy(off).cuda(), torch.from_numpy(pairs).cuda(), x, w, wq, sw))
+
+    def step(p):
+        off, pairs, x, w, wq, sw = p
+        y = moeq.grouped_gemm(x, w, off, pairs=pairs, k=2)
+        return y, moeq.linear_i8(x, wq, sw, offsets=off, pairs=pairs, k=2), moeq.grouped_wgrad(y, x, off, pairs=pairs, k=2)
+
+    eager = [[t.clone() for t in step(p)] for p in passes]
+    graphs, outs = [], []
+    for p in passes:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(step(p))
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for o in outs:
+            for t in o:
+                t.zero_()
+        torch.cuda.synchronize()
+        live = []
+        for g, s, p in zip(graphs, streams, passes):
+            with torch.cuda.stream(s):
+                g.replay()
+                live.append(step(p))
+        torch.cuda.synchronize()
+        for o, l, e in zip(outs, live, eager):
+            assert all(torch.equal(a, b) for a, b in zip(o, e))
+            assert all(torch.equal(a, b) for a, b in zip(l, e))

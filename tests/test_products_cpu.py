@@ -128,3 +128,17 @@ def test_oracle_codes():
                                      dtype=np.float32))
     assert q.tolist() == [[127, -64, 0, 2], [0] * 4, [0] * 4, [0] * 4]
     assert s[0] == 1 and s[1] == 1 and np.isnan(s[2]) and s[3] == 1
+
+
+def test_host_tensors_refused():
+    """Tensors in host memory never reach the library."""
+    torch = pytest.importorskip("torch")
+    from bit_quantized_moe_token_amd import moeq
+    x, w, off = torch.zeros(4, 8).half(), torch.zeros(2, 6, 8).half(), torch.zeros(3).int()
+    v = torch.zeros(8).half()
+    for call in (lambda: moeq.grouped_gemm(x, w, off), lambda: moeq.grouped_wgrad(x, x, off), lambda: moeq.quantize_i8(x),
+                 lambda: moeq.linear_i8(x, w[0].char(), torch.ones(6)), lambda: moeq.gemm_i8(x.char(), torch.ones(4), w[0].char(), torch.ones(6)),
+                 lambda: moeq.block_norm(x, x, w_pre=v), lambda: moeq.block_norm_grad(x, x, x, w_pre=v),
+                 lambda: moeq.grouped_gemm(None, w, off), lambda: moeq.block_norm(None), lambda: moeq.block_norm_grad(x, None)):
+        with pytest.raises(TypeError):
+            call()
