@@ -8,7 +8,8 @@ using namespace moeq;
 namespace {
 
 constexpr int32_t kMaxLen = 1 << 20;     // row length of an operand
-constexpr int32_t kMaxI8K = 131072;      // 127^2 * K stays within 31 bits
+constexpr int32_t kMaxI8K = 131071;      // 128^2 K stays within 31 bits
+constexpr int32_t kMaxRows = 1 << 29;    // sorted rows: 4 bytes of pair id each within 31 bits
 
 int elt_size(int dtype) { return dtype == MOEQ_F32 ? 4 : dtype == kI8 ? 1 : 2; }
 
@@ -16,6 +17,8 @@ moeq_status check_groups(const char *who, const moeq_groups *g) {
   if (!g) return fail(MOEQ_ERR_INVALID, "%s: null groups", who);
   if (g->E < 1 || g->E > 256) return fail(MOEQ_ERR_INVALID, "%s: E=%d not in 1..256", who, g->E);
   if (g->P < 0 || g->T < 0) return fail(MOEQ_ERR_INVALID, "%s: negative P=%d or T=%d", who, g->P, g->T);
+  if (g->P > kMaxRows) return fail(MOEQ_ERR_UNSUPPORTED, "%s: P=%d above %d", who, g->P, kMaxRows);
+  if (g->P && !g->T) return fail(MOEQ_ERR_INVALID, "%s: P=%d rows without source rows", who, g->P);
   if (!g->offsets && g->E != 1) return fail(MOEQ_ERR_INVALID, "%s: no offsets with E=%d", who, g->E);
   if (g->pairs && g->k < 1) return fail(MOEQ_ERR_INVALID, "%s: k=%d must be positive", who, g->k);
   if (!g->pairs && g->T < g->P) return fail(MOEQ_ERR_INVALID, "%s: T=%d source rows for P=%d rows", who, g->T, g->P);

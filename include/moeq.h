@@ -462,7 +462,8 @@ moeq_status moeq_expert_ffn_noalloc(const moeq_layer *L, const uint16_t *x, int3
  *   offsets DEVICE [E + 1] int32, or NULL: one expert (E = 1), all P rows.
  *   pairs   DEVICE [P] int32, or NULL: sorted row r reads row r (T >= P, k
  *           is then ignored).
- *   1 <= E <= 256; P, T >= 0; k >= 1.
+ *   1 <= E <= 256; 0 <= P <= 2^29; T >= 0, and >= 1 where there are rows;
+ *   k >= 1.
  * The counts stay on the device: nothing is read back.  Offsets outside
  * [0, P] are taken as the nearer end; a pair whose source row lies outside
  * [0, T) reads a row of zeros; rows at or behind offsets[E] (and before
@@ -512,7 +513,8 @@ moeq_status moeq_grouped_wgrad(const moeq_groups *g, const void *dy, int64_t ldd
  * (each quotient rounded to fp32, rint = half to even; codes in -127..127).  A row with a < 2^-118 gets codes 0 and scale 1; a row that
  * holds an infinity or a NaN gets codes 0 and scale NaN (so that what is
  * computed from it is NaN).
- *   x DEVICE [rows, cols] of dtype MOEQ_F16, MOEQ_BF16 or MOEQ_F32;
+ *   x DEVICE [rows, cols] of dtype MOEQ_F16, MOEQ_BF16 or MOEQ_F32, rows
+ *   below 2^22, cols up to 2^20;
  *   codes DEVICE [rows, cols] int8 out; scales DEVICE [rows] fp32 out.
  */
 moeq_status moeq_quantize_i8(const void *x, int64_t ldx, int32_t rows, int32_t cols, int32_t dtype, int8_t *codes,
@@ -522,8 +524,8 @@ moeq_status moeq_quantize_i8(const void *x, int64_t ldx, int32_t rows, int32_t c
  * moeq_gemm_i8 — products of 8-bit codes with a scale per source row
  * (token) and per (expert, output channel):
  *   y[r, n] = (sum_c xq[src(r), c] * wq_e[n, c]) * sx[src(r)] * sw[e, n]
- * The integer sum is exact (K <= 131072); the scaling is fp32, rounded once
- * to y_dtype.
+ * The integer sum is exact, whatever the codes (K <= 131071); the scaling is
+ * fp32, rounded once to y_dtype.
  *   xq DEVICE [T, K] int8, sx DEVICE [T] fp32; wq DEVICE E matrices [N, K]
  *   int8 stride_w elements apart, sw DEVICE [E, N] fp32; y DEVICE [P, N] of
  *   y_dtype MOEQ_F16, MOEQ_BF16 or MOEQ_F32.
@@ -551,7 +553,7 @@ moeq_status moeq_linear_i8(const moeq_groups *g, const void *x, int64_t ldx, int
  *   r' = alpha * residual + gate * p                 rounded to res_dtype
  *   n  = w_pre * r' / sqrt(mean(r'^2) + eps)         of the rounded r'
  * Statistics and sums are fp32, each output rounded once.
- *   T tokens, H values each (T >= 0, 1 <= H <= 32768); every matrix is
+ *   T tokens, H values each (0 <= T < 2^22, 1 <= H <= 32768); every matrix is
  *   [T, H], rows one after the other, aligned to its elements.
  *   dtype: MOEQ_F16, MOEQ_BF16 or MOEQ_F32, of y, n, the weights and the
  *   gate; res_dtype: of residual and r', dtype or MOEQ_F32.

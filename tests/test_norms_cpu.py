@@ -22,7 +22,7 @@ def _d(T=4, H=64, dtype=0, res=0, w_pre=P, w_post=P, gate=P, per_token=0, post=1
     return ctypes.byref(_lib.Norm(T, H, dtype, res, w_pre, w_post, gate, per_token, post, alpha, eps))
 
 
-BAD = [(dict(T=-1), 1), (dict(H=0), 1), (dict(H=32769), 2), (dict(dtype=3), 1), (dict(res=2), 1),
+BAD = [(dict(T=-1), 1), (dict(T=1 << 22), 2), (dict(H=0), 1), (dict(H=32769), 2), (dict(dtype=3), 1), (dict(res=2), 1),
        (dict(dtype=1, res=0), 1), (dict(post=2), 1), (dict(post=0), 1), (dict(per_token=2), 1), (dict(eps=0.0), 1),
        (dict(eps=float("nan")), 1), (dict(alpha=float("inf")), 1), (dict(w_pre=4097), 1), (dict(gate=4097), 1),
        (dict(dtype=1, res=1, w_post=4098), 1)]

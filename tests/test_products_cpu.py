@@ -27,7 +27,7 @@ def _gemm(L, g=None, x=P16, ldx=64, w=P16, ldw=64, sw=64 * 32, trans=0, N=32, K=
     return L.moeq_grouped_gemm(g or _g(), x, ldx, w, ldw, sw, trans, N, K, dt, y, ldy, ydt, None)
 
 
-BAD_GROUPS = [dict(E=0), dict(E=257), dict(P=-1), dict(T=-1), dict(k=0), dict(off=None), dict(pairs=None),
+BAD_GROUPS = [dict(T=0), dict(E=0), dict(E=257), dict(P=-1), dict(T=-1), dict(k=0), dict(off=None), dict(pairs=None),
               dict(off=4098), dict(pairs=4097)]
 
 
@@ -50,6 +50,14 @@ def test_groups_refused(L, bad):
 def test_grouped_gemm_refused(L, bad, status):
     assert _gemm(L, **bad) == status
     assert L.moeq_last_error()
+
+
+def test_too_many_rows(L):
+    p, n = P16, (1 << 29) + 1
+    g = _g(P=n, T=n)
+    assert _gemm(L, g) == 2 and L.moeq_grouped_wgrad(g, p, 32, p, 64, 32, 64, 0, p, 64, 2048, 1, None) == 2
+    assert L.moeq_gemm_i8(g, p, 64, p, p, 64, 2048, p, 32, 64, p, 32, 0, None) == 2
+    assert L.moeq_quantize_i8(p, 64, 1 << 22, 64, 0, p, 64, p, None) == 2
 
 
 def test_null_groups(L):
@@ -79,12 +87,12 @@ def test_i8_refused(L):
     for bad in (dict(x=None), dict(sx=None), dict(w=None), dict(sw=None), dict(y=None), dict(ldx=63), dict(ldw=63),
                 dict(ldy=31), dict(ydt=3), dict(sx=4098), dict(sw=4097), dict(N=0), dict(K=0)):
         assert call(**bad) == 1, bad
-    assert call(K=131073, ldx=1 << 18, ldw=1 << 18) == 2       # the sum could pass 32 bits
+    assert call(K=131072, ldx=1 << 18, ldw=1 << 18) == 2       # the sum could pass 32 bits
     p = P16
     n = ctypes.c_size_t(0)
     assert L.moeq_linear_i8_workspace_size(4, 65, ctypes.byref(n)) == 0 and n.value == 4 * (128 + 4)
     assert L.moeq_linear_i8_workspace_size(-1, 65, ctypes.byref(n)) == 1
-    assert L.moeq_linear_i8_workspace_size(1, 131073, ctypes.byref(n)) == 2
+    assert L.moeq_linear_i8_workspace_size(1, 131072, ctypes.byref(n)) == 2
 
     def lin(ws=p, n=4 * (128 + 4), dt=0):
         return L.moeq_linear_i8(_g(), p, 65, dt, p, 65, 4096, p, 32, 65, p, 32, 0, ws, n, None)
