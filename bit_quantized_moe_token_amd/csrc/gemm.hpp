@@ -158,7 +158,9 @@ __device__ __forceinline__ bool find_tile(const GemmArgs &a, int BI, Tile *t) {
       t->row = l + jt * BJ;
       t->rows = h - t->row;
       t->i0 = in / width * BI;
-      return true;
+      // (offsets that do not ascend can make the counts above overflow: such
+      // a tile is none)
+      return (uint32_t)jt < (uint32_t)n && (uint32_t)t->i0 < (uint32_t)a.ni;
     }
   }
   return false;
@@ -301,6 +303,10 @@ struct Operand {
     return 16 * ((o % (2 * R)) / 16 ^ (2 * rmaj_swz(o / (2 * R))));
   }
 
+  // The range check is by dword and wants a dword whole: the one that holds
+  // the last element of an odd row counts in full.
+  __device__ __forceinline__ uint32_t range_width() const { return ((uint32_t)width + 3u) & ~3u; }
+
   // r contiguous: row x of the tile starts `stride` bytes times index(x)
   // (negative: a row of zeros) behind `from`; `last` the largest index
   template <class Index>
@@ -329,7 +335,7 @@ struct Operand {
   // r as row index: rows given stage by stage
   __device__ __forceinline__ void gather(const uint8_t *from, int64_t stride, int64_t last, int n_r, int row_bytes) {
     cols(from, stride, n_r, row_bytes);
-    if constexpr (DMA) rs = raw_rsrc(base, (uint32_t)(last * stride + width));
+    if constexpr (DMA) rs = raw_rsrc(base, (uint32_t)(last * stride + range_width()));
   }
 
   // DMA: block i of stage t into the tile at `dst` (stages behind the last:
@@ -339,7 +345,7 @@ struct Operand {
   }
   __device__ __forceinline__ void dma_cols(int i, int t, uint8_t *dst) const {
     const int left = std::min(kStageRows, nr - t * kStageRows);
-    const i32x4 r = raw_rsrc(base + (int64_t)t * kStageRows * ld, left > 0 ? (uint32_t)(left - 1) * (uint32_t)ld + (uint32_t)width : 0u);
+    const i32x4 r = raw_rsrc(base + (int64_t)t * kStageRows * ld, left > 0 ? (uint32_t)(left - 1) * (uint32_t)ld + range_width() : 0u);
     lds_dma_raw<16>(r, voff[i], 0, dst + block(i) * 1024);
   }
   __device__ __forceinline__ void dma_gather(int i, int src, uint8_t *dst) const {

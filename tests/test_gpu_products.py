@@ -75,21 +75,23 @@ SHAPES = [
     ([1] * 200 + [0] * 56, 2, 64, 64),
     ([700], 1, 1030, 258),
     ([33, 5], 2, 72, 2000),
-    ([1100, 3, 900, 0], 2, 136, 6664),      # enough tiles for the largest ones
+    ([1100, 3, 900, 0], 2, 144, 6664),      # enough tiles for the largest ones
     ([9, 9, 9], 1, 40, 33),
     ([50, 0, 70, 33], 1, 2056, 2104),       # and in the matrices' gradient
     ([600, 2, 811], 2, 200, 6300),
-    # each tile of the aligned and, at odd indices, of the unaligned path; rows
-    # of 4096 bytes and more take longer rings
-    ([90] * 15 + [91], 2, 136, 1000),
+    # each tile of the aligned and, at odd indices, of the unaligned path;
+    # long rows and few tiles take longer rings
+    ([90] * 15 + [91], 2, 144, 2500),
     ([90] * 15 + [91], 2, 135, 1001),
-    ([50] * 16, 2, 136, 1000),
+    ([50] * 16, 2, 144, 2500),
     ([50] * 16, 2, 133, 1003),
     ([90] * 16, 2, 2048, 1000),
     ([7, 0, 3], 1, 2100, 50),
     ([50] * 16, 2, 2048, 1000),
     ([3] * 5, 1, 77, 130),
     ([3, 9, 1], 2, 4096, 200),
+    ([1, 2], 1, 19, 70),
+    ([3] * 60, 1, 80, 600),
 ]
 
 
@@ -147,6 +149,42 @@ def test_grouped_wgrad(i, dtype):
     _check(dw, ref, n * 2.0 ** -23 * mag + _round_tol(ref, out_dtype), SHAPES[i])
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("counts,K,N", [([70, 0, 9], 72, 133), ([90] * 16, 88, 1003), ([700, 300], 104, 6661), ([3], 8, 1)])
+def test_padded_rows(counts, K, N, dtype):
+    """Rows that start at multiples of 16 bytes and end within one, NaN
+    between them, in a tensor that ends with its last row."""
+    from bit_quantized_moe_token_amd import moeq
+    rng = np.random.default_rng(N)
+    E, P = len(counts), sum(counts)
+    pad = lambda n: (n + 7) // 8 * 8 + 8
+
+    def rows(*shape):
+        ld, count = pad(shape[-1]), int(np.prod(shape[:-1]))
+        buf = torch.full(((count - 1) * ld + shape[-1],), float("nan"), dtype=dtype, device="cuda")
+        strides = (shape[-2] * ld, ld, 1) if len(shape) == 3 else (ld, 1)
+        return buf.as_strided(shape, strides).copy_(torch.from_numpy(rng.standard_normal(shape)).to(dtype))
+
+    off = torch.from_numpy(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)).cuda()
+    src = np.arange(P)
+    zero = np.zeros((P, N))
+    # the rows' gradient: w [E, K, N] with N no multiple of 8
+    x, w = rows(P, K), rows(E, K, N)
+    y = moeq.grouped_gemm(x, w, off, trans=True)
+    wn = _np(w).swapaxes(1, 2)
+    ref = products.grouped(_np(x), wn, off.cpu().numpy(), src, zero)
+    mag = products.grouped(np.abs(_np(x)), np.abs(wn), off.cpu().numpy(), src, zero)
+    _check(y, ref, K * 2.0 ** -23 * mag + _round_tol(ref, dtype), "trans")
+    # the matrices' gradient: dy [P, N]
+    dy = rows(P, N)
+    for a, b, what in ((dy, x, "wgrad"), (x, dy, "wgrad, the other way")):
+        dw = moeq.grouped_wgrad(a, b, off)
+        ref = products.wgrad(_np(a), _np(b), off.cpu().numpy(), src)
+        mag = products.wgrad(np.abs(_np(a)), np.abs(_np(b)), off.cpu().numpy(), src)
+        n = np.asarray(counts, dtype=np.float64)[:, None, None]
+        _check(dw, ref, n * 2.0 ** -23 * mag + _round_tol(ref, F32), what)
+
+
 def test_grouped_without_pairs_and_bad_pairs():
     """Without pairs row r reads row r; a pair outside the source rows reads
     zeros; offsets outside [0, P] count as its ends."""
@@ -155,6 +193,9 @@ def test_grouped_without_pairs_and_bad_pairs():
     x, w = _rows(rng, (50, 72), F16), _rows(rng, (2, 24, 72), F16)
     off = torch.tensor([-4, 20, 90], dtype=torch.int32).cuda()
     y = moeq.grouped_gemm(x, w, off, out_dtype=F32)
+    for wild in ([0, 50, 0], [50, 0, 50], [2147483647, -2147483648, 2147483647]):     # nothing to hold them to but bounds
+        moeq.grouped_gemm(x, w, torch.tensor(wild, dtype=torch.int32).cuda())
+        moeq.grouped_wgrad(x, x, torch.tensor(wild, dtype=torch.int32).cuda())
     ref = products.grouped(_np(x), _np(w), [0, 20, 50], np.arange(50), np.zeros((50, 24)))
     mag = products.grouped(np.abs(_np(x)), np.abs(_np(w)), [0, 20, 50], np.arange(50), np.zeros((50, 24)))
     _check(y, ref, 72 * 2.0 ** -23 * mag + _round_tol(ref, F32), "no pairs")
@@ -270,18 +311,72 @@ def test_i8(i, dtype):
 
 
 def test_i8_sum_is_exact_at_its_longest():
-    """The integer sum of 131072 products of 127 x 127 is exact (and beyond
-    it refused)."""
+    """The integer sum of 131071 products of -128 x -128 and of 127 x -127 is
+    exact (longer rows are refused)."""
     from bit_quantized_moe_token_amd import moeq
-    K = 131072
-    xq = torch.full((2, K), 127, dtype=torch.int8, device="cuda")
-    wq = torch.full((17, K), 127, dtype=torch.int8, device="cuda")
-    wq[1] = -127
+    K = 131071
+    xq = torch.full((2, K), -128, dtype=torch.int8, device="cuda")
+    wq = torch.full((17, K), -128, dtype=torch.int8, device="cuda")
+    xq[1], wq[1] = 127, -127
     one, ones = torch.ones(2, device="cuda"), torch.ones(17, device="cuda")
     y = moeq.gemm_i8(xq, one, wq, ones, out_dtype=F32)
-    want = torch.full((2, 17), float(np.float32(127 * 127 * K)))
-    want[:, 1] *= -1
-    assert torch.equal(y.cpu(), want)
+    want = torch.tensor([-128, 127], dtype=torch.float64)[:, None] * wq[:, 0].cpu().double()[None] * K
+    assert torch.equal(y.cpu(), want.float())
+
+
+def test_subnormal_inputs():
+    """Subnormal fp16 and bf16 values keep their value in the products."""
+    from bit_quantized_moe_token_amd import moeq
+    off = torch.tensor([0, 4], dtype=torch.int32).cuda()
+    for dtype, small in ((F16, 2.0 ** -24), (BF16, 2.0 ** -130)):
+        x = (torch.arange(1, 5, device="cuda")[:, None].double() * small).to(dtype).expand(4, 64).contiguous()
+        w = torch.full((1, 32, 64), 2.0 ** 14, dtype=dtype, device="cuda")
+        y = moeq.grouped_gemm(x, w, off, out_dtype=F32)
+        assert torch.equal(y.double(), (x[:, :1].double() * 2.0 ** 20).expand(4, 32))
+        dw = moeq.grouped_wgrad(w[0].T[:4].contiguous(), x, off)
+        assert torch.equal(dw.double(), x.double().sum(0).expand(1, 32, 64) * 2.0 ** 14)
+
+
+def test_offsets_beyond_32_bits():
+    """Source rows, matrices and outputs that lie more than 2^32 bytes into
+    their tensors."""
+    from bit_quantized_moe_token_amd import moeq
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rand = lambda *s: torch.randn(s, generator=g, device="cuda").half()
+
+    def check(y, x, w):
+        ref, mag = x.double() @ w.double().T, x.double().abs() @ w.double().abs().T
+        _check(y, ref.cpu().numpy(), (x.shape[1] * 2.0 ** -23 * mag).cpu().numpy() + _round_tol(ref.cpu().numpy(), F16), "far")
+
+    T, K, N = 1100000, 2048, 96                      # x: 4.5 GB
+    x = torch.zeros(T, K, dtype=F16, device="cuda")
+    rows = torch.tensor([0, 5, T // 2, T - 2, T - 1], device="cuda")
+    x[rows] = rand(5, K)
+    w = rand(1, N, K)
+    off = torch.tensor([0, 5], dtype=torch.int32).cuda()
+    check(moeq.grouped_gemm(x, w, off, pairs=rows.int(), k=1), x[rows], w[0])
+    dy = rand(5, N)
+    dw = moeq.grouped_wgrad(dy, x, off, pairs=rows.int(), k=1)
+    ref = dy.double().T @ x[rows].double()
+    _check(dw[0], ref.cpu().numpy(), (5 * 2.0 ** -23 * (dy.double().abs().T @ x[rows].double().abs())).cpu().numpy() +
+           _round_tol(ref.cpu().numpy(), F32), "far wgrad")
+    q, s = moeq.quantize_i8(x)
+    qr, sr = products.code_i8(x[rows].float().cpu().numpy())
+    assert np.array_equal(q[rows].cpu().numpy(), qr) and np.array_equal(s[rows].cpu().numpy(), sr)
+    del x, q, s
+    E, N, K = 5, 65536, 8192                         # w: 5.4 GB
+    w = torch.zeros(E, N, K, dtype=F16, device="cuda")
+    w[E - 1, N - 300:] = rand(300, K)
+    x = rand(3, K)
+    y = moeq.grouped_gemm(x, w, torch.tensor([0, 0, 0, 0, 0, 3], dtype=torch.int32).cuda())
+    check(y[:, N - 300:], x, w[E - 1, N - 300:])
+    assert not y[:, :N - 300].any()
+    del w
+    P, N, K = 300000, 8192, 16                       # y: 4.9 GB
+    x, w = rand(P, K), rand(1, N, K)
+    y = moeq.grouped_gemm(x, w, torch.tensor([0, P], dtype=torch.int32).cuda())
+    check(y[P - 40:, 4000:4100], x[P - 40:], w[0, 4000:4100])
+    check(y[:40, 4000:4100], x[:40], w[0, 4000:4100])
 
 
 def test_graph_stream_and_repeat():
