@@ -52,14 +52,16 @@ bool dma_ok(const GemmArgs &a) {
 // exist and spread few rows over more CUs (one matrix of 4096 x 4096: 200
 // rows 64 x 32 22 us, 128 x 128 30; 64 rows of each expert above: 128 x 64
 // 176, 128 x 128 183, 256 x 256 220).  Small tiles take a longer ring where
-// rows are long, so that a workgroup alone on its CU does not wait for every
-// stage (one row, one matrix of 4096 x 4096: 16 us with four stages, 30 with
-// two); for short rows more workgroups per CU are better (128 experts of 512
-// x 768, one row each: 20 and 18 us).
+// rows are long or workgroups few, so that a workgroup does not wait for
+// every stage (one row, one matrix of 4096 x 4096: 16 us with four stages, 30
+// with two; 16 experts of 120 rows, K 1000, N 760: 10.3 us with three, 12.5
+// with two); else more workgroups per CU are better (128 experts of 512 x 768,
+// one row each: 20 us with four, 18 with two).
 // Through registers (rows that are not 16-byte aligned) the largest tile has
 // no room: 128 x 128 at most.
 constexpr int kFewTiles = 200;
 constexpr int kLongRow = 4096;     // bytes
+constexpr int kFewPerCu = 512;     // workgroups: two per CU
 
 template <int TY, int MODE>
 moeq_status launch_mode(const GemmArgs &a, hipStream_t s, const char *name) {
@@ -80,18 +82,19 @@ moeq_status launch_mode(const GemmArgs &a, hipStream_t s, const char *name) {
     return launch_tiles<TY, MODE, 128, 128, 4, 2, 2, 2, true>(a, s, name);
   } else {
     constexpr int BI = MODE == kRows ? 128 : 64;       // (transposing reads need 128 columns)
-    const bool deep = (int64_t)a.nr * Elt<TY>::size >= kLongRow;
+    const bool longrow = (int64_t)a.nr * Elt<TY>::size >= kLongRow;
+    const auto deep = [&](int bi, int bj) { return longrow || tile_grid<MODE>(a, bi, bj) < kFewPerCu; };
     if (rows >= 160 && tile_grid<MODE>(a, 256, 256) >= kFewTiles)
       return launch_tiles<TY, MODE, 256, 256, 2, 4, 3, 2, true>(a, s, name);
     if (wide) {
-      if (deep) return launch_tiles<TY, MODE, 128, 128, 4, 2, 3, 3, true>(a, s, name);
+      if (deep(128, 128)) return launch_tiles<TY, MODE, 128, 128, 4, 2, 3, 3, true>(a, s, name);
       return launch_tiles<TY, MODE, 128, 128, 4, 2, 2, 2, true>(a, s, name);
     }
     if (rows >= 40 && tile_grid<MODE>(a, 128, 64) >= kFewTiles) {
-      if (deep) return launch_tiles<TY, MODE, 128, 64, 4, 2, 3, 3, true>(a, s, name);
+      if (deep(128, 64)) return launch_tiles<TY, MODE, 128, 64, 4, 2, 3, 3, true>(a, s, name);
       return launch_tiles<TY, MODE, 128, 64, 4, 2, 2, 2, true>(a, s, name);
     }
-    if (deep) return launch_tiles<TY, MODE, BI, 32, 4, 1, 4, 4, true>(a, s, name);
+    if (deep(BI, 32)) return launch_tiles<TY, MODE, BI, 32, 4, 1, 4, 4, true>(a, s, name);
     return launch_tiles<TY, MODE, BI, 32, 4, 1, 2, 2, true>(a, s, name);
   }
 }
