@@ -407,6 +407,59 @@ __device__ __forceinline__ void store4(const GemmArgs &a, int64_t o, f32x4 v, in
   }
 }
 
+// Tiles of the matrices' gradient take a time that depends on the expert's
+// rows.  Each XCD gets short runs of tiles (in bands of kBand i tiles) of all
+// the experts in turn, not one run of whole experts, and the experts with the
+// most rows come first, so that no long tile starts last.  A run has up to 8
+// tiles of 256 x 256, as many outputs of smaller ones, and as few as leave
+// every XCD the same number of runs.  (64 experts of 1408 x 2048, 24576 rows,
+// bf16, fp32 out: equal rows 309 us, runs of whole experts 298; shares falling
+// with the root of the rank 336, whole experts 392, runs of 32 tiles 354;
+// falling with the power 1.1 352, 605 and 462.)
+__host__ __device__ constexpr int mats_run(int all, int BI, int BJ) {
+  const int most = 8 * (256 * 256 / (BI * BJ));
+  const int rounds = (all + 8 * most - 1) / (8 * most);
+  return (all + 8 * rounds - 1) / (8 * rounds);
+}
+
+// The expert at place n of the order by rows, to a power of two times the
+// mean (more exactly, E compares per lane would take longer than they save);
+// its first row and its rows.
+__device__ __forceinline__ int nth_expert(const GemmArgs &a, int n, int *row, int *rows) {
+  constexpr int NB = kMaxExperts / kWave;     // experts per lane
+  const int lane = threadIdx.x & 63, mean = a.P / a.E + 1;
+  int lo[NB], len[NB], cls[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    lo[b] = len[b] = 0;
+    cls[b] = -1;
+    const int e = b * kWave + lane;
+    if (e >= a.E) continue;
+    int hi;
+    expert_rows(a, e, &lo[b], &hi);
+    len[b] = hi - lo[b];
+    cls[b] = (len[b] >= mean / 2) + (len[b] >= mean) + (len[b] >= 2ll * mean) + (len[b] >= 4ll * mean);
+  }
+  for (int c = 4; c >= 0; --c) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      if (b * kWave >= a.E) break;
+      const uint64_t in = __ballot(cls[b] == c);
+      const int count = __builtin_popcountll(in);
+      if (n < count) {
+        const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(in >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)in, 0));
+        const int src = __builtin_ctzll(__ballot(cls[b] == c && before == n));
+        *row = __builtin_amdgcn_readlane(lo[b], src);
+        *rows = __builtin_amdgcn_readlane(len[b], src);
+        return b * kWave + src;
+      }
+      n -= count;
+    }
+  }
+  *row = *rows = 0;                            // (not reached: every expert is in a class)
+  return 0;
+}
+
 // Output tile of a workgroup, the extent of r and, for the matrices'
 // gradient, the first j; all in scalar registers.
 template <int MODE, int BI, int BJ>
@@ -415,16 +468,14 @@ __device__ __forceinline__ bool pick_tile(const GemmArgs &a, Tile *t, int *nr, i
   int r = a.nr, j = 0;
   if constexpr (MODE == kMats) {
     const int n_it = (a.ni + BI - 1) / BI, n_jt = (a.nj + BJ - 1) / BJ, all = a.E * n_it * n_jt;
-    const int per = (all + 7) >> 3, idx = (int)blockIdx.x >> 3, L = ((int)blockIdx.x & 7) * per + idx;
-    if (idx >= per || L >= all) return false;
-    v.e = L / (n_it * n_jt);
-    const int in = L - v.e * n_it * n_jt;
-    j = in / n_it * BJ;
-    v.i0 = in % n_it * BI;
-    int lo, hi;
-    expert_rows(a, v.e, &lo, &hi);
-    v.row = lo;
-    r = hi - lo;
+    const int per = mats_run(all, BI, BJ), xcd = (int)blockIdx.x & 7, idx = (int)blockIdx.x >> 3;
+    const int L = (idx / per * 8 + xcd) * per + idx % per;
+    if (L >= all) return false;
+    const int nth = L / (n_it * n_jt), local = L - nth * n_it * n_jt, band = local / (kBand * n_jt);
+    const int in = local - band * kBand * n_jt, width = std::min(kBand, n_it - band * kBand);
+    j = in / width * BJ;
+    v.i0 = (band * kBand + in % width) * BI;
+    v.e = nth_expert(a, nth, &v.row, &r);
     v.rows = a.nj - j;
   } else {
     if (!find_tile<BJ>(a, BI, &v)) return false;

@@ -8,15 +8,22 @@ moeq_status launch_gemm_f16(const GemmArgs &a, GemmMode mode, hipStream_t s);
 moeq_status launch_gemm_bf16(const GemmArgs &a, GemmMode mode, hipStream_t s);
 moeq_status launch_gemm_i8(const GemmArgs &a, hipStream_t s);
 
+constexpr int64_t kMaxGrid = 0x7fffff00 / 512;   // (threads of a launch fit 32 bits)
+
 // Workgroups of a launch with tiles of BI x BJ: row tiles are bounded by one
 // partial tile per expert that has rows.
 template <int MODE>
 int64_t tile_grid(const GemmArgs &a, int BI, int BJ) {
   const int64_t n_it = (a.ni + BI - 1) / BI;
-  const int64_t n_jt = MODE == kMats ? (int64_t)a.E * ((a.nj + BJ - 1) / BJ) : a.P / BJ + std::min(a.E, a.P);
+  if constexpr (MODE == kMats) {                 // whole rounds of runs on the 8 XCDs
+    const int64_t all = n_it * ((a.nj + BJ - 1) / BJ) * a.E;
+    if (all > kMaxGrid) return all;
+    const int run = 8 * mats_run((int)all, BI, BJ);
+    return (all + run - 1) / run * run;
+  }
+  const int64_t n_jt = a.P / BJ + std::min(a.E, a.P);
   return (n_it * n_jt + 7) / 8 * 8;
 }
-constexpr int64_t kMaxGrid = 0x7fffff00 / 512;   // (threads of a launch fit 32 bits)
 
 template <int TY, int MODE, int BI, int BJ, int WI, int WJ, int RI, int RJ, bool DMA>
 moeq_status launch_tiles(const GemmArgs &a, hipStream_t s, const char *name) {

@@ -149,6 +149,24 @@ def test_grouped_wgrad(i, dtype):
     _check(dw, ref, n * 2.0 ** -23 * mag + _round_tol(ref, out_dtype), SHAPES[i])
 
 
+@pytest.mark.parametrize("E,K,N,ld", [(200, 264, 392, 0), (256, 40, 300, 0), (3, 2600, 1112, 0), (90, 130, 1200, 1), (1, 2200, 2200, 0)])
+def test_wgrad_of_uneven_experts(E, K, N, ld):
+    """Experts in every class of rows, more than a lane's worth of them, more
+    tiles than a round of runs, more columns of tiles than a band."""
+    from bit_quantized_moe_token_amd import moeq
+    rng = np.random.default_rng(E)
+    counts = rng.choice([0, 1, 7, 40, 130, 500], size=E, p=[0.2, 0.2, 0.2, 0.2, 0.15, 0.05]) if E > 3 else [330, 0, 21][:E]
+    off, pairs = _routing(rng, counts, 2, 300, before=3, behind=2)
+    x = _rows(rng, (300, K), BF16, ld=K + ld)
+    dy = _rows(rng, (len(pairs), N), BF16, ld=N + ld)
+    dw = moeq.grouped_wgrad(dy, x, torch.from_numpy(off).cuda(), pairs=torch.from_numpy(pairs).cuda(), k=2, out_dtype=F32)
+    src = products.source_rows(len(pairs), 300, pairs, 2)
+    ref = products.wgrad(_np(dy), _np(x), off, src)
+    mag = products.wgrad(np.abs(_np(dy)), np.abs(_np(x)), off, src)
+    n = np.asarray(counts, dtype=np.float64)[:, None, None]
+    _check(dw, ref, n * 2.0 ** -23 * mag + _round_tol(ref, F32), (E, K, N))
+
+
 @pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
 @pytest.mark.parametrize("counts,K,N", [([70, 0, 9], 72, 133), ([90] * 16, 88, 1003), ([700, 300], 104, 6661), ([3], 8, 1)])
 def test_padded_rows(counts, K, N, dtype):
