@@ -64,20 +64,28 @@ bool dma_ok(const GemmArgs &a) {
 // with two; 16 experts of 120 rows, K 1000, N 760: 10.3 us with three, 12.5
 // with two); else more workgroups per CU are better (128 experts of 512 x 768,
 // one row each: 20 us with four, 18 with two).
+// A few rows on fewer workgroups than CUs take 32 x 16 outputs each and a
+// ring of eight (one row, bf16, a matrix of 4096 x 4096: 19.0 -> 13.9 us, of
+// 4096 x 14336 58.5 -> 39.8, rows of no alignment, 4097 x 4097: 53 -> 46);
+// with more workgroups it is slower (8 experts of 14336 x 4096, 4 rows each:
+// 153 -> 163 us).
 // Through registers (rows that are not 16-byte aligned) the largest tile has
 // no room: 128 x 128 at most.
 constexpr int kFewTiles = 200;
 constexpr int kLongRow = 4096;     // bytes
 constexpr int kFewPerCu = 512;     // workgroups: two per CU
+constexpr int kCus = 256;
 
 template <int TY, int MODE>
 moeq_status launch_mode(const GemmArgs &a, hipStream_t s, const char *name) {
   const int rows = a.P / a.E + (a.P % a.E != 0);       // mean rows per expert
   const bool wide = MODE == kMats || (rows >= 80 && tile_grid<MODE>(a, 128, 128) >= kFewTiles);
+  const bool tiny = MODE == kFwd && rows <= 16 && tile_grid<MODE>(a, 64, 32) < kCus;
   if (!dma_ok<TY, MODE>(a)) {
     if (wide) return launch_tiles<TY, MODE, 128, 128, 4, 2, 2, 2, false>(a, s, name);
     if constexpr (MODE == kRows) return launch_tiles<TY, MODE, 128, 64, 4, 2, 2, 2, false>(a, s, name);
     if constexpr (MODE == kFwd) {
+      if (tiny) return launch_tiles<TY, MODE, 32, 16, 2, 1, 2, 2, false>(a, s, name);
       if (rows >= 16 && tile_grid<MODE>(a, 128, 64) >= kFewTiles) return launch_tiles<TY, MODE, 128, 64, 4, 2, 2, 2, false>(a, s, name);
       return launch_tiles<TY, MODE, 64, 32, 4, 1, 2, 2, false>(a, s, name);
     }
@@ -100,6 +108,9 @@ moeq_status launch_mode(const GemmArgs &a, hipStream_t s, const char *name) {
     if (rows >= 40 && tile_grid<MODE>(a, 128, 64) >= kFewTiles) {
       if (deep(128, 64)) return launch_tiles<TY, MODE, 128, 64, 4, 2, 3, 3, true>(a, s, name);
       return launch_tiles<TY, MODE, 128, 64, 4, 2, 2, 2, true>(a, s, name);
+    }
+    if constexpr (MODE == kFwd) {
+      if (tiny) return launch_tiles<TY, MODE, 32, 16, 2, 1, 8, 8, true>(a, s, name);
     }
     if (deep(BI, 32)) return launch_tiles<TY, MODE, BI, 32, 4, 1, 4, 4, true>(a, s, name);
     return launch_tiles<TY, MODE, BI, 32, 4, 1, 2, 2, true>(a, s, name);
