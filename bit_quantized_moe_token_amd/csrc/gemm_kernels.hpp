@@ -60,15 +60,15 @@ bool dma_ok(const GemmArgs &a) {
 // rows 64 x 32 22 us, 128 x 128 30; 64 rows of each expert above: 128 x 64
 // 176, 128 x 128 183, 256 x 256 220).  Small tiles take a longer ring where
 // rows are long or workgroups few, so that a workgroup does not wait for
-// every stage (one row, one matrix of 4096 x 4096: 16 us with four stages, 30
-// with two; 16 experts of 120 rows, K 1000, N 760: 10.3 us with three, 12.5
-// with two); else more workgroups per CU are better (128 experts of 512 x 768,
-// one row each: 20 us with four, 18 with two).
-// A few rows on fewer workgroups than CUs take 32 x 16 outputs each and a
-// ring of eight (one row, bf16, a matrix of 4096 x 4096: 19.0 -> 13.9 us, of
-// 4096 x 14336 58.5 -> 39.8, rows of no alignment, 4097 x 4097: 53 -> 46);
-// with more workgroups it is slower (8 experts of 14336 x 4096, 4 rows each:
-// 153 -> 163 us).
+// every stage (8 experts of 14336 x 4096, 4 rows each: 153 us with four
+// stages, 203 with two; 16 experts of 120 rows, K 1000, N 760: 10.3 us with
+// three, 12.5 with two); else more workgroups per CU are better (128 experts
+// of 512 x 768, one row each: 20 us with four, 18 with two).
+// Where 64 x 32 gives fewer workgroups than CUs, tiles of 32 x 16 and a ring
+// of eight (bf16, one row, a matrix of 4096 x 4096: 19.0 -> 13.9 us, of 4096 x
+// 14336 58.5 -> 39.8; 64 rows, 4096 x 4096 19.5 -> 17.4; rows of no alignment,
+// 4097 x 4097, one 53 -> 46, 32 58 -> 48); with more workgroups it is slower
+// (8 experts of 14336 x 4096, 4 rows each: 153 -> 163 us).
 // Through registers (rows that are not 16-byte aligned) the largest tile has
 // no room: 128 x 128 at most.
 constexpr int kFewTiles = 200;
@@ -80,7 +80,7 @@ template <int TY, int MODE>
 moeq_status launch_mode(const GemmArgs &a, hipStream_t s, const char *name) {
   const int rows = a.P / a.E + (a.P % a.E != 0);       // mean rows per expert
   const bool wide = MODE == kMats || (rows >= 80 && tile_grid<MODE>(a, 128, 128) >= kFewTiles);
-  const bool tiny = MODE == kFwd && rows <= 16 && tile_grid<MODE>(a, 64, 32) < kCus;
+  const bool tiny = MODE == kFwd && tile_grid<MODE>(a, 64, 32) < kCus;
   if (!dma_ok<TY, MODE>(a)) {
     if (wide) return launch_tiles<TY, MODE, 128, 128, 4, 2, 2, 2, false>(a, s, name);
     if constexpr (MODE == kRows) return launch_tiles<TY, MODE, 128, 64, 4, 2, 2, 2, false>(a, s, name);

@@ -92,6 +92,8 @@ SHAPES = [
     ([3, 9, 1], 2, 4096, 200),
     ([1, 2], 1, 19, 70),
     ([3] * 60, 1, 80, 600),
+    ([20] * 40, 2, 99, 300),
+    ([20] * 40, 2, 96, 300),
 ]
 
 
