@@ -232,3 +232,28 @@ def test_graph_and_stream():
         other = step()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(other, eager))
+
+
+def test_rows_beyond_32_bit_offsets():
+    """Rows whose elements lie behind 2^31 come out as in a call of their own
+    (of enough rows for the same variant of the kernel)."""
+    from bit_quantized_moe_token_amd import moeq
+    H, T = 8192, 2 ** 18 + 40
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    few = lambda: torch.randn((64, H), generator=gen, device="cuda").to(BF16)
+    many = lambda t: t.repeat(T // 64 + 1, 1)[:T].contiguous()
+    res, y, gate, d_n = few(), few(), few(), few()
+    w = (1 + 0.2 * torch.randn(H, generator=gen, device="cuda")).to(BF16)
+    last = [(T - 1 - i) % 64 for i in range(300)]
+    r, n = moeq.block_norm(many(res), many(y), w_pre=w, w_post=w, gate=many(gate), alpha=0.5)
+    r0, n0 = moeq.block_norm(res[last], y[last], w_pre=w, w_post=w, gate=gate[last], alpha=0.5)
+    assert torch.equal(r[-300:].flip(0), r0) and torch.equal(n[-300:].flip(0), n0)
+    del n
+    g = moeq.block_norm_grad(r, many(d_n), many(y), w_pre=w, w_post=w, gate=many(gate), alpha=0.5)
+    g0 = moeq.block_norm_grad(r0, d_n[last], y[last], w_pre=w, w_post=w, gate=gate[last], alpha=0.5)
+    for name in ("d_residual", "d_y", "d_gate"):
+        assert torch.equal(g[name][-300:].flip(0), g0[name]), name
+    del g
+    q, s = moeq.quantize_i8(r)
+    q0, s0 = moeq.quantize_i8(r0)
+    assert torch.equal(q[-300:].flip(0), q0) and torch.equal(s[-300:].flip(0), s0)
