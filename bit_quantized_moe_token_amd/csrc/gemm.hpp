@@ -680,9 +680,10 @@ __global__ void __launch_bounds__(64 * WI * WJ, 1) gemm_tile_kernel(GemmArgs a) 
     for (int j = 0; j < TJ; ++j) y[0][j] = fj.read(gemm_lds, j, 0);
     // The MFMAs of a half stage (set C), with the reads of the next one
     // (half 1 - C of the stage at sti, stj) between them, in kSeg parts.  In the
-    // second half a part starts with its share of the DMA operations (all at once after the barrier they hold the waves up: a CU
-    // takes one in about 16 cycles).  The last part has no reads, so that its
-    // MFMAs cover their latency.
+    // second half a part starts with its share of the DMA operations (all at
+    // once after the barrier they hold the waves up: a CU takes one in about
+    // 16 cycles).  The last part has no reads, so that its MFMAs cover their
+    // latency.
     auto half = [&](auto c, const uint8_t *sti, const uint8_t *stj, int k, uint8_t *toi, uint8_t *toj) {
       constexpr int C = decltype(c)::value, N = 1 - C;
       constexpr int kSeg = TI < 4 ? TI : 4, kRd = kSeg > 1 ? kSeg - 1 : 1, IS = TI / kSeg;

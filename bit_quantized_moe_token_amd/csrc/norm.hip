@@ -16,10 +16,10 @@
 // Bound by memory: every row is read once and kept in registers (as stored)
 // through the row's two reductions (16384 rows of 4096, bf16 beside an fp32
 // residual: 150 us, 5.4 TB/s; gradients of 8192 rows of 4096 in bf16 with a
-// gate per token: 123 us and 5 for the column sums, 4.2 TB/s).  Sums, statistics and gradients are
-// fp32; the squares' sums need the norms 1 / a and 1 / b anyway, so the
-// backward pass recomputes them from the rows that it reads in any case and
-// needs no saved statistics.
+// gate per token: 123 us and 5 for the column sums, 4.2 TB/s).  Sums,
+// statistics and gradients are fp32; the backward pass reads the rows in any
+// case, so it recomputes 1 / a and 1 / b from them and needs no saved
+// statistics.
 #include "vec8.hpp"
 
 namespace moeq {
