@@ -276,6 +276,18 @@ __device__ __forceinline__ i32x4 raw_rsrc(const uint8_t *base, uint32_t bytes) {
 // addresses; a stage is loaded one stage before it is stored.
 constexpr uint32_t kNowhere = 0x80000000u;   // an offset behind every range used here
 
+// Offsets of the 16 bytes `piece` of stage t of a row `width` bytes long whose
+// lane offset is `row` (piece included): the lane's and the uniform one.  The
+// range check takes the uniform offset from the range, so that it must not
+// pass the range: a stage behind the row's end has none.
+struct StageOffsets {
+  uint32_t voff, soff;
+};
+__host__ __device__ constexpr StageOffsets stage_offsets(int t, int piece, int width, uint32_t row) {
+  const int at = t * kStageBytes;
+  return {piece < width - at ? row : kNowhere, at < width ? (uint32_t)at : 0u};
+}
+
 template <int ES, int R, int NW, bool RMAJ, bool DMA>
 struct Operand {
   static constexpr int NB = R * kStageBytes / (1024 * NW);
@@ -341,7 +353,8 @@ struct Operand {
   // DMA: block i of stage t into the tile at `dst` (stages behind the last:
   // zeros)
   __device__ __forceinline__ void dma_rows(int i, int t, uint8_t *dst) const {
-    lds_dma_raw<16>(rs, piece_of(i) < width - t * kStageBytes ? voff[i] : kNowhere, (uint32_t)t * kStageBytes, dst + block(i) * 1024);
+    const StageOffsets o = stage_offsets(t, piece_of(i), width, voff[i]);
+    lds_dma_raw<16>(rs, o.voff, o.soff, dst + block(i) * 1024);
   }
   __device__ __forceinline__ void dma_cols(int i, int t, uint8_t *dst) const {
     const int left = std::min(kStageRows, nr - t * kStageRows);
