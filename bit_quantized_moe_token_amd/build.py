@@ -26,16 +26,15 @@ CFLAGS = [
 ]
 
 
-# Per-source flags.  (-Wno-inline-asm: the products' DMA sets m0, which the
-# compiler reserves, and lists it as clobbered.)  The tiled kernels keep their MFMA accumulators in
+# Per-source flags.  The tiled kernels keep their MFMA accumulators in
 # ordinary VGPRs: with the accumulation-register form the allocator
 # permutes the loop-carried accumulators through copies on every K tile.
 FILE_FLAGS = {
     "tiled_gu.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     "tiled_dn.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
-    "gemm_f16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1", "-Wno-inline-asm"],
-    "gemm_bf16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1", "-Wno-inline-asm"],
-    "gemm_i8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1", "-Wno-inline-asm"],
+    "gemm_f16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    "gemm_bf16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    "gemm_i8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
 }
 
 

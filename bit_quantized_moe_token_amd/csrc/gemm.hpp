@@ -246,19 +246,19 @@ __device__ __forceinline__ const uint8_t *uniform(const uint8_t *p) {   // into 
 // unknown to the compiler (rs: the four words of the buffer resource): it
 // puts a wait for all transfers before every transposing LDS read
 // otherwise.  The kernel waits by count before the step that reads the
-// data; the instruction has no register output.  m0 holds the LDS address.
+// data; the instruction has no register output.  m0 holds the LDS address;
+// it is the compiler's to write, as an input of the asm, which changes no
+// register (saving m0 and giving it back within the asm cost 1%).
 // (s_nop 4: five wait states between a VALU write of a scalar register, as
-// v_readfirstlane makes for rs, and a memory instruction that reads it; the
-// compiler does not look into the asm for that.)
+// v_readfirstlane makes for rs, and a memory instruction that reads it; one
+// after a write of m0; the compiler does not look into the asm for either.)
 template <int SIZE>
 __device__ __forceinline__ void lds_dma_raw(i32x4 rs, uint32_t voff, uint32_t soff, const uint8_t *lds) {
   const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t *)lds;
   if constexpr (SIZE == 16)
-    asm volatile("s_mov_b32 m0, %3\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
-                 :: "v"(voff), "s"(rs), "s"(soff), "s"(at) : "m0", "memory");
+    asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" :: "v"(voff), "s"(rs), "s"(soff), "{m0}"(at) : "memory");
   else
-    asm volatile("s_mov_b32 m0, %3\n\ts_nop 4\n\tbuffer_load_dword %0, %1, %2 offen lds"
-                 :: "v"(voff), "s"(rs), "s"(soff), "s"(at) : "m0", "memory");
+    asm volatile("s_nop 4\n\tbuffer_load_dword %0, %1, %2 offen lds" :: "v"(voff), "s"(rs), "s"(soff), "{m0}"(at) : "memory");
 }
 __device__ __forceinline__ i32x4 raw_rsrc(const uint8_t *base, uint32_t bytes) {   // both uniform
   const uint64_t v = (uint64_t)uniform(base);
