@@ -60,13 +60,77 @@ __device__ __forceinline__ void row_sum(float *v, float *s, int buf) {
   }
 }
 
+// The largest of the NT threads' values, buf as above.
+template <int NT>
+__device__ __forceinline__ float row_top(float v, float *s, int buf) {
+#pragma unroll
+  for (int o = 32; o; o >>= 1) v = __builtin_fmaxf(v, __shfl_xor(v, o, kWave));
+  if constexpr (NT > 64) {
+    float *p = s + buf * 3 * 16;
+    if ((threadIdx.x & 63) == 0) p[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = p[0];
+#pragma unroll
+    for (int w = 1; w < NT / 64; ++w) v = __builtin_fmaxf(v, p[w]);
+  }
+  return v;
+}
+
+// mean(v^2) + eps in fp32 is as good as the sum of squares, which is exact to
+// its roundings between these.  Beyond them (rows of bf16 and fp32 values
+// around 2^64 and more; values that vanish when squared beside an eps as
+// small) the row is summed again, times row_unit.
+__device__ __forceinline__ bool plain_square(float q) { return q >= 0x1p-90f && q < __builtin_inff(); }
+
+// The power of two that brings the larger of a row's largest magnitude and
+// sqrt(eps) to between 1 and 2 (2^-127 for an infinite one): no square
+// overflows then, and what vanishes does not count beside 1.
+__device__ __forceinline__ float row_unit(float top, float eps) {
+  return __builtin_ldexpf(1.f, -std::min(ilogb_f32(__builtin_fmaxf(top, __builtin_sqrtf(eps))), 127));
+}
+
 // Threads per workgroup: a row's NT, or four waves of one row each.
 constexpr int norm_block(int NT) { return NT == 64 ? 256 : NT; }
+
+// 1 / sqrt(mean(v^2) + eps) of the row whose pieces the threads hold, zeros
+// behind its end, from this thread's sum of squares.  Uses buffers buf, 2 and
+// 3 of s.
+template <int NT, int TV, int CH>
+__device__ __forceinline__ float inverse_rms(const Oct<TV> (&v)[CH], float sum, float rh, float eps, float *s, int buf) {
+  float ss[1] = {sum};
+  row_sum<NT, 1>(ss, s, buf);
+  const float q = ss[0] * rh + eps;
+  if (__builtin_expect(plain_square(q), 1)) return 1.f / __builtin_sqrtf(q);
+  // (opaque: the compiler would share fp32 values of the row with the usual
+  // path, whose registers they would take)
+  float top = 0.f;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    Oct<TV> w = v[c];
+    w.opaque();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = __builtin_fmaxf(top, __builtin_fabsf(w[j]));
+  }
+  const float u = row_unit(row_top<NT>(top, s, 2), eps);
+  ss[0] = 0.f;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    Oct<TV> w = v[c];
+    w.opaque();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float x = w[j] * u;
+      ss[0] += x * x;
+    }
+  }
+  row_sum<NT, 1>(ss, s, 3);
+  return u / __builtin_sqrtf(ss[0] * rh + eps * u * u);
+}
 
 // Thread t of a row holds the pieces of eight elements t, t + NT, ...
 template <int TY, int TR, int NT, int CH>
 __global__ void __launch_bounds__(norm_block(NT)) block_norm_kernel(NormArgs a) {
-  __shared__ float s[2 * 3 * 16];
+  __shared__ float s[4 * 3 * 16];
   const int t = threadIdx.x % NT;
   const int64_t row = (int64_t)blockIdx.x * (norm_block(NT) / NT) + threadIdx.x / NT;
   if (row >= a.T) return;      // (whole waves, and only where no barrier follows)
@@ -81,15 +145,14 @@ __global__ void __launch_bounds__(norm_block(NT)) block_norm_kernel(NormArgs a) 
     if (a.y) x[c].load(a.y, at + i, a.H - i);
   }
   if (a.y) {
-    float ss[1] = {0.f};
+    float ss = 0.f, b = 1.f;
     if (a.post) {
 #pragma unroll
       for (int c = 0; c < CH; ++c)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss[0] += x[c][j] * x[c][j];
-      row_sum<NT, 1>(ss, s, 0);
+        for (int j = 0; j < 8; ++j) ss += x[c][j] * x[c][j];
+      b = inverse_rms<NT>(x, ss, rh, a.eps, s, 0);
     }
-    const float b = a.post ? 1.f / __builtin_sqrtf(ss[0] * rh + a.eps) : 1.f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int i = (c * NT + t) * 8;
@@ -108,15 +171,14 @@ __global__ void __launch_bounds__(norm_block(NT)) block_norm_kernel(NormArgs a) 
       r[c].store(a.res_out, at + i, a.H - i);
     }
   }
-  float ss[1] = {0.f};
+  float ss = 0.f;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int i = (c * NT + t) * 8;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss[0] += i + j < a.H ? r[c][j] * r[c][j] : 0.f;
+    for (int j = 0; j < 8; ++j) ss += i + j < a.H ? r[c][j] * r[c][j] : 0.f;
   }
-  row_sum<NT, 1>(ss, s, 1);
-  const float k = 1.f / __builtin_sqrtf(ss[0] * rh + a.eps);
+  const float k = inverse_rms<NT>(r, ss, rh, a.eps, s, 1);
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int i = (c * NT + t) * 8;

@@ -552,7 +552,9 @@ moeq_status moeq_linear_i8(const moeq_groups *g, const void *x, int64_t ldx, int
  *   p  = w_post * y / sqrt(mean(y^2) + eps)          (p = y if !post_norm)
  *   r' = alpha * residual + gate * p                 rounded to res_dtype
  *   n  = w_pre * r' / sqrt(mean(r'^2) + eps)         of the rounded r'
- * Statistics and sums are fp32, each output rounded once.
+ * Statistics and sums are fp32, each output rounded once.  Rows may have any
+ * finite magnitude: where a sum of squares leaves the range of fp32, it is
+ * formed from the row times a power of two.
  *   T tokens, H values each (0 <= T < 2^22, 1 <= H <= 32768); every matrix is
  *   [T, H], rows one after the other, aligned to its elements.
  *   dtype: MOEQ_F16, MOEQ_BF16 or MOEQ_F32, of y, n, the weights and the

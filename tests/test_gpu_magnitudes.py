@@ -1,0 +1,112 @@
+"""Rows of very large and very small magnitudes against the fp64 forms.
+
+A row's scale drops out of its norm, so what a sum of squares loses to the
+range of fp32 is lost from the result: rows of bf16 and fp32 values from about
+2^64 on, and rows whose squares vanish where eps is as small.  Tolerances are
+those of the norms' own tests, with 2 roundings more for the scaled sum; a
+result of fp32 arithmetic below 2^-126 is off by another 2^-150 for every
+step (at most 16 here).
+"""
+
+import numpy as np
+import pytest
+
+from oracle import norms
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+TINY = {F16: 2.0 ** -25, BF16: 2.0 ** -134, F32: 2.0 ** -150}
+U = 2.0 ** -24
+
+
+def _np(t):
+    return None if t is None else t.detach().to(torch.float32).cpu().numpy().astype(np.float64)
+
+
+def _round(ref, dtype):
+    return np.abs(ref) * (torch.finfo(dtype).eps / 2) + TINY[dtype]
+
+
+def _close(got, ref, tol, what):
+    got = _np(got)
+    assert got.shape == ref.shape and np.isfinite(ref).all(), what
+    bad = ~(np.abs(got - ref) <= tol + 16 * 2.0 ** -150)
+    assert not bad.any(), (f"{what}: {bad.sum()} of {bad.size} off, worst "
+                           f"{np.nanmax(np.abs(got - ref) / np.maximum(tol, 1e-300)):.3g} of the tolerance, first at "
+                           f"{np.argwhere(bad)[0]}")
+
+
+# (magnitude of the block's rows, of the residual's, eps)
+MAGNITUDES = [(1e20, 1.0, 1e-6), (1.0, 1e20, 1e-6), (1e20, 1e20, 1e-6), (1e-20, 1e-20, 1e-6), (1e-20, 1e-20, 1e-38),
+              (1e-20, 1e-20, 1e-42), (1e36, 1e36, 1e-6), (1e18, 1e18, 1e-6), (1.0, 1e-20, 1e-30), (1e20, 1e20, 1e29)]
+# every width class of the kernels
+WIDTHS = [1, 7, 64, 520, 1030, 4096, 8192, 16384, 20000]
+
+
+def _rows(rng, T, H, scale, dtype):
+    """Normal values times `scale`; row 1 zeros but for one value, row 2 a
+    mixture of scales, where there are such rows."""
+    v = rng.standard_normal((T, H)) * scale
+    if T > 2:
+        v[1, : H - 1] = 0
+        v[2] *= np.where(rng.random(H) < 0.5, 1.0, 1e-10)
+    return torch.from_numpy(v).to(dtype).cuda()
+
+
+@pytest.mark.parametrize("types", [(BF16, BF16), (BF16, F32), (F32, F32)], ids=["bf16", "bf16-f32", "f32"])
+@pytest.mark.parametrize("m", range(len(MAGNITUDES)))
+def test_block_norm_of_any_magnitude(m, types):
+    from bit_quantized_moe_token_amd import moeq
+    dtype, res_dtype = types
+    my, mr, eps = MAGNITUDES[m]
+    eps = float(np.float32(eps))
+    for H in WIDTHS:
+        rng = np.random.default_rng(1000 * m + H)
+        T = 3 if H > 1 else 1
+        y, res = _rows(rng, T, H, my, dtype), _rows(rng, T, H, mr, res_dtype)
+        w, q = (torch.from_numpy(1 + 0.2 * rng.standard_normal(H)).to(dtype).cuda() for _ in range(2))
+        r, n = moeq.block_norm(res, y, w_pre=w, w_post=q, alpha=0.75, eps=eps)
+        ref, _ = norms.block_norm(_np(res), _np(y), _np(w), _np(q), None, 0.75, eps, True)
+        branch = ref - 0.75 * _np(res)
+        tol = (H / 2 + 10) * U * np.abs(branch) + 2 * U * np.abs(0.75 * _np(res)) + U * np.abs(ref)
+        _close(r, ref, tol * (1 + 2.0 ** -10) + _round(ref, res_dtype) * (1 + 2.0 ** -7), f"r' {T}x{H}")
+        s = _np(r)
+        ref_n = s / norms.rms(s, eps) * _np(w)
+        _close(n, ref_n, (H / 2 + 10) * U * np.abs(ref_n) * (1 + 2.0 ** -10) + _round(ref_n, dtype) * (1 + 2.0 ** -7), f"n {T}x{H}")
+        # without a block, on the same residual
+        _, n = moeq.block_norm(res, w_pre=w, eps=eps)
+        s = _np(res)
+        ref_n = s / norms.rms(s, eps) * _np(w)
+        _close(n, ref_n, (H / 2 + 10) * U * np.abs(ref_n) * (1 + 2.0 ** -10) + _round(ref_n, dtype) * (1 + 2.0 ** -7), f"n of res {T}x{H}")
+
+
+def test_small_eps_in_fp16():
+    """fp16 rows of subnormal values whose squares are far above eps."""
+    from bit_quantized_moe_token_amd import moeq
+    rng = np.random.default_rng(7)
+    eps = float(np.float32(1e-30))
+    for H in (7, 300, 4096):
+        res = torch.from_numpy(rng.standard_normal((4, H)) * 1e-6).half().cuda()
+        _, n = moeq.block_norm(res, eps=eps)
+        ref = _np(res) / norms.rms(_np(res), eps)
+        _close(n, ref, (H / 2 + 10) * U * np.abs(ref) + _round(ref, F16) * (1 + 2.0 ** -7), H)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_infinities_and_nan_beside_large_rows(dtype):
+    """A row with an infinity or a NaN gives none of finite value where that
+    stands, and leaves the rows beside it, large or not, as they are alone."""
+    from bit_quantized_moe_token_amd import moeq
+    for H in (40, 700, 4096):
+        rng = np.random.default_rng(H)
+        v = _rows(rng, 6, H, 1e20, dtype)
+        v[0] = torch.from_numpy(rng.standard_normal(H)).to(dtype)
+        v[3, 5], v[4, 0] = float("inf"), float("nan")
+        _, n = moeq.block_norm(v)
+        assert bool(torch.isnan(n[3, 5])) and bool(torch.isnan(n[4]).all())
+        assert not n[3, :5].any() and not n[3, 6:].any()
+        for i in (0, 1, 2, 5):
+            assert bool(torch.isfinite(n[i]).all())
+            assert torch.equal(n[i], moeq.block_norm(v[i:i + 1].contiguous())[1][0])
