@@ -16,10 +16,10 @@
 // Bound by memory: every row is read once and kept in registers (as stored)
 // through the row's two reductions (16384 rows of 4096, bf16 beside an fp32
 // residual: 150 us, 5.4 TB/s; gradients of 8192 rows of 4096 in bf16 with a
-// gate per token: 123 us and 5 for the column sums, 4.2 TB/s).  Sums,
-// statistics and gradients are fp32; the backward pass reads the rows in any
-// case, so it recomputes 1 / a and 1 / b from them and needs no saved
-// statistics.
+// gate per token: 123 us and 5 for the column sums, 4.2 TB/s); the gradients
+// of rows above 8192 values read theirs twice.  Sums, statistics and gradients
+// are fp32; the backward pass reads the rows in any case, so it recomputes 1 /
+// a and 1 / b from them and needs no saved statistics.
 #include "vec8.hpp"
 
 namespace moeq {
@@ -28,15 +28,16 @@ struct NormArgs {
   const void *res, *y, *w_pre, *w_post, *gate;
   const void *d_res, *d_n;
   void *res_out, *n, *d_y, *d_r, *d_gate;
-  float *part;                       // [grid][3][H] column sums of each workgroup
+  float *part;                       // [units][3][H] column sums of each run of rows
+  struct RowStats *stats;            // [T], wide rows only; null: no column sum is wanted
   int64_t ld_gate;                   // 0: one gate row for all tokens
   int32_t T, H, post, cols;          // cols: any column sum is wanted
   float alpha, eps;
 };
 
-// Sums of N values over the NT threads of a row.  NT > 64: the waves' sums
-// meet in LDS; the caller alternates `buf` (0, 1) between reductions, so
-// that one barrier each is enough.
+// Sums of N values over the NT threads of a row, in scalar registers.  NT >
+// 64: the waves' sums meet in LDS; the caller alternates `buf` (0, 1) between
+// reductions, so that one barrier each is enough.
 template <int NT, int N>
 __device__ __forceinline__ void row_sum(float *v, float *s, int buf) {
 #pragma unroll
@@ -58,6 +59,8 @@ __device__ __forceinline__ void row_sum(float *v, float *s, int buf) {
       for (int w = 0; w < NW; ++w) v[i] += p[i * 16 + w];
     }
   }
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v[i])));
 }
 
 // The largest of the NT threads' values, buf as above.
@@ -195,128 +198,257 @@ __global__ void __launch_bounds__(norm_block(NT)) block_norm_kernel(NormArgs a) 
   }
 }
 
-// Gradients.  With more than one piece of eight per thread the sums and a
-// row in flight do not fit 128 registers, and fewer waves hide the loads
-// (two pieces of 256 threads: 138 us for the rows above).
-// A workgroup takes a contiguous run of rows and keeps its
-// column sums in registers; they leave once, as one row of a.part per
-// workgroup, for the summing kernel below (no atomics: the order is fixed).
-template <int TY, int TR, int NT, int CH>
-__global__ void __launch_bounds__(norm_block(NT), CH == 1 ? 4 : 1) block_norm_grad_kernel(NormArgs a) {
+// Element `at` (uniform) of a matrix: a scalar address, beside which a thread's
+// columns are a 32-bit offset.
+template <int T, class P>
+__device__ __forceinline__ P *row_at(P *base, int64_t at) {
+  using Bytes = std::conditional_t<std::is_const_v<P>, const uint8_t, uint8_t>;
+  return (P *)((Bytes *)base + at * Val<T>::size);
+}
+
+// Eight columns of the gradients' row operands and of the weights, as stored.
+template <int TY, int TR>
+struct GradPiece {
+  Oct<TR> r, dr;
+  Oct<TY> x, dn, wq, wp, gt;
+
+  __device__ __forceinline__ void load_weights(const NormArgs &a, int i) {
+    if (a.w_pre) wq.load(a.w_pre, i, a.H - i);
+    else wq.fill(1.f);
+    if (a.w_post) wp.load(a.w_post, i, a.H - i);
+    else wp.fill(1.f);
+    if (a.gate && !a.ld_gate) gt.load(a.gate, i, a.H - i);
+    else gt.fill(1.f);
+  }
+  __device__ __forceinline__ void load_row(const NormArgs &a, int64_t at, int i) {
+    r.load(row_at<TR>(a.res, at), i, a.H - i);
+    dn.load(row_at<TY>(a.d_n, at), i, a.H - i);
+    if (a.d_res) dr.load(row_at<TR>(a.d_res, at), i, a.H - i);
+    else dr.fill(0.f);
+    if (a.y) x.load(row_at<TY>(a.y, at), i, a.H - i);
+    else x.fill(0.f);
+    if (a.gate && a.ld_gate) gt.load(row_at<TY>(a.gate, at), i, a.H - i);
+  }
+  // opaque to the compiler, the row after its sums and the weights in every
+  // row: it would keep their fp32 values in registers otherwise
+  __device__ __forceinline__ void opaque_row() {
+    r.opaque();
+    dr.opaque();
+    x.opaque();
+    dn.opaque();
+  }
+  __device__ __forceinline__ void opaque_weights() {
+    wq.opaque();
+    wp.opaque();
+    gt.opaque();
+  }
+};
+
+// g - u m, of the g that the row's sums took: rounded before the difference.
+__device__ __forceinline__ float off_mean(float d_n, float w, float u, float m) {
+#pragma clang fp contract(off)
+  const float g = d_n * w;
+  return __builtin_fmaf(-u, m, g);
+}
+
+// Column sums of a run of rows: d_w_pre, d_w_post, d_gate.  They leave once,
+// as one row of a.part per unit, for the summing kernel below (no atomics:
+// the order is fixed).
+struct ColumnSums {
+  float v[3][8];
+  __device__ __forceinline__ ColumnSums() {
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[q][j] = 0.f;
+  }
+  __device__ __forceinline__ void store(const NormArgs &a, int64_t unit, int i) const {
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      float *p = a.part + (unit * 3 + q) * a.H + i;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) if (i + j < a.H) p[j] = v[q][j];
+    }
+  }
+};
+
+// Gradients of rows of up to 8 NT columns, one piece of eight a thread.  A
+// workgroup takes a contiguous run of rows and keeps its column sums in
+// registers: with a row in flight they fit the 128 registers of 16 waves per
+// CU, where addresses and row sums are scalar (with vector ones 6 to 120 of
+// them went through scratch: 4096 rows of 8192 in fp32 275 us, now 183).  Two
+// pieces of 256 threads took 138 us for the rows above.
+template <int TY, int TR, int NT>
+__global__ void __launch_bounds__(norm_block(NT), 4) block_norm_grad_kernel(NormArgs a) {
   constexpr int RW = norm_block(NT) / NT;   // rows at a time
   __shared__ float s[2 * 3 * 16];
-  const int t = threadIdx.x % NT;
-  const int64_t unit = (int64_t)blockIdx.x * RW + threadIdx.x / NT, units = (int64_t)gridDim.x * RW;
-  const int64_t lo = unit * a.T / units, hi = (unit + 1) * a.T / units;
+  const int i = threadIdx.x % NT * 8;
+  const int64_t unit = (int64_t)blockIdx.x * RW + __builtin_amdgcn_readfirstlane(threadIdx.x / NT);
+  const int64_t units = (int64_t)gridDim.x * RW, lo = unit * a.T / units, hi = (unit + 1) * a.T / units;
   const float rh = 1.f / (float)a.H;
-  float sums[3][CH][8];       // d_w_pre, d_w_post, d_gate
-#pragma unroll
-  for (int q = 0; q < 3; ++q)
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sums[q][c][j] = 0.f;
-  // the rows' weights as stored; opaque to the compiler in every row, which
-  // would keep their fp32 values in registers otherwise
-  Oct<TY> wq[CH], wp[CH], gt[CH];
-#pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const int i = (c * NT + t) * 8;
-    if (a.w_pre) wq[c].load(a.w_pre, i, a.H - i);
-    else wq[c].fill(1.f);
-    if (a.w_post) wp[c].load(a.w_post, i, a.H - i);
-    else wp[c].fill(1.f);
-    if (a.gate && !a.ld_gate) gt[c].load(a.gate, i, a.H - i);
-    else gt[c].fill(1.f);
-  }
+  ColumnSums sums;
+  GradPiece<TY, TR> p;
+  p.load_weights(a, i);
   const bool tok = a.gate && a.ld_gate;     // a gate row per token
   for (int64_t row = lo; row < hi; ++row) {
     const int64_t at = row * a.H;
-    Oct<TR> r[CH], dr[CH];
-    Oct<TY> x[CH], dn[CH];
+    p.load_row(a, at, i);
+    p.opaque_weights();
     float q3[3] = {0.f, 0.f, 0.f};         // sums of r^2, g r, y^2
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int i = (c * NT + t) * 8;
-      r[c].load(a.res, at + i, a.H - i);
-      dn[c].load(a.d_n, at + i, a.H - i);
-      if (a.d_res) dr[c].load(a.d_res, at + i, a.H - i);
-      else dr[c].fill(0.f);
-      if (a.y) x[c].load(a.y, at + i, a.H - i);
-      else x[c].fill(0.f);
-      if (tok) gt[c].load(a.gate, at + i, a.H - i);
-      wq[c].opaque();
-      wp[c].opaque();
-      gt[c].opaque();
-    }
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float g = dn[c][j] * wq[c][j];
-        q3[0] += r[c][j] * r[c][j];
-        q3[1] += g * r[c][j];
-        q3[2] += x[c][j] * x[c][j];
-      }
+    for (int j = 0; j < 8; ++j) {
+      const float g = p.dn[j] * p.wq[j];
+      q3[0] += p.r[j] * p.r[j];
+      q3[1] += g * p.r[j];
+      q3[2] += p.x[j] * p.x[j];
     }
     row_sum<NT, 3>(q3, s, 0);
     const float k = 1.f / __builtin_sqrtf(q3[0] * rh + a.eps);
     const float m = q3[1] * k * rh;         // mean(g u)
     const float b = a.post ? 1.f / __builtin_sqrtf(q3[2] * rh + a.eps) : 1.f;
+    p.opaque_row();
     const float al = a.y ? a.alpha : 1.f;
-    float d[CH][8], z[1] = {0.f};           // c, sum of c v
+    float d[8], z[1] = {0.f};               // c, sum of c v
+    float ov[8], dv[8];
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int i = (c * NT + t) * 8;
-      float ov[8], dv[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float u = r[c][j] * k;
-        const float e = k * (dn[c][j] * wq[c][j] - u * m) + dr[c][j];
-        sums[0][c][j] += dn[c][j] * u;
-        ov[j] = al * e;
-        const float v = x[c][j] * b, eg = e * gt[c][j];
-        sums[1][c][j] += eg * v;
-        dv[j] = e * v * wp[c][j];
-        sums[2][c][j] += dv[j];
-        d[c][j] = eg * wp[c][j];
-        z[0] += d[c][j] * v;
-      }
-      Oct<TR> out;
-      out.pack(ov);
-      out.store(a.d_r, at + i, a.H - i);
-      if (tok) {
-        Oct<TY> o;
-        o.pack(dv);
-        o.store(a.d_gate, at + i, a.H - i);
-      }
+    for (int j = 0; j < 8; ++j) {
+      const float u = p.r[j] * k;
+      const float e = k * off_mean(p.dn[j], p.wq[j], u, m) + p.dr[j];
+      sums.v[0][j] += p.dn[j] * u;
+      ov[j] = al * e;
+      const float v = p.x[j] * b, eg = e * p.gt[j];
+      sums.v[1][j] += eg * v;
+      dv[j] = e * v * p.wp[j];
+      sums.v[2][j] += dv[j];
+      d[j] = eg * p.wp[j];
+      z[0] += d[j] * v;
+    }
+    Oct<TR> out;
+    out.pack(ov);
+    out.store(row_at<TR>(a.d_r, at), i, a.H - i);
+    Oct<TY> o;
+    if (tok) {
+      o.pack(dv);
+      o.store(row_at<TY>(a.d_gate, at), i, a.H - i);
     }
     // (also a barrier between this row's sums in s and the next one's)
     row_sum<NT, 1>(z, s, 1);
     if (a.y) {
       const float mz = a.post ? z[0] * rh : 0.f;
+      float v[8];
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int i = (c * NT + t) * 8;
-        Oct<TY> o;
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = b * (d[c][j] - x[c][j] * b * mz);
-        o.pack(v);
-        o.store(a.d_y, at + i, a.H - i);
-      }
+      for (int j = 0; j < 8; ++j) v[j] = b * (d[j] - p.x[j] * b * mz);
+      o.pack(v);
+      o.store(row_at<TY>(a.d_y, at), i, a.H - i);
     }
   }
-  if (!a.cols) return;
+  if (a.cols) sums.store(a, unit, i);
+}
+
+// Gradients of wide rows.  A row in flight with its column sums does not fit
+// the registers of 1024 threads from two pieces on (held in scratch: 339 us
+// where this takes 161, 2048 rows of 16384 in bf16, and 1116 against 373,
+// 1024 rows of 32768 in fp32): one workgroup per row forms what its gradients
+// need of the whole row, then workgroups of 2048 columns and a run of rows
+// apply it, a piece of every row a thread.  The rows are read twice.  Without
+// column sums the row's own workgroup applies it.
+struct RowStats {
+  float k, m, b, mz;   // 1 / rms(r'), mean(g u), 1 / rms(y) (1 without post norm), mean(c v) (0)
+};
+
+// The row's gradients at the columns of p, and (SUMS) their part of the column
+// sums.
+template <bool SUMS, int TY, int TR>
+__device__ __forceinline__ void apply_stats(const NormArgs &a, const GradPiece<TY, TR> &p, int64_t at, int i, RowStats st,
+                                            ColumnSums &sums) {
+  const float al = a.y ? a.alpha : 1.f;
+  float ov[8], gv[8], yv[8];
 #pragma unroll
-  for (int q = 0; q < 3; ++q)
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int i = (c * NT + t) * 8;
-      float *p = a.part + (unit * 3 + q) * a.H + i;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) if (i + j < a.H) p[j] = sums[q][c][j];
+  for (int j = 0; j < 8; ++j) {
+    const float u = p.r[j] * st.k, v = p.x[j] * st.b;
+    const float e = st.k * off_mean(p.dn[j], p.wq[j], u, st.m) + p.dr[j], eg = e * p.gt[j];
+    ov[j] = al * e;
+    gv[j] = e * v * p.wp[j];
+    yv[j] = st.b * (eg * p.wp[j] - v * st.mz);
+    if constexpr (SUMS) {
+      sums.v[0][j] += p.dn[j] * u;
+      sums.v[1][j] += eg * v;
+      sums.v[2][j] += gv[j];
     }
+  }
+  Oct<TR> o;
+  o.pack(ov);
+  o.store(row_at<TR>(a.d_r, at), i, a.H - i);
+  Oct<TY> q;
+  if (a.gate && a.ld_gate) {
+    q.pack(gv);
+    q.store(row_at<TY>(a.d_gate, at), i, a.H - i);
+  }
+  if (a.y) {
+    q.pack(yv);
+    q.store(row_at<TY>(a.d_y, at), i, a.H - i);
+  }
+}
+
+// Sums of r^2, g r, y^2 and, with f = gate w_post y, of f dr, f g and f r:
+// c v = f b (dr + k g - k^2 m r) sums to mean(c v) without another pass.
+template <int TY, int TR>
+__global__ void __launch_bounds__(1024) norm_stats_kernel(NormArgs a) {
+  __shared__ float s[6 * 16];
+  const int64_t row = blockIdx.x, at = row * a.H;
+  const float rh = 1.f / (float)a.H;
+  float q[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int i = threadIdx.x * 8; i < a.H; i += 8192) {
+    GradPiece<TY, TR> p;
+    p.load_weights(a, i);
+    p.load_row(a, at, i);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float r = p.r[j], x = p.x[j], g = p.dn[j] * p.wq[j], f = p.gt[j] * p.wp[j] * x;
+      q[0] += r * r;
+      q[1] += g * r;
+      q[2] += x * x;
+      q[3] += f * p.dr[j];
+      q[4] += f * g;
+      q[5] += f * r;
+    }
+  }
+  row_sum<1024, 6>(q, s, 0);
+  RowStats st;
+  st.k = 1.f / __builtin_sqrtf(q[0] * rh + a.eps);
+  st.m = q[1] * st.k * rh;
+  st.b = a.post ? 1.f / __builtin_sqrtf(q[2] * rh + a.eps) : 1.f;
+  st.mz = a.post ? st.b * rh * (q[3] + st.k * q[4] - (st.k * st.m) * (st.k * q[5])) : 0.f;
+  if (a.stats) {
+    if (threadIdx.x == 0) a.stats[row] = st;
+    return;
+  }
+  ColumnSums none;
+#pragma unroll 1
+  for (int i = threadIdx.x * 8; i < a.H; i += 8192) {
+    GradPiece<TY, TR> p;
+    p.load_weights(a, i);
+    p.load_row(a, at, i);
+    apply_stats<false>(a, p, at, i, st, none);
+  }
+}
+
+template <int TY, int TR>
+__global__ void __launch_bounds__(256, 4) norm_apply_kernel(NormArgs a) {
+  const int i = ((int)blockIdx.x * 256 + (int)threadIdx.x) * 8;
+  if (i >= a.H) return;
+  const int64_t unit = blockIdx.y, units = gridDim.y;
+  const int64_t lo = unit * a.T / units, hi = (unit + 1) * a.T / units;
+  GradPiece<TY, TR> p;
+  p.load_weights(a, i);
+  ColumnSums sums;
+  for (int64_t row = lo; row < hi; ++row) {
+    p.load_row(a, row * a.H, i);
+    p.opaque_weights();
+    apply_stats<true>(a, p, row * a.H, i, a.stats[row], sums);
+  }
+  sums.store(a, unit, i);
 }
 
 // Column sums of the units' partial sums: 32 columns per workgroup, 32
@@ -345,18 +477,25 @@ __global__ void __launch_bounds__(1024) norm_columns_kernel(const float *__restr
 constexpr int kNormMaxH = 32768;
 constexpr int kNormMaxT = (1 << 22) - 1;   // workgroups of 1024 threads: a launch has fewer than 2^32
 
-// Threads per row of the gradient kernel for rows of H: one piece of eight a
-// thread as far as 1024 threads go, so that the column sums and a row in
-// flight stay within 128 registers and a CU holds 16 waves.
+// Threads per row of the gradient kernel for rows of H up to kGradMaxH: one
+// piece of eight a thread as far as 1024 threads go, so that the column sums
+// and a row in flight stay within 128 registers and a CU holds 16 waves.
+constexpr int kGradMaxH = 8192;
 static int grad_threads(int H) { return H <= 512 ? 64 : H <= 1024 ? 128 : H <= 2048 ? 256 : H <= 4096 ? 512 : 1024; }
 
-// Units (rows in flight) of the gradient kernel: 1024 threads per CU, each
-// unit leaving one row of partial column sums.
+// Units (rows in flight, or runs of rows of one workgroup) of the gradient
+// kernels: 1024 threads per CU, each unit leaving one row of partial column
+// sums.
 static int grad_units(int T, int H) {
+  if (H > kGradMaxH) return std::min(T, 1024 / ((H + 2047) / 2048));
   const int nt = grad_threads(H), rw = nt == 64 ? 4 : 1;
   const int groups = std::min((T + rw - 1) / rw, 256 * 1024 / (nt * rw));
   return groups * rw;
 }
+
+// Workspace of the column sums: the rows' statistics, the units' sums.
+static size_t grad_stats_bytes(int T, int H) { return H > kGradMaxH ? (size_t)T * sizeof(RowStats) : 0; }
+static size_t grad_workspace(int T, int H) { return grad_stats_bytes(T, H) + (size_t)grad_units(T, H) * 3 * (size_t)H * 4; }
 
 template <int TY, int TR, int NT, int CH>
 static void launch_norm(const NormArgs &a, hipStream_t s) {
@@ -364,22 +503,28 @@ static void launch_norm(const NormArgs &a, hipStream_t s) {
   hipLaunchKernelGGL((block_norm_kernel<TY, TR, NT, CH>), dim3((a.T + RW - 1) / RW), dim3(norm_block(NT)), 0, s, a);
 }
 
-template <int TY, int TR, int NT, int CH>
+template <int TY, int TR, int NT>
 static void launch_grad(const NormArgs &a, hipStream_t s) {
   constexpr int RW = norm_block(NT) / NT;
-  hipLaunchKernelGGL((block_norm_grad_kernel<TY, TR, NT, CH>), dim3(grad_units(a.T, a.H) / RW), dim3(norm_block(NT)), 0, s, a);
+  hipLaunchKernelGGL((block_norm_grad_kernel<TY, TR, NT>), dim3(grad_units(a.T, a.H) / RW), dim3(norm_block(NT)), 0, s, a);
+}
+
+template <int TY, int TR>
+static void launch_grad_wide(const NormArgs &a, hipStream_t s) {
+  hipLaunchKernelGGL((norm_stats_kernel<TY, TR>), dim3(a.T), dim3(1024), 0, s, a);
+  if (a.stats)
+    hipLaunchKernelGGL((norm_apply_kernel<TY, TR>), dim3((a.H + 2047) / 2048, grad_units(a.T, a.H)), dim3(256), 0, s, a);
 }
 
 template <int TY, int TR>
 static void launch_norm_h(const NormArgs &a, bool grad, hipStream_t s) {
   if (grad) {
-    if (a.H <= 512) launch_grad<TY, TR, 64, 1>(a, s);
-    else if (a.H <= 1024) launch_grad<TY, TR, 128, 1>(a, s);
-    else if (a.H <= 2048) launch_grad<TY, TR, 256, 1>(a, s);
-    else if (a.H <= 4096) launch_grad<TY, TR, 512, 1>(a, s);
-    else if (a.H <= 8192) launch_grad<TY, TR, 1024, 1>(a, s);
-    else if (a.H <= 16384) launch_grad<TY, TR, 1024, 2>(a, s);
-    else launch_grad<TY, TR, 1024, 4>(a, s);
+    if (a.H <= 512) launch_grad<TY, TR, 64>(a, s);
+    else if (a.H <= 1024) launch_grad<TY, TR, 128>(a, s);
+    else if (a.H <= 2048) launch_grad<TY, TR, 256>(a, s);
+    else if (a.H <= 4096) launch_grad<TY, TR, 512>(a, s);
+    else if (a.H <= kGradMaxH) launch_grad<TY, TR, 1024>(a, s);
+    else launch_grad_wide<TY, TR>(a, s);
     return;
   }
   if (a.H <= 512) launch_norm<TY, TR, 64, 1>(a, s);
@@ -475,7 +620,7 @@ MOEQ_API moeq_status moeq_block_norm_grad_workspace_size(int32_t T, int32_t H, s
   if (T < 0 || H < 1) return fail(MOEQ_ERR_INVALID, "%s: T=%d, H=%d", who, T, H);
   if (H > kNormMaxH) return fail(MOEQ_ERR_UNSUPPORTED, "%s: H=%d above %d", who, H, kNormMaxH);
   if (T > kNormMaxT) return fail(MOEQ_ERR_UNSUPPORTED, "%s: T=%d above %d", who, T, kNormMaxT);
-  *bytes = (size_t)grad_units(T, H) * 3 * (size_t)H * 4;
+  *bytes = grad_workspace(T, H);
   return MOEQ_OK;
 }
 
@@ -502,7 +647,8 @@ MOEQ_API moeq_status moeq_block_norm_grad(const moeq_norm *d, const void *res, c
   float *g_cols = d->gate && !d->gate_per_token ? (float *)d_gate : nullptr;
   const bool cols = d_w_pre || d_w_post || g_cols;
   const int units = grad_units(d->T, d->H);
-  const size_t need = (size_t)units * 3 * (size_t)d->H * 4;
+  const size_t need = grad_workspace(d->T, d->H);
+  float *part = (float *)((char *)ws + grad_stats_bytes(d->T, d->H));
   if (cols && need) {
     if (!ws || ((uintptr_t)ws & 15)) return fail(MOEQ_ERR_INVALID, "%s: null or misaligned workspace", who);
     if (ws_bytes < need) return fail(MOEQ_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", who, ws_bytes, need);
@@ -514,7 +660,8 @@ MOEQ_API moeq_status moeq_block_norm_grad(const moeq_norm *d, const void *res, c
     a.d_r = d_residual;
     a.d_y = d_y;
     a.d_gate = d_gate;
-    a.part = (float *)ws;
+    a.stats = cols && d->H > kGradMaxH ? (RowStats *)ws : nullptr;
+    a.part = part;
     a.cols = cols;
     prof_begin("block_norm_grad", stream);
     launch_norm_types(a, d->dtype, d->res_dtype, true, stream);
@@ -523,7 +670,7 @@ MOEQ_API moeq_status moeq_block_norm_grad(const moeq_norm *d, const void *res, c
   }
   if (cols) {
     prof_begin("norm_columns", stream);
-    hipLaunchKernelGGL(norm_columns_kernel, dim3((d->H + 31) / 32, 3), dim3(1024), 0, stream, (const float *)ws, units,
+    hipLaunchKernelGGL(norm_columns_kernel, dim3((d->H + 31) / 32, 3), dim3(1024), 0, stream, part, units,
                        d->H, d_w_pre, d_w_post, g_cols);
     prof_end("norm_columns", stream);
     MOEQ_TRY(check_launch("norm_columns"));

@@ -42,3 +42,16 @@ def test_reserved_registers_keep_their_value(tmp_path):
     for b in blocks:
         assert not any(re.match(r"\S+ m0\b", l) for l in b)
     assert len(re.findall(r"^\s*s_\w+ m0,", out.read_text(), re.M)) >= 2
+
+
+@pytest.mark.skipif(not os.path.exists(build.HIPCC) and not shutil.which(build.HIPCC), reason="no compiler")
+def test_norms_use_no_scratch():
+    """The norms' kernels hold their rows and sums in registers: the compiler
+    reports no scratch for any of them."""
+    src = os.path.join(build.CSRC, "norm.hip")
+    r = subprocess.run([build.HIPCC, *build.CFLAGS, "-Rpass-analysis=kernel-resource-usage", "-S", "--cuda-device-only", src,
+                        "-o", os.devnull], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
+    found = re.findall(r"Function Name: (\S+).*?ScratchSize \[bytes/lane\]: (\d+)", r.stderr, re.S)
+    assert len(found) > 60
+    assert not [name for name, size in found if int(size)]
