@@ -35,6 +35,10 @@ struct NormArgs {
   float alpha, eps;
 };
 
+__device__ __forceinline__ float scalar(float v) {   // a value that all lanes have
+  return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v)));
+}
+
 // Sums of N values over the NT threads of a row, in scalar registers.  NT >
 // 64: the waves' sums meet in LDS; the caller alternates `buf` (0, 1) between
 // reductions, so that one barrier each is enough.
@@ -60,7 +64,7 @@ __device__ __forceinline__ void row_sum(float *v, float *s, int buf) {
     }
   }
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v[i])));
+  for (int i = 0; i < N; ++i) v[i] = scalar(v[i]);
 }
 
 // The largest of the NT threads' values, buf as above.
@@ -76,7 +80,7 @@ __device__ __forceinline__ float row_top(float v, float *s, int buf) {
 #pragma unroll
     for (int w = 1; w < NT / 64; ++w) v = __builtin_fmaxf(v, p[w]);
   }
-  return v;
+  return scalar(v);
 }
 
 // mean(v^2) + eps in fp32 is as good as the sum of squares, which is exact to
@@ -272,6 +276,18 @@ struct ColumnSums {
   }
 };
 
+// Powers of two (row_unit) for r' and y, from the largest magnitudes that the
+// threads met.  Uses buffers 2 and 3 of s.
+struct RowUnits {
+  float r = 1.f, y = 1.f;
+};
+template <int NT>
+__device__ __forceinline__ RowUnits row_units(float top_r, float top_y, float eps, float *s) {
+  top_r = row_top<NT>(top_r, s, 2);
+  top_y = row_top<NT>(top_y, s, 3);
+  return RowUnits{row_unit(top_r, eps), row_unit(top_y, eps)};
+}
+
 // Gradients of rows of up to 8 NT columns, one piece of eight a thread.  A
 // workgroup takes a contiguous run of rows and keeps its column sums in
 // registers: with a row in flight they fit the 128 registers of 16 waves per
@@ -281,7 +297,7 @@ struct ColumnSums {
 template <int TY, int TR, int NT>
 __global__ void __launch_bounds__(norm_block(NT), 4) block_norm_grad_kernel(NormArgs a) {
   constexpr int RW = norm_block(NT) / NT;   // rows at a time
-  __shared__ float s[2 * 3 * 16];
+  __shared__ float s[4 * 3 * 16];
   const int i = threadIdx.x % NT * 8;
   const int64_t unit = (int64_t)blockIdx.x * RW + __builtin_amdgcn_readfirstlane(threadIdx.x / NT);
   const int64_t units = (int64_t)gridDim.x * RW, lo = unit * a.T / units, hi = (unit + 1) * a.T / units;
@@ -303,9 +319,36 @@ __global__ void __launch_bounds__(norm_block(NT), 4) block_norm_grad_kernel(Norm
       q3[2] += p.x[j] * p.x[j];
     }
     row_sum<NT, 3>(q3, s, 0);
-    const float k = 1.f / __builtin_sqrtf(q3[0] * rh + a.eps);
-    const float m = q3[1] * k * rh;         // mean(g u)
-    const float b = a.post ? 1.f / __builtin_sqrtf(q3[2] * rh + a.eps) : 1.f;
+    const float qr = q3[0] * rh + a.eps, qy = q3[2] * rh + a.eps;
+    float k, m, b;                          // 1 / rms(r'), mean(g u), 1 / rms(y)
+    if (__builtin_expect(plain_square(qr) && (!a.post || plain_square(qy)) && __builtin_fabsf(q3[1]) < __builtin_inff(), 1)) {
+      k = 1.f / __builtin_sqrtf(qr);
+      m = q3[1] * k * rh;
+      b = a.post ? 1.f / __builtin_sqrtf(qy) : 1.f;
+    } else {                                // as inverse_rms
+      float top_r = 0.f, top_y = 0.f;
+      p.opaque_row();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        top_r = __builtin_fmaxf(top_r, __builtin_fabsf(p.r[j]));
+        top_y = __builtin_fmaxf(top_y, __builtin_fabsf(p.x[j]));
+      }
+      const RowUnits u = row_units<NT>(top_r, top_y, a.eps, s);
+      q3[0] = q3[1] = q3[2] = 0.f;
+      p.opaque_row();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float r = p.r[j] * u.r, y = p.x[j] * u.y;
+        q3[0] += r * r;
+        q3[1] += p.dn[j] * p.wq[j] * r;
+        q3[2] += y * y;
+      }
+      row_sum<NT, 3>(q3, s, 0);             // (the barriers above lie behind its first use)
+      const float h = 1.f / __builtin_sqrtf(q3[0] * rh + a.eps * u.r * u.r);
+      k = u.r * h;
+      m = q3[1] * h * rh;
+      b = a.post ? u.y / __builtin_sqrtf(q3[2] * rh + a.eps * u.y * u.y) : 1.f;
+    }
     p.opaque_row();
     const float al = a.y ? a.alpha : 1.f;
     float d[8], z[1] = {0.f};               // c, sum of c v
@@ -394,32 +437,58 @@ __device__ __forceinline__ void apply_stats(const NormArgs &a, const GradPiece<T
 // c v = f b (dr + k g - k^2 m r) sums to mean(c v) without another pass.
 template <int TY, int TR>
 __global__ void __launch_bounds__(1024) norm_stats_kernel(NormArgs a) {
-  __shared__ float s[6 * 16];
+  __shared__ float s[4 * 3 * 16];
   const int64_t row = blockIdx.x, at = row * a.H;
   const float rh = 1.f / (float)a.H;
-  float q[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-  for (int i = threadIdx.x * 8; i < a.H; i += 8192) {
-    GradPiece<TY, TR> p;
-    p.load_weights(a, i);
-    p.load_row(a, at, i);
+  float q[6];
+  const auto sums = [&](RowUnits u) {          // of the row with r' times u.r and y times u.y
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float r = p.r[j], x = p.x[j], g = p.dn[j] * p.wq[j], f = p.gt[j] * p.wp[j] * x;
-      q[0] += r * r;
-      q[1] += g * r;
-      q[2] += x * x;
-      q[3] += f * p.dr[j];
-      q[4] += f * g;
-      q[5] += f * r;
+    for (int n = 0; n < 6; ++n) q[n] = 0.f;
+#pragma unroll 1
+    for (int i = threadIdx.x * 8; i < a.H; i += 8192) {
+      GradPiece<TY, TR> p;
+      p.load_weights(a, i);
+      p.load_row(a, at, i);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float r = p.r[j] * u.r, x = p.x[j] * u.y, g = p.dn[j] * p.wq[j], f = p.gt[j] * p.wp[j] * x;
+        q[0] += r * r;
+        q[1] += g * r;
+        q[2] += x * x;
+        q[3] += f * p.dr[j];
+        q[4] += f * g;
+        q[5] += f * r;
+      }
     }
+    row_sum<1024, 6>(q, s, 0);
+  };
+  RowUnits u;
+  sums(RowUnits{1.f, 1.f});
+  float qr = q[0] * rh + a.eps, qy = q[2] * rh + a.eps, sum = __builtin_fabsf(q[1]);
+  if (a.post) sum += __builtin_fabsf(q[3]) + __builtin_fabsf(q[4]) + __builtin_fabsf(q[5]);
+  if (__builtin_expect(!(plain_square(qr) && (!a.post || plain_square(qy)) && sum < __builtin_inff()), 0)) {
+    float top_r = 0.f, top_y = 0.f;            // as inverse_rms
+#pragma unroll 1
+    for (int i = threadIdx.x * 8; i < a.H; i += 8192) {
+      GradPiece<TY, TR> p;
+      p.load_row(a, at, i);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        top_r = __builtin_fmaxf(top_r, __builtin_fabsf(p.r[j]));
+        top_y = __builtin_fmaxf(top_y, __builtin_fabsf(p.x[j]));
+      }
+    }
+    u = row_units<1024>(top_r, top_y, a.eps, s);
+    sums(u);
+    qr = q[0] * rh + a.eps * u.r * u.r;
+    qy = q[2] * rh + a.eps * u.y * u.y;
   }
-  row_sum<1024, 6>(q, s, 0);
+  const float hr = 1.f / __builtin_sqrtf(qr), hy = 1.f / __builtin_sqrtf(qy);   // 1 / rms of r' u.r and of y u.y
   RowStats st;
-  st.k = 1.f / __builtin_sqrtf(q[0] * rh + a.eps);
-  st.m = q[1] * st.k * rh;
-  st.b = a.post ? 1.f / __builtin_sqrtf(q[2] * rh + a.eps) : 1.f;
-  st.mz = a.post ? st.b * rh * (q[3] + st.k * q[4] - (st.k * st.m) * (st.k * q[5])) : 0.f;
+  st.k = u.r * hr;
+  st.m = q[1] * hr * rh;
+  st.b = a.post ? u.y * hy : 1.f;
+  st.mz = a.post ? hy * rh * (q[3] + st.k * q[4] - (st.k * st.m) * (hr * q[5])) : 0.f;
   if (a.stats) {
     if (threadIdx.x == 0) a.stats[row] = st;
     return;

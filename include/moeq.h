@@ -583,8 +583,8 @@ moeq_status moeq_block_norm(const moeq_norm *d, const void *residual, const void
 /*
  * moeq_block_norm_grad — gradients of all inputs from those of r' (d_res, of
  * res_dtype, or NULL: zeros) and of n (d_n, of dtype), given the forward's
- * res = r' and y (NULL without a block).  The rounding of r' passes the
- * gradient unchanged.
+ * res = r' and y (NULL without a block), rows of any finite magnitude here too.
+ * The rounding of r' passes the gradient unchanged.
  *   d_residual DEVICE [T, H] res_dtype; d_y DEVICE [T, H] dtype (with y);
  *   d_w_pre, d_w_post DEVICE [H] fp32 or NULL (not wanted);
  *   d_gate (with gate) DEVICE [H] fp32, or [T, H] of dtype for a gate per
