@@ -511,10 +511,16 @@ __device__ __forceinline__ void write_tile(const GemmArgs &a, const Tile &t, int
   for (int j = 0; j < TJ; ++j) {
     const int x = jb + j * 16 + (lane & 15);   // row of the tile
     if (x >= t.rows) continue;
-    float sc = 1.f;
+    float sc = 1.f, up = 1.f;
     if constexpr (TY == kI8) {
       const int s = source_row(a, t.row + x);
       sc = s >= 0 ? a.sj[s] : 0.f;
+      // (a sum of up to 2^31 times a scale of 2^96 and more could leave fp32
+      // where the product with the channel's scale does not)
+      if (__builtin_fabsf(sc) >= 0x1p96f) {
+        sc *= 0x1p-40f;
+        up = 0x1p40f;
+      }
     }
     const int64_t ob = MODE == kMats ? (int64_t)t.e * a.e_out + (int64_t)(j0 + x) * a.ldo : (int64_t)(t.row + x) * a.ldo;
 #pragma unroll
@@ -525,7 +531,7 @@ __device__ __forceinline__ void write_tile(const GemmArgs &a, const Tile &t, int
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         v[q] = (float)acc[i][j][q];
-        if constexpr (TY == kI8) v[q] = v[q] * sc * (c + q < a.ni ? a.si[(int64_t)t.e * a.ni + c + q] : 0.f);
+        if constexpr (TY == kI8) v[q] = v[q] * sc * (c + q < a.ni ? a.si[(int64_t)t.e * a.ni + c + q] : 0.f) * up;
       }
       store4(a, ob + c, v, a.ni - c);
     }

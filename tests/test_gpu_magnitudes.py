@@ -175,3 +175,36 @@ def test_large_gradients_of_small_rows():
         g, u = np.abs(_np(d_n)), np.abs(_np(r) * a)
         mag = a * (g + u * np.mean(g * u, axis=1, keepdims=True))
         _close(got, ref, 1.25 * (2 * H + 16) * U * mag + _round(ref, F32), H)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,K,N", [(1, 64, 40), (5, 4096, 33), (40, 200, 130)])
+def test_linear_i8_of_large_rows(T, K, N, dtype):
+    """Rows up to the type's largest values with channel scales that bring the
+    result back: three fp32 roundings, then one to the output's type."""
+    from bit_quantized_moe_token_amd import moeq
+    rng = np.random.default_rng(K)
+    x = rng.uniform(-1, 1, (T, K)) * np.exp2(rng.choice([0, 60, 100, 127], (T, 1)))
+    x = torch.from_numpy(x).to(dtype).cuda()
+    wq = torch.from_numpy(rng.integers(-127, 128, (N, K)).astype(np.int8)).cuda()
+    sw = torch.from_numpy((rng.uniform(0.5, 1.5, N) * 2.0 ** rng.choice([-120, -60, -20], N)).astype(np.float32)).cuda()
+    xq, sx = moeq.quantize_i8(x)
+    ints = xq.cpu().numpy().astype(np.float64) @ wq.cpu().numpy().astype(np.float64).T
+    ref = ints * sx.cpu().numpy().astype(np.float64)[:, None] * sw.cpu().numpy().astype(np.float64)
+    assert np.abs(ref).max() < 2.0 ** 126
+    for y in (moeq.linear_i8(x, wq, sw), moeq.gemm_i8(xq, sx, wq, sw, out_dtype=dtype)):
+        _close(y, ref, 3 * U * np.abs(ref) * (1 + 2.0 ** -8) + _round(ref, dtype) * (1 + 2.0 ** -8), (T, K, N))
+
+
+def test_gemm_i8_with_scales_at_the_ends_of_fp32():
+    from bit_quantized_moe_token_amd import moeq
+    xq = torch.full((6, 1000), 127, dtype=torch.int8, device="cuda")
+    wq = torch.full((3, 1000), -127, dtype=torch.int8, device="cuda")
+    sx = torch.tensor([3e38, -3e38, 2.0 ** 95, float("inf"), float("nan"), 1.0], device="cuda")
+    sw = torch.tensor([2.0 ** -120, 2.0 ** -149, 1.0], device="cuda")
+    y = _np(moeq.gemm_i8(xq, sx, wq, sw, out_dtype=F32))
+    ref = -16129000.0 * _np(sx)[:, None] * _np(sw)
+    large = np.abs(ref) > 3.4028235e38
+    assert np.array_equal(np.isnan(y), np.isnan(ref)) and np.array_equal(np.isinf(y), large & ~np.isnan(ref))
+    ok = ~np.isnan(ref) & ~large
+    assert np.all(np.abs(y - ref)[ok] <= 3 * U * np.abs(ref[ok]) + 4 * 2.0 ** -150)
