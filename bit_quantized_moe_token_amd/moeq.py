@@ -382,6 +382,13 @@ def _like(t, dtypes, ndim, dev, name):
         raise ValueError(f"{name} must be contiguous along its last dimension")
 
 
+def _sizes(**sizes):
+    """Refuses sizes that the library's 32-bit arguments would cut off."""
+    for name, v in sizes.items():
+        if v > 0x7fffffff:
+            raise ValueError(f"{name}={v} is beyond 32 bits")
+
+
 def _ld(t):
     """Elements between the rows of t (its row length when there is one row)."""
     return t.stride(-2) if t.shape[-2] > 1 else t.shape[-1]
@@ -404,6 +411,8 @@ def _groups(T, E, offsets, pairs, k, dev):
     if pairs is not None:
         _like(pairs, (torch.int32,), 1, dev, "pairs")
         P = pairs.shape[0]
+    if T > 0x7fffffff or P > 0x7fffffff or E > 0x7fffffff or k > 0x7fffffff:
+        _sizes(T=T, P=P, E=E, k=k)
     return _lib.Groups(offsets.data_ptr() if offsets is not None else None,
                        pairs.data_ptr() if pairs is not None else None, E, P, T, k), P
 
@@ -450,6 +459,8 @@ def grouped_gemm(x, w, offsets, pairs=None, k=1, trans=False, out=None, out_dtyp
     E, N, Kw = w.shape if not trans else (w.shape[0], w.shape[2], w.shape[1])
     if Kw != K:
         raise ValueError(f"x has {K} columns, w {Kw}")
+    if N > 0x7fffffff or K > 0x7fffffff:
+        _sizes(N=N, K=K)
     g, P = _groups(T, E, offsets, pairs, k, dev)
     out = _out(out, (P, N), out_dtype or x.dtype, (x.dtype, torch.float32), dev, x)
     _launch("moeq_grouped_gemm", dev, g, x.data_ptr(), _ld(x), w.data_ptr(), _ld(w), w.stride(0), int(trans), N, K,
@@ -470,6 +481,8 @@ def grouped_wgrad(dy, x, offsets, pairs=None, k=1, out=None, out_dtype=torch.flo
     g, P = _groups(T, E, offsets, pairs, k, dev)
     if P != dy.shape[0]:
         raise ValueError(f"dy has {dy.shape[0]} rows for {P} sorted rows")
+    if N > 0x7fffffff or K > 0x7fffffff:
+        _sizes(N=N, K=K)
     out = _out(out, (E, N, K), out_dtype, (dy.dtype, torch.float32), dev, dy)
     _launch("moeq_grouped_wgrad", dev, g, dy.data_ptr(), _ld(dy), x.data_ptr(), _ld(x), N, K, _DTYPE[dy.dtype],
             out.data_ptr(), _ld(out), out.stride(0), _DTYPE[out.dtype])
@@ -485,6 +498,7 @@ def quantize_i8(x):
         q, s = quantize_i8(x.reshape(-1, x.shape[-1]))
         return q.view(x.shape), s.view(x.shape[:2])
     _like(x, _DTYPE, 2, dev, "x")
+    _sizes(rows=x.shape[0], cols=x.shape[1])
     q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
     s = torch.empty((x.shape[0],), dtype=torch.float32, device=x.device)
     _launch("moeq_quantize_i8", dev, x.data_ptr(), _ld(x), x.shape[0], x.shape[1], _DTYPE[x.dtype], q.data_ptr(),
@@ -499,6 +513,8 @@ def _i8_weights(x, wq, sw, dev):
     N = wq.shape[-2]
     if wq.shape[-1] != x.shape[1]:
         raise ValueError(f"x has {x.shape[1]} columns, wq {wq.shape[-1]}")
+    if N > 0x7fffffff or x.shape[1] > 0x7fffffff:
+        _sizes(N=N, K=x.shape[1])
     _like(sw, (torch.float32,), wq.dim() - 1, dev, "sw")
     if sw.shape != wq.shape[:-1] or not sw.is_contiguous():
         raise ValueError(f"sw must be contiguous of shape {tuple(wq.shape[:-1])}, got {tuple(sw.shape)}")
@@ -543,6 +559,7 @@ def linear_i8(x, wq, sw, offsets=None, pairs=None, k=1, out=None, out_dtype=None
 
 @functools.lru_cache(maxsize=1024)
 def linear_i8_workspace_size(T, K):
+    _sizes(T=T, K=K)
     n = ctypes.c_size_t(0)
     check(lib().moeq_linear_i8_workspace_size(T, K, ctypes.byref(n)), "moeq_linear_i8_workspace_size")
     return n.value
@@ -576,6 +593,8 @@ def _norm(res, dtype, y, w_pre, w_post, gate, alpha, eps, post_norm, dev):
     T, H = res.shape
     if dtype not in _DTYPE:
         raise TypeError(f"{dtype} is not a type of the norms")
+    if T > 0x7fffffff or H > 0x7fffffff:
+        _sizes(T=T, H=H)
     vec = (H,)
     if y is not None:
         _dense(y, res.shape, dtype, dev, "y")
@@ -668,6 +687,7 @@ def block_norm_grad(res, d_n, y=None, d_res=None, w_pre=None, w_post=None, gate=
 
 @functools.lru_cache(maxsize=1024)
 def block_norm_grad_workspace_size(T, H):
+    _sizes(T=T, H=H)
     n = ctypes.c_size_t(0)
     check(lib().moeq_block_norm_grad_workspace_size(T, H, ctypes.byref(n)), "moeq_block_norm_grad_workspace_size")
     return n.value
