@@ -3,6 +3,11 @@
 torch provides device memory and the current HIP stream; each function below
 validates shapes, passes raw pointers to the C ABI and returns the tensors
 the library filled.  No arithmetic of the method happens here.
+
+The functions record nothing for autograd: what they return does not require
+grad, whatever their inputs do.  Gradients are calls of their own
+(grouped_gemm with trans, grouped_wgrad, block_norm_grad), for an
+autograd.Function of the caller's to make.
 """
 
 import ctypes
@@ -418,12 +423,20 @@ def _groups(T, E, offsets, pairs, k, dev):
 
 
 def _out(out, shape, dtype, dtypes, dev, like, name="out"):
+    """The caller's output tensor, or a new one."""
     if out is None:
         return like.new_empty(shape, dtype=dtype)
     _like(out, dtypes, len(shape), dev, name)
     if tuple(out.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(out.shape)}")
+    _written(out)
     return out
+
+
+def _written(t):
+    """Counts a write of the library into t, as torch's own operations do: a
+    backward pass that saved t before reports it instead of using it."""
+    torch.autograd.graph.increment_version(t)
 
 
 _FUNCS = {}
@@ -451,7 +464,8 @@ def grouped_gemm(x, w, offsets, pairs=None, k=1, trans=False, out=None, out_dtyp
     x fp16 or bf16 [T, K]; w of the same type [E, N, K] ([E, K, N] with
     trans); offsets int32 [E + 1]; pairs int32 [P] or None (out[r] from
     x[r]).  Returns [P, N] of out_dtype (x's type, or float32); rows outside
-    the offsets are left as they were (undefined in a new tensor)."""
+    the offsets are left as they were (undefined in a new tensor).  No autograd:
+    the gradients are this call with trans and grouped_wgrad."""
     dev = x.get_device() if isinstance(x, torch.Tensor) else -1
     _like(x, _16BIT, 2, dev, "x")
     _like(w, (x.dtype,), 3, dev, "w")
@@ -541,7 +555,8 @@ def gemm_i8(xq, sx, wq, sw, offsets=None, pairs=None, k=1, out=None, out_dtype=t
 def linear_i8(x, wq, sw, offsets=None, pairs=None, k=1, out=None, out_dtype=None, ws=None):
     """gemm_i8 of the rows x (fp16, bf16 or fp32 [T, K]) coded as by
     quantize_i8 (see moeq_linear_i8).  ws: uint8 workspace tensor, or None
-    for one of the call's own.  Returns [P, N] of out_dtype (x's type)."""
+    for one of the call's own.  Returns [P, N] of out_dtype (x's type).  No
+    autograd, and no gradient of its own."""
     dev = x.get_device() if isinstance(x, torch.Tensor) else -1
     _like(x, _DTYPE, 2, dev, "x")
     T, K = x.shape
@@ -629,7 +644,8 @@ def block_norm(residual, y=None, w_pre=None, w_post=None, gate=None, alpha=1.0, 
     residual [T, H] (y's type or float32); y [T, H] fp16, bf16 or fp32, or
     None (r' is the residual itself, n of w_pre's type); w_pre, w_post [H],
     gate [H] or [T, H] of y's type, or None (ones).  res_out may be the
-    residual and n_out may be y (in place)."""
+    residual and n_out may be y (in place).  No autograd: the gradients are
+    block_norm_grad."""
     dev = _res(residual, "residual")
     dtype = y.dtype if y is not None else w_pre.dtype if w_pre is not None else residual.dtype
     d = _norm(residual, dtype, y, w_pre, w_post, gate, alpha, eps, post_norm, dev)
@@ -642,11 +658,13 @@ def block_norm(residual, y=None, w_pre=None, w_post=None, gate=None, alpha=1.0, 
     else:
         r = res_out
         _dense(r, residual.shape, residual.dtype, dev, "res_out")
+        _written(r)
     if n_out is None:
         n = torch.empty_like(residual if y is None else y, dtype=dtype)
     else:
         n = n_out
         _dense(n, residual.shape, dtype, dev, "n_out")
+        _written(n)
     _launch("moeq_block_norm", dev, d, residual.data_ptr(), _addr(y), r.data_ptr(), n.data_ptr())
     return r, n
 
