@@ -464,8 +464,9 @@ def grouped_gemm(x, w, offsets, pairs=None, k=1, trans=False, out=None, out_dtyp
     x fp16 or bf16 [T, K]; w of the same type [E, N, K] ([E, K, N] with
     trans); offsets int32 [E + 1]; pairs int32 [P] or None (out[r] from
     x[r]).  Returns [P, N] of out_dtype (x's type, or float32); rows outside
-    the offsets are left as they were (undefined in a new tensor).  No autograd:
-    the gradients are this call with trans and grouped_wgrad."""
+    the offsets are left as they were (undefined in a new tensor).  out may
+    not overlap the inputs.  No autograd: the gradients are this call with trans
+    and grouped_wgrad."""
     dev = x.get_device() if isinstance(x, torch.Tensor) else -1
     _like(x, _16BIT, 2, dev, "x")
     _like(w, (x.dtype,), 3, dev, "w")
@@ -486,7 +487,8 @@ def grouped_wgrad(dy, x, offsets, pairs=None, k=1, out=None, out_dtype=torch.flo
     """Gradient of the experts' matrices (see moeq_grouped_wgrad): out[e] =
     sum over e's sorted rows r of the outer product of dy[r] and
     x[pairs[r] // k].  dy [P, N] and x [T, K] of one 16-bit type; returns
-    [E, N, K] of out_dtype (float32 or that type)."""
+    [E, N, K] of out_dtype (float32 or that type).  out may not overlap the
+    inputs."""
     dev = dy.get_device() if isinstance(dy, torch.Tensor) else -1
     _like(dy, _16BIT, 2, dev, "dy")
     _like(x, (dy.dtype,), 2, dev, "x")
@@ -539,7 +541,7 @@ def gemm_i8(xq, sx, wq, sw, offsets=None, pairs=None, k=1, out=None, out_dtype=t
     """Products of 8-bit codes with their scales (see moeq_gemm_i8): rows xq
     int8 [T, K] with sx fp32 [T]; one matrix wq int8 [N, K] with sw [N], or
     one per expert [E, N, K] with sw [E, N] and the sorted rows of
-    grouped_gemm.  Returns [P, N]."""
+    grouped_gemm.  Returns [P, N]; out may not overlap the inputs."""
     dev = xq.get_device() if isinstance(xq, torch.Tensor) else -1
     _like(xq, (torch.int8,), 2, dev, "xq")
     T, K = xq.shape
@@ -555,8 +557,9 @@ def gemm_i8(xq, sx, wq, sw, offsets=None, pairs=None, k=1, out=None, out_dtype=t
 def linear_i8(x, wq, sw, offsets=None, pairs=None, k=1, out=None, out_dtype=None, ws=None):
     """gemm_i8 of the rows x (fp16, bf16 or fp32 [T, K]) coded as by
     quantize_i8 (see moeq_linear_i8).  ws: uint8 workspace tensor, or None
-    for one of the call's own.  Returns [P, N] of out_dtype (x's type).  No
-    autograd, and no gradient of its own."""
+    for one of the call's own; neither it nor out may overlap the inputs.
+    Returns [P, N] of out_dtype (x's type).  No autograd, and no gradient of
+    its own."""
     dev = x.get_device() if isinstance(x, torch.Tensor) else -1
     _like(x, _DTYPE, 2, dev, "x")
     T, K = x.shape
@@ -644,7 +647,9 @@ def block_norm(residual, y=None, w_pre=None, w_post=None, gate=None, alpha=1.0, 
     residual [T, H] (y's type or float32); y [T, H] fp16, bf16 or fp32, or
     None (r' is the residual itself, n of w_pre's type); w_pre, w_post [H],
     gate [H] or [T, H] of y's type, or None (ones).  res_out may be the
-    residual and n_out may be y (in place).  No autograd: the gradients are
+    residual and n_out may be y (in place); no other operands may overlap.  The
+    low-bit expert layer takes fp16 only: beside it, y and n are fp16 (the
+    residual may be float32).  No autograd: the gradients are
     block_norm_grad."""
     dev = _res(residual, "residual")
     dtype = y.dtype if y is not None else w_pre.dtype if w_pre is not None else residual.dtype

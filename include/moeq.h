@@ -510,9 +510,11 @@ moeq_status moeq_grouped_wgrad(const moeq_groups *g, const void *dy, int64_t ldd
 /*
  * moeq_quantize_i8 — symmetric 8-bit codes of every row, in fp32:
  *   a = max |x|,  scale = a / 127,  code = rint(x / scale)
- * (each quotient rounded to fp32, rint = half to even; codes in -127..127).  A row with a < 2^-118 gets codes 0 and scale 1; a row that
- * holds an infinity or a NaN gets codes 0 and scale NaN (so that what is
- * computed from it is NaN).
+ * (each quotient rounded to fp32, rint = half to even; codes in -127..127).
+ * For 16-bit x the code is that of the exact quotient 127 x / a, but for x =
+ * +-a / 2, half way between 63 and 64, where the rounded scale decides.  A row
+ * with a < 2^-118 gets codes 0 and scale 1; a row that holds an infinity or a
+ * NaN gets codes 0 and scale NaN (so that what is computed from it is NaN).
  *   x DEVICE [rows, cols] of dtype MOEQ_F16, MOEQ_BF16 or MOEQ_F32, rows
  *   below 2^22, cols up to 2^20;
  *   codes DEVICE [rows, cols] int8 out; scales DEVICE [rows] fp32 out.

@@ -123,3 +123,34 @@ def test_wide_without_a_block():
     for k in ref:
         t = tol[k] * (1 + 2.0 ** -8) + np.abs(ref[k]) * (torch.finfo(got[k].dtype).eps / 2) * (1 + 2.0 ** -6) + TINY[got[k].dtype]
         assert (np.abs(_np(got[k]) - ref[k]) <= t).all(), k
+
+
+def test_wide_gradients_captured_and_on_another_stream():
+    """A captured pass, replayed with eager work between the replays, and a
+    pass on another stream give the eager bits."""
+    from bit_quantized_moe_token_amd import moeq
+    v, d_r, d_n = _case(90, 9000, BF16, F32, "vector", True, 8)
+    v["r"][3] *= 1e25                      # (a row whose sums are formed twice)
+
+    def step():
+        g = moeq.block_norm_grad(v["r"], d_n, v["y"], d_res=d_r, w_pre=v["w_pre"], w_post=v["w_post"], gate=v["gate"], alpha=0.5)
+        return [g[k] for k in sorted(g)]
+
+    eager = [t.clone() for t in step()]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for _ in range(3):
+        for t in outs:
+            t.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, eager))
+        assert all(torch.equal(a, b) for a, b in zip(step(), eager))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        other = step()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(other, eager))
