@@ -380,7 +380,10 @@ __global__ void __launch_bounds__(norm_block(NT), 4) block_norm_grad_kernel(Norm
       const float mz = a.post ? z[0] * rh : 0.f;
       float v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = b * (d[j] - p.x[j] * b * mz);
+      for (int j = 0; j < 8; ++j) {
+        const float xb = a.post ? p.x[j] * b : 0.f;     // (without post norm y may be anything)
+        v[j] = b * (d[j] - xb * mz);
+      }
       o.pack(v);
       o.store(row_at<TY>(a.d_y, at), i, a.H - i);
     }
@@ -412,7 +415,7 @@ __device__ __forceinline__ void apply_stats(const NormArgs &a, const GradPiece<T
     const float e = st.k * off_mean(p.dn[j], p.wq[j], u, st.m) + p.dr[j], eg = e * p.gt[j];
     ov[j] = al * e;
     gv[j] = e * v * p.wp[j];
-    yv[j] = st.b * (eg * p.wp[j] - v * st.mz);
+    yv[j] = st.b * (eg * p.wp[j] - (a.post ? v : 0.f) * st.mz);   // (without post norm y may be anything)
     if constexpr (SUMS) {
       sums.v[0][j] += p.dn[j] * u;
       sums.v[1][j] += eg * v;

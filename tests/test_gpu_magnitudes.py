@@ -208,3 +208,21 @@ def test_gemm_i8_with_scales_at_the_ends_of_fp32():
     assert np.array_equal(np.isnan(y), np.isnan(ref)) and np.array_equal(np.isinf(y), large & ~np.isnan(ref))
     ok = ~np.isnan(ref) & ~large
     assert np.all(np.abs(y - ref)[ok] <= 3 * U * np.abs(ref[ok]) + 4 * 2.0 ** -150)
+
+
+@pytest.mark.parametrize("H", [40, 700, 4096, 8192, 10000])
+def test_gradient_of_a_block_without_post_norm_does_not_read_it(H):
+    """d_y = dr gate, whatever y holds, where y is not normed; d_gate is dr y."""
+    from bit_quantized_moe_token_amd import moeq
+    g = torch.Generator(device="cuda").manual_seed(H)
+    r, y, d_n, gate = (torch.randn(s, generator=g, device="cuda") for s in ((3, H), (3, H), (3, H), (H,)))
+    kw = dict(gate=gate, post_norm=False, alpha=0.5)
+    want = moeq.block_norm_grad(r, d_n, y, **kw)
+    bad = y.clone()
+    bad[1, 3], bad[1, 7], bad[2, H - 1] = float("inf"), float("-inf"), float("nan")
+    got = moeq.block_norm_grad(r, d_n, bad, **kw)
+    assert torch.equal(got["d_y"], want["d_y"]) and torch.equal(got["d_residual"], want["d_residual"])
+    same = torch.ones(H, dtype=torch.bool)
+    same[[3, 7, H - 1]] = False
+    assert torch.equal(got["d_gate"][same.cuda()], want["d_gate"][same.cuda()])
+    assert not torch.isfinite(got["d_gate"][~same.cuda()]).any()
