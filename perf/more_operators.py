@@ -88,7 +88,7 @@ def draw(rng):
     if op in ("combine", "combine_grad"):
         h, k = _size(rng, 64, 14336), rng.randint(1, 8)
         kind = rng.choice((kind, kind, "f32"))
-        c = dict(op=op, tokens=_spread(rng, 1, min(16384, 2 ** 25 // (h * k))), k=k, h=h, type=kind,
+        c = dict(op=op, tokens=_spread(rng, 1, min(16384, 2 ** 26 // (h * k * SIZE[kind]))), k=k, h=h, type=kind,
                  out=rng.choice((kind, "f32")))
         if op == "combine":
             c.update(gates=rng.random() < 0.7, base=rng.random() < 0.5)
