@@ -54,6 +54,17 @@ class Norm(ctypes.Structure):
                 ("alpha", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
+class Scoring(ctypes.Structure):
+    _fields_ = [("score", c_i32), ("renorm", c_i32), ("scale", ctypes.c_float), ("bias", c_void_p), ("groups", c_i32),
+                ("top_groups", c_i32), ("group_score", c_i32)]
+
+
+class AdaptersSet(ctypes.Structure):
+    _fields_ = [("a", c_void_p), ("b", c_void_p), ("lda", c_i64), ("stride_a", c_i64), ("ldb", c_i64), ("stride_b", c_i64),
+                ("scale", c_void_p), ("ranks", c_void_p), ("n", c_i32), ("R", c_i32), ("N", c_i32), ("K", c_i32),
+                ("dtype", c_i32)]
+
+
 # (name, restype, argtypes) of every exported entry point
 SIGNATURES = [
     ("moeq_status_string", ctypes.c_char_p, [c_i32]),
@@ -89,6 +100,17 @@ SIGNATURES = [
                                      ctypes.POINTER(ctypes.c_double), ctypes.POINTER(c_i32)]),
     ("moeq_route_mass", c_i32, [ctypes.POINTER(Routing), c_i32, c_i32, c_i32, c_void_p, c_i32, c_void_p,
                                 c_void_p, c_void_p]),
+    ("moeq_route_scored", c_i32, [ctypes.POINTER(Scoring), c_void_p, c_i64, c_i32, c_i32, c_i32, c_i32,
+                                  ctypes.POINTER(Routing), c_void_p, c_size_t, c_void_p]),
+    ("moeq_route_scored_grad", c_i32, [ctypes.POINTER(Scoring), c_void_p, c_i64, c_i32, c_i32, c_i32, c_i32, c_void_p,
+                                       c_void_p, c_void_p, c_i64, c_void_p]),
+    ("moeq_combine", c_i32, [c_void_p, c_i64, c_i32, c_i32, c_void_p, c_void_p, c_i32, c_i32, c_i32, c_void_p, c_i64,
+                             c_void_p, c_i64, c_i32, c_void_p]),
+    ("moeq_combine_grad", c_i32, [c_void_p, c_i64, c_i32, c_void_p, c_void_p, c_i32, c_i32, c_i32, c_void_p, c_i64, c_i32,
+                                  c_i32, c_void_p, c_i64, c_void_p, c_void_p]),
+    ("moeq_adapters_workspace_size", c_i32, [c_i32, c_i32, c_i32, ctypes.POINTER(c_size_t)]),
+    ("moeq_adapters", c_i32, [ctypes.POINTER(AdaptersSet), c_void_p, c_i64, c_void_p, c_i32, c_void_p, c_i64, c_void_p,
+                              c_i64, c_i32, c_void_p, c_size_t, c_void_p]),
     ("moeq_ffn_workspace_size", c_i32, [c_void_p, c_i32, c_i32, ctypes.POINTER(FfnOptions), ctypes.POINTER(c_size_t)]),
     ("moeq_expert_ffn", c_i32, [c_void_p, c_void_p, c_i32, c_i32, ctypes.POINTER(Routing), c_i32,
                                 c_void_p, c_i32, c_void_p, c_size_t, ctypes.POINTER(FfnOptions), c_void_p]),

@@ -1,0 +1,208 @@
+// The experts' rows back to their tokens, weighted by the gates, and the
+// gradients of rows and gates.
+#include "check.hpp"
+#include "vec8.hpp"
+
+namespace moeq {
+
+constexpr int kCombineThreads = 256;
+constexpr int kMaxSlots = 256;   // pairs per token
+
+struct CombineArgs {
+  const void *rows;      // [P, N]
+  const int32_t *pos;    // [T * k]
+  const float *gates;    // [T * k] or null (ones)
+  const void *tok;       // base [T, N] or null; gradient: dy [T, N]
+  void *out;             // [T, N]; gradient: d_rows [P, N]
+  float *d_gates;        // gradient: [T * k] or null
+  int64_t ldr, ldt, ldo;
+  int T, k, N, P;
+  int lanes;             // forward: log2 of the threads along a row
+};
+
+// TR: type of the rows, TO: of base and out.  2^lanes threads along a row,
+// eight columns each.
+template <int TR, int TO>
+__global__ void __launch_bounds__(kCombineThreads)
+combine_kernel(CombineArgs a) {
+  const int t = blockIdx.x * (kCombineThreads >> a.lanes) + (threadIdx.x >> a.lanes);
+  const int c = ((blockIdx.y << a.lanes) + (threadIdx.x & ((1 << a.lanes) - 1))) * 8;
+  const int n = a.N - c;
+  if (t >= a.T || n <= 0) return;
+  float acc[8];
+  if (a.tok) {
+    Oct<TO> b;
+    b.load(a.tok, t * a.ldt + c, n);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = b[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+  }
+  for (int j = 0; j < a.k; ++j) {
+    const int64_t p = (int64_t)t * a.k + j;
+    const int at = a.pos[p];
+    if ((uint32_t)at >= (uint32_t)a.P) continue;
+    const float g = a.gates ? a.gates[p] : 1.f;
+    Oct<TR> r;
+    r.load(a.rows, at * a.ldr + c, n);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] += g * r[i];
+  }
+  Oct<TO> o;
+  o.pack(acc);
+  o.store(a.out, t * a.ldo + c, n);
+}
+
+// One workgroup per token: for every slot its row's gradient and the product
+// of its row with dy.
+template <int TR, int TO>
+__global__ void __launch_bounds__(kCombineThreads)
+combine_grad_kernel(CombineArgs a) {
+  __shared__ float part[kCombineThreads / kWave];
+  const int t = blockIdx.x, tid = threadIdx.x;
+  for (int j = 0; j < a.k; ++j) {
+    const int64_t p = (int64_t)t * a.k + j;
+    const int at = a.pos[p];
+    const bool ok = (uint32_t)at < (uint32_t)a.P;
+    const float g = a.gates ? a.gates[p] : 1.f;
+    float dot = 0.f;
+    for (int c = tid * 8; ok && c < a.N; c += kCombineThreads * 8) {
+      const int n = a.N - c;
+      Oct<TO> d;
+      d.load(a.tok, t * a.ldt + c, n);
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = g * d[i];
+      if (a.d_gates) {
+        Oct<TR> r;
+        r.load(a.rows, at * a.ldr + c, n);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dot += d[i] * r[i];
+      }
+      Oct<TR> o;
+      o.pack(v);
+      o.store(a.out, at * a.ldo + c, n);
+    }
+    if (a.d_gates) {
+#pragma unroll
+      for (int m = 32; m >= 1; m >>= 1) dot += __shfl_xor(dot, m, kWave);
+      if ((tid & 63) == 0) part[tid >> 6] = dot;
+      __syncthreads();
+      if (tid == 0) {
+        float s = 0.f;
+        for (int w = 0; w < kCombineThreads / kWave; ++w) s += part[w];
+        a.d_gates[p] = s;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+template <int TR, int TO>
+static void launch_combine(CombineArgs a, bool grad, hipStream_t s) {
+  if (grad) {
+    hipLaunchKernelGGL((combine_grad_kernel<TR, TO>), dim3(a.T), dim3(kCombineThreads), 0, s, a);
+    return;
+  }
+  a.lanes = 0;
+  while (a.lanes < 8 && (8 << a.lanes) < a.N) ++a.lanes;
+  const int per = kCombineThreads >> a.lanes, cols = 8 << a.lanes;
+  hipLaunchKernelGGL((combine_kernel<TR, TO>), dim3((a.T + per - 1) / per, (a.N + cols - 1) / cols), dim3(kCombineThreads), 0,
+                     s, a);
+}
+
+static void launch_combine_types(const CombineArgs &a, int tr, int to, bool grad, hipStream_t s) {
+  if (tr == MOEQ_F16) {
+    if (to == MOEQ_F16) launch_combine<MOEQ_F16, MOEQ_F16>(a, grad, s);
+    else launch_combine<MOEQ_F16, MOEQ_F32>(a, grad, s);
+  } else if (tr == MOEQ_BF16) {
+    if (to == MOEQ_BF16) launch_combine<MOEQ_BF16, MOEQ_BF16>(a, grad, s);
+    else launch_combine<MOEQ_BF16, MOEQ_F32>(a, grad, s);
+  } else {
+    if (to == MOEQ_F16) launch_combine<MOEQ_F32, MOEQ_F16>(a, grad, s);
+    else if (to == MOEQ_BF16) launch_combine<MOEQ_F32, MOEQ_BF16>(a, grad, s);
+    else launch_combine<MOEQ_F32, MOEQ_F32>(a, grad, s);
+  }
+}
+
+static moeq_status check_combine(const char *who, int32_t P, int32_t dtype, const int32_t *pos, const float *gates,
+                                 int32_t T, int32_t k, int32_t N, int32_t other) {
+  if (T < 0 || P < 0) return fail(MOEQ_ERR_INVALID, "%s: negative T=%d or P=%d", who, T, P);
+  if (k < 1 || k > kMaxSlots) return fail(MOEQ_ERR_INVALID, "%s: k=%d not in 1..%d", who, k, kMaxSlots);
+  if (T > kMaxTokens || P > kMaxRows || (int64_t)T * k > kMaxRows)
+    return fail(MOEQ_ERR_UNSUPPORTED, "%s: T=%d above %d, or P=%d or T*k above %d", who, T, kMaxTokens, P, kMaxRows);
+  MOEQ_TRY(check_len(who, "N", N, kMaxLen));
+  if (!okout(dtype)) return fail(MOEQ_ERR_INVALID, "%s: bad dtype %d", who, dtype);
+  if (!okout(other) || (other != dtype && other != MOEQ_F32 && dtype != MOEQ_F32))
+    return fail(MOEQ_ERR_INVALID, "%s: dtype %d beside rows of dtype %d", who, other, dtype);
+  if (T && (!pos || ((uintptr_t)pos & 3))) return fail(MOEQ_ERR_INVALID, "%s: null or misaligned pair_pos", who);
+  if ((uintptr_t)gates & 3) return fail(MOEQ_ERR_INVALID, "%s: misaligned gates", who);
+  return MOEQ_OK;
+}
+
+}  // namespace moeq
+
+using namespace moeq;
+
+MOEQ_API moeq_status moeq_combine(const void *rows, int64_t ldr, int32_t P, int32_t dtype, const int32_t *pair_pos,
+                                  const float *gates, int32_t T, int32_t k, int32_t N, const void *base, int64_t ldb,
+                                  void *out, int64_t ldo, int32_t out_dtype, hipStream_t stream) {
+  const char *who = "combine";
+  MOEQ_TRY(check_combine(who, P, dtype, pair_pos, gates, T, k, N, out_dtype));
+  if (!T) return MOEQ_OK;
+  if (P) MOEQ_TRY(check_matrix(who, "rows", rows, ldr, N, dtype));
+  if (base) MOEQ_TRY(check_matrix(who, "base", base, ldb, N, out_dtype));
+  MOEQ_TRY(check_matrix(who, "out", out, ldo, N, out_dtype));
+  CombineArgs a{};
+  a.rows = rows;
+  a.pos = pair_pos;
+  a.gates = gates;
+  a.tok = base;
+  a.out = out;
+  a.ldr = ldr;
+  a.ldt = ldb;
+  a.ldo = ldo;
+  a.T = T;
+  a.k = k;
+  a.N = N;
+  a.P = P;
+  prof_begin("combine", stream);
+  launch_combine_types(a, dtype, out_dtype, false, stream);
+  prof_end("combine", stream);
+  return check_launch("combine");
+}
+
+MOEQ_API moeq_status moeq_combine_grad(const void *dy, int64_t ldy, int32_t dy_dtype, const int32_t *pair_pos,
+                                       const float *gates, int32_t T, int32_t k, int32_t N, const void *rows,
+                                       int64_t ldr, int32_t P, int32_t dtype, void *d_rows, int64_t ldd, float *d_gates,
+                                       hipStream_t stream) {
+  const char *who = "combine_grad";
+  MOEQ_TRY(check_combine(who, P, dtype, pair_pos, gates, T, k, N, dy_dtype));
+  if (d_gates && !gates) return fail(MOEQ_ERR_INVALID, "%s: d_gates without gates", who);
+  if ((uintptr_t)d_gates & 3) return fail(MOEQ_ERR_INVALID, "%s: misaligned d_gates", who);
+  if (!T) return MOEQ_OK;
+  MOEQ_TRY(check_matrix(who, "dy", dy, ldy, N, dy_dtype));
+  if (P) {
+    if (d_gates) MOEQ_TRY(check_matrix(who, "rows", rows, ldr, N, dtype));
+    MOEQ_TRY(check_matrix(who, "d_rows", d_rows, ldd, N, dtype));
+  }
+  CombineArgs a{};
+  a.rows = rows;
+  a.pos = pair_pos;
+  a.gates = gates;
+  a.tok = dy;
+  a.out = d_rows;
+  a.d_gates = d_gates;
+  a.ldr = ldr;
+  a.ldt = ldy;
+  a.ldo = ldd;
+  a.T = T;
+  a.k = k;
+  a.N = N;
+  a.P = P;
+  prof_begin("combine_grad", stream);
+  launch_combine_types(a, dtype, dy_dtype, true, stream);
+  prof_end("combine_grad", stream);
+  return check_launch("combine_grad");
+}

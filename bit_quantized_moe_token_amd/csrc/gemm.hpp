@@ -14,14 +14,12 @@
 // consecutive i of one j: outputs leave in 8- or 16-byte stores.
 #pragma once
 #include <type_traits>
-#include "common.hpp"
+#include "check.hpp"
 
 namespace moeq {
 
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-
-constexpr int kI8 = 3;   // element type of the 8-bit products, beside MOEQ_F16 and MOEQ_BF16
 
 enum GemmMode { kFwd = 0, kRows = 1, kMats = 2 };   // see above
 

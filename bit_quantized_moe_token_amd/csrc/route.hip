@@ -259,6 +259,21 @@ route_mass_kernel(const float *__restrict__ gates, const int32_t *__restrict__ o
   }
 }
 
+size_t route_ws_bytes(int T, int E) { return T > kScanMinTokens ? (size_t)route_segments(T) * E * 4 : 0; }
+
+void launch_place(const int32_t *ids, int T, int E, int k, int32_t *offsets, int32_t *sorted_pairs, int32_t *pair_pos,
+                  void *ws, hipStream_t stream) {
+  const int nseg = route_segments(T);
+  int32_t *hist = nullptr;
+  if (T > kScanMinTokens) {
+    hist = static_cast<int32_t *>(ws);
+    hipLaunchKernelGGL(route_count_kernel, dim3(nseg), dim3(kSegThreads), 0, stream, ids, T, E, k, hist);
+    hipLaunchKernelGGL(route_scan_kernel, dim3(1), dim3(kMaxE), 0, stream, nseg, E, hist, offsets);
+  }
+  hipLaunchKernelGGL(route_place_kernel, dim3(nseg), dim3(kSegThreads), 0, stream, ids, T, E, k, offsets, sorted_pairs,
+                     pair_pos, (const int32_t *)hist);
+}
+
 }  // namespace moeq
 
 using namespace moeq;
@@ -269,9 +284,6 @@ using namespace moeq;
 // workspace is needed only beyond kScanMinTokens tokens.
 constexpr int kRouteSingleMax = kRouteTokens;
 static inline bool route_single(int T) { return T <= kRouteSingleMax; }
-static inline size_t route_ws_bytes(int T, int E) {
-  return T > kScanMinTokens ? (size_t)route_segments(T) * E * 4 : 0;
-}
 
 MOEQ_API moeq_status moeq_route_workspace_size(int32_t T, int32_t E, int32_t k, size_t *bytes) {
   if (!bytes) return fail(MOEQ_ERR_INVALID, "route_workspace_size: null output");
@@ -295,21 +307,13 @@ MOEQ_API moeq_status moeq_route(const float *logits, int32_t T, int32_t E, int32
   if (need > 0 && (!ws || ws_bytes < need))
     return fail(MOEQ_ERR_WORKSPACE, "route: workspace has %zu bytes, needs %zu", ws_bytes, need);
   prof_begin("route", stream);
-  const int nseg = route_segments(T);
   if (route_single(T)) {
     const RouteOut o{logits, out->topk_ids, out->topk_gates, out->expert_offsets, out->sorted_pairs, out->pair_pos};
     hipLaunchKernelGGL(route_kernel, dim3(1), dim3(kRouteThreads), 0, stream, o, T, E, k);
   } else {
     hipLaunchKernelGGL(route_topk_kernel, dim3((T + kTopkWaves - 1) / kTopkWaves), dim3(kTopkThreads), 0, stream,
                        logits, T, E, k, out->topk_ids, out->topk_gates);
-    int32_t *hist = nullptr;
-    if (need > 0) {
-      hist = static_cast<int32_t *>(ws);
-      hipLaunchKernelGGL(route_count_kernel, dim3(nseg), dim3(kSegThreads), 0, stream, out->topk_ids, T, E, k, hist);
-      hipLaunchKernelGGL(route_scan_kernel, dim3(1), dim3(kMaxE), 0, stream, nseg, E, hist, out->expert_offsets);
-    }
-    hipLaunchKernelGGL(route_place_kernel, dim3(nseg), dim3(kSegThreads), 0, stream, out->topk_ids, T, E, k,
-                       out->expert_offsets, out->sorted_pairs, out->pair_pos, (const int32_t *)hist);
+    launch_place(out->topk_ids, T, E, k, out->expert_offsets, out->sorted_pairs, out->pair_pos, ws, stream);
   }
   prof_end("route", stream);
   return check_launch("route");

@@ -138,28 +138,19 @@ struct RouteOut {
   int32_t *pair_pos;
 };
 
-// Routing of up to kRouteTokens tokens by one workgroup of NTH threads
-// (every thread of the workgroup calls it).
-// Phase 1: top-k + gates, kRouteTokens / NW tokens per wave; the histogram
-//          and the ids also go to LDS, so the later phases read nothing
-//          back from memory.
-// Phase 2: exclusive scan of the histogram -> expert offsets.
-// Phase 3: pairs in chunks of NTH in ascending pair id; a pair's rank among
+// The counting sort of up to kRouteTokens tokens whose expert ids (s.ids) and
+// their histogram (s.count; s.run zeroed) stand in LDS, by one workgroup of
+// NTH threads (every thread of the workgroup calls it).
+// Phase 1: exclusive scan of the histogram -> expert offsets.
+// Phase 2: pairs in chunks of NTH in ascending pair id; a pair's rank among
 //          equal experts inside its wave comes from ballots over the expert
 //          id bits (peer mask); across waves and chunks from per-wave
 //          counters in LDS.  Every slot is computed, none is found by
 //          atomics, so the result is deterministic.
 template <int NTH>
-__device__ __forceinline__ void route_block(const RouteOut &o, int T, int E, int k, RouteLds<NTH / kWave> &s) {
+__device__ __forceinline__ void place_block(const RouteOut &o, int T, int E, int k, RouteLds<NTH / kWave> &s) {
   constexpr int NW = NTH / kWave;
-  static_assert(kRouteTokens % NW == 0, "each wave takes the same number of tokens");
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  for (int e = tid; e < kMaxE; e += NTH) { s.count[e] = 0; s.run[e] = 0; }
-  __syncthreads();
-
-  topk_tokens<kRouteTokens / NW>(o.logits, wave, T, NW, E, k, o.ids, o.gates, s.count, s.ids);
-  __syncthreads();
-
   const int P = T * k;
   if (wave == 0) {
     int carry = 0;
@@ -213,5 +204,28 @@ __device__ __forceinline__ void route_block(const RouteOut &o, int T, int E, int
     __syncthreads();
   }
 }
+
+// Routing of up to kRouteTokens tokens by one workgroup of NTH threads
+// (every thread of the workgroup calls it): top-k + gates, kRouteTokens / NW
+// tokens per wave; the histogram and the ids also go to LDS, so the placement
+// reads nothing back from memory.
+template <int NTH>
+__device__ __forceinline__ void route_block(const RouteOut &o, int T, int E, int k, RouteLds<NTH / kWave> &s) {
+  constexpr int NW = NTH / kWave;
+  static_assert(kRouteTokens % NW == 0, "each wave takes the same number of tokens");
+  const int tid = threadIdx.x, wave = tid >> 6;
+  for (int e = tid; e < kMaxE; e += NTH) { s.count[e] = 0; s.run[e] = 0; }
+  __syncthreads();
+
+  topk_tokens<kRouteTokens / NW>(o.logits, wave, T, NW, E, k, o.ids, o.gates, s.count, s.ids);
+  __syncthreads();
+  place_block<NTH>(o, T, E, k, s);
+}
+
+// The counting sort of T * k pairs by their experts ids, T >= 1 (kernels of
+// route.hip); ws: route_ws_bytes bytes.
+size_t route_ws_bytes(int T, int E);
+void launch_place(const int32_t *ids, int T, int E, int k, int32_t *offsets, int32_t *sorted_pairs, int32_t *pair_pos,
+                  void *ws, hipStream_t stream);
 
 }  // namespace moeq

@@ -6,8 +6,8 @@ the library filled.  No arithmetic of the method happens here.
 
 The functions record nothing for autograd: what they return does not require
 grad, whatever their inputs do.  Gradients are calls of their own
-(grouped_gemm with trans, grouped_wgrad, block_norm_grad), for an
-autograd.Function of the caller's to make.
+(grouped_gemm with trans, grouped_wgrad, route_scored_grad, combine_grad,
+block_norm_grad), for an autograd.Function of the caller's to make.
 """
 
 import ctypes
@@ -580,6 +580,212 @@ def linear_i8_workspace_size(T, K):
     _sizes(T=T, K=K)
     n = ctypes.c_size_t(0)
     check(lib().moeq_linear_i8_workspace_size(T, K, ctypes.byref(n)), "moeq_linear_i8_workspace_size")
+    return n.value
+
+
+# ------------------------------ routing by scores, rows back to tokens
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_GROUP_SCORES = {"max": 0, "top2": 1}
+
+
+def _name(names, value, what):
+    v = names.get(value)
+    if v is None:
+        raise ValueError(f"{what} must be one of {tuple(names)}, got {value!r}")
+    return v
+
+
+def route_scored(logits, k, score="softmax", bias=None, groups=1, top_groups=None, group_score="max", renorm=True,
+                 scale=1.0, out=None):
+    """Routing of logits [T, E] (fp16, bf16 or fp32) by their scores (see
+    moeq_scoring, moeq_route_scored): the k experts with the largest score +
+    bias, ties to the lower id, with gates scale * score, divided by the k
+    scores' sum with renorm; and the counting sort of route.
+
+    score: "softmax" (over all E) or "sigmoid".  bias: fp32 [E] or None, for
+    the choice only.  groups > 1: the experts stand in that many groups of
+    consecutive ones, and only the top_groups best groups (default: all) are
+    chosen from, by their largest choice (group_score "max") or the sum of
+    their two largest ("top2").  A logit of -infinity takes its expert out.
+    Returns a RoutingOut (out, if given).  No autograd: the logits' gradient is
+    route_scored_grad."""
+    dev = logits.get_device() if isinstance(logits, torch.Tensor) else -1
+    _like(logits, _DTYPE, 2, dev, "logits")
+    T, E = logits.shape
+    if bias is not None:
+        _flat(bias, E, torch.float32, dev, "bias")
+    top_groups = groups if top_groups is None else top_groups
+    if T > 0x7fffffff or k > 0x7fffffff or groups > 0x7fffffff or top_groups > 0x7fffffff:
+        _sizes(T=T, k=k, groups=groups, top_groups=top_groups)
+    d = _lib.Scoring(_name(_SCORES, score, "score"), bool(renorm), scale, _addr(bias), groups, top_groups,
+                     _name(_GROUP_SCORES, group_score, "group_score"))
+    if out is None:
+        out = RoutingOut(T, E, k, logits.device)
+    elif (out.T, out.E, out.k) != (T, E, k) or out.ids.get_device() != dev:
+        raise ValueError(f"out is a routing of {(out.T, out.E, out.k)}, not of {(T, E, k)} on the logits' device")
+    else:
+        for t in (out.ids, out.gates, out.offsets, out.sorted_pairs, out.pair_pos):
+            _written(t)
+    _launch("moeq_route_scored", dev, d, logits.data_ptr(), _ld(logits), _DTYPE[logits.dtype], T, E, k, out.c,
+            out.ws.data_ptr(), out.ws_bytes)
+    return out
+
+
+def route_scored_grad(logits, ids, d_gates, score="softmax", renorm=True, scale=1.0, out=None):
+    """Gradient of the logits [T, E] from that of the gates (d_gates fp32
+    [T, k]) of route_scored's experts ids [T, k] (see moeq_route_scored_grad).
+    Returns [T, E] of the logits' type; out may be the logits (in place)."""
+    dev = logits.get_device() if isinstance(logits, torch.Tensor) else -1
+    _like(logits, _DTYPE, 2, dev, "logits")
+    T, E = logits.shape
+    _like(ids, (torch.int32,), 2, dev, "ids")
+    k = ids.shape[1]
+    _dense(ids, (T, k), torch.int32, dev, "ids")
+    _dense(d_gates, (T, k), torch.float32, dev, "d_gates")
+    if T > 0x7fffffff or E > 0x7fffffff or k > 0x7fffffff:
+        _sizes(T=T, E=E, k=k)
+    d = _lib.Scoring(_name(_SCORES, score, "score"), bool(renorm), scale, None, 1, 1, 0)
+    out = _out(out, (T, E), logits.dtype, (logits.dtype,), dev, logits)
+    _launch("moeq_route_scored_grad", dev, d, logits.data_ptr(), _ld(logits), _DTYPE[logits.dtype], T, E, k,
+            ids.data_ptr(), d_gates.data_ptr(), out.data_ptr(), _ld(out))
+    return out
+
+
+def _pairs_of(pair_pos, gates, k, dev):
+    """(tokens, pairs per token) of the positions pair_pos [T * k]."""
+    _like(pair_pos, (torch.int32,), 1, dev, "pair_pos")
+    if gates is not None:
+        _like(gates, (torch.float32,), 2, dev, "gates")
+        if not gates.is_contiguous():
+            raise ValueError("gates must be contiguous")
+        if k is not None and k != gates.shape[1]:
+            raise ValueError(f"k={k} beside gates of shape {tuple(gates.shape)}")
+        T, k = gates.shape
+    elif k is None:
+        raise ValueError("k is needed without gates")
+    else:
+        T = pair_pos.shape[0] // k if k > 0 else -1
+    if T * k != pair_pos.shape[0]:
+        raise ValueError(f"pair_pos has {pair_pos.shape[0]} positions, not {k} for each of {T} tokens")
+    return T, k
+
+
+def _beside(dtype):
+    """Types of a token's rows beside expert-sorted rows of `dtype`."""
+    return tuple(_DTYPE) if dtype == torch.float32 else (dtype, torch.float32)
+
+
+def combine(rows, pair_pos, gates=None, k=None, base=None, out=None, out_dtype=None):
+    """The experts' rows back to their tokens (see moeq_combine): out[t] =
+    base[t] + the sum over j < k of gates[t, j] * rows[pair_pos[t * k + j]].
+
+    rows [P, N] fp16, bf16 or fp32 in expert order; pair_pos int32 [T * k] (of
+    a routing; a position outside [0, P) adds nothing); gates fp32 [T, k], or
+    None (ones) with k given; base [T, N] of out's type or None.  Returns
+    [T, N] of out_dtype (base's or the rows' type, or float32; any of the three
+    for fp32 rows).  out may be base (in place), and may overlap nothing else.
+    No autograd: the gradients are combine_grad."""
+    dev = rows.get_device() if isinstance(rows, torch.Tensor) else -1
+    _like(rows, _DTYPE, 2, dev, "rows")
+    P, N = rows.shape
+    T, k = _pairs_of(pair_pos, gates, k, dev)
+    out = _out(out, (T, N), out_dtype or (rows.dtype if base is None else base.dtype), _beside(rows.dtype), dev, rows)
+    if base is not None:
+        _like(base, (out.dtype,), 2, dev, "base")
+        if base.shape != out.shape:
+            raise ValueError(f"base must have shape {tuple(out.shape)}, got {tuple(base.shape)}")
+    if P > 0x7fffffff or T > 0x7fffffff or N > 0x7fffffff:
+        _sizes(P=P, T=T, N=N)
+    _launch("moeq_combine", dev, rows.data_ptr(), _ld(rows), P, _DTYPE[rows.dtype], pair_pos.data_ptr(), _addr(gates), T, k,
+            N, _addr(base), _ld(base) if base is not None else 0, out.data_ptr(), _ld(out), _DTYPE[out.dtype])
+    return out
+
+
+def combine_grad(dy, pair_pos, gates=None, rows=None, k=None, out=None, out_dtype=None):
+    """Gradients of combine's inputs from that of its output, dy [T, N] (see
+    moeq_combine_grad): (d_rows, d_gates) with d_rows[pair_pos[p]] = gates[p] *
+    dy[p // k] and d_gates[p] = dy[p // k] . rows[pair_pos[p]].
+
+    rows [P, N] as combine took them, or None: P = T * k (or out's rows), and
+    d_gates is None, as it is without gates.  d_rows has the rows' type (out_dtype, or dy's,
+    without rows); rows of it that no pair points at are left as they were
+    (undefined in a new tensor).  No position may occur twice.  The gradient of
+    base is dy.  out may not overlap the inputs."""
+    dev = dy.get_device() if isinstance(dy, torch.Tensor) else -1
+    _like(dy, _DTYPE, 2, dev, "dy")
+    T, k = _pairs_of(pair_pos, gates, k, dev)
+    N = dy.shape[1]
+    if dy.shape[0] != T:
+        raise ValueError(f"dy has {dy.shape[0]} rows for {T} tokens")
+    dtype = rows.dtype if rows is not None else out_dtype or (out.dtype if out is not None else dy.dtype)
+    if rows is not None:
+        _like(rows, _DTYPE, 2, dev, "rows")
+        if rows.shape[1] != N:
+            raise ValueError(f"rows have {rows.shape[1]} columns, dy {N}")
+        if out_dtype not in (None, dtype):
+            raise TypeError(f"d_rows has the rows' type {dtype}, not {out_dtype}")
+    if dtype not in _DTYPE or dy.dtype not in _beside(dtype):
+        raise TypeError(f"dy of {dy.dtype} beside rows of {dtype}")
+    P = rows.shape[0] if rows is not None else T * k if out is None else out.shape[0]
+    out = _out(out, (P, N), dtype, (dtype,), dev, dy)
+    d_gates = torch.empty_like(gates) if rows is not None and gates is not None else None
+    if P > 0x7fffffff or T > 0x7fffffff or N > 0x7fffffff:
+        _sizes(P=P, T=T, N=N)
+    _launch("moeq_combine_grad", dev, dy.data_ptr(), _ld(dy), _DTYPE[dy.dtype], pair_pos.data_ptr(), _addr(gates), T, k, N,
+            _addr(rows), _ld(rows) if rows is not None else 0, P, _DTYPE[dtype], out.data_ptr(), _ld(out), _addr(d_gates))
+    return out, d_gates
+
+
+# ------------------------------------------------- adapters of requests
+
+def adapters(x, a, b, ids, y, scale=None, ranks=None, out=None, ws=None):
+    """Low-rank adapters of the rows' requests beside a projection y of the
+    rows x (see moeq_adapters): out[r] = y[r] + scale[i] * b[i] @ (a[i] @ x[r])
+    for i = ids[r], and y[r] where ids[r] is no adapter (-1, say).
+
+    x fp16 or bf16 [T, K]; a [n, R, K] and b [n, N, R] of the same type; ids
+    int32 [T]; y [T, N] of that type or float32 (linear_i8 or grouped_gemm of
+    the same x, or the expert layer's); scale fp32 [n] or None (ones); ranks
+    int32 [n] or None (R): how much of R counts.  Returns [T, N] of y's type;
+    out may be y (in place).  ws: uint8 workspace tensor, or None for one of
+    the call's own; neither it nor out may overlap the other inputs.  No
+    autograd, and no gradient of its own."""
+    dev = x.get_device() if isinstance(x, torch.Tensor) else -1
+    _like(x, _16BIT, 2, dev, "x")
+    dtype, (T, K) = x.dtype, x.shape
+    _like(a, (dtype,), 3, dev, "a")
+    _like(b, (dtype,), 3, dev, "b")
+    (n, R, Ka), N = a.shape, b.shape[1]
+    if Ka != K or b.shape[0] != n or b.shape[2] != R:
+        raise ValueError(f"a of {tuple(a.shape)} and b of {tuple(b.shape)} are no adapters for {K} columns")
+    _flat(ids, T, torch.int32, dev, "ids")
+    _like(y, (dtype, torch.float32), 2, dev, "y")
+    if y.shape[0] != T or y.shape[1] != N:
+        raise ValueError(f"y must have shape {(T, N)}, got {tuple(y.shape)}")
+    if scale is not None:
+        _flat(scale, n, torch.float32, dev, "scale")
+    if ranks is not None:
+        _flat(ranks, n, torch.int32, dev, "ranks")
+    out = _out(out, (T, N), y.dtype, (y.dtype,), dev, y)
+    if ws is None:
+        ws = x.new_empty((adapters_workspace_size(T, R, K),), dtype=torch.uint8)
+    else:
+        _like(ws, (torch.uint8,), 1, dev, "ws")
+    if n > 0x7fffffff or N > 0x7fffffff:
+        _sizes(n=n, N=N)
+    s = _lib.AdaptersSet(a.data_ptr(), b.data_ptr(), _ld(a), a.stride(0), _ld(b), b.stride(0), _addr(scale), _addr(ranks), n, R,
+                         N, K, _DTYPE[dtype])
+    _launch("moeq_adapters", dev, s, x.data_ptr(), _ld(x), ids.data_ptr(), T, y.data_ptr(), _ld(y), out.data_ptr(), _ld(out),
+            _DTYPE[y.dtype], ws.data_ptr(), ws.numel())
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def adapters_workspace_size(T, R, K):
+    _sizes(T=T, R=R, K=K)
+    n = ctypes.c_size_t(0)
+    check(lib().moeq_adapters_workspace_size(T, R, K, ctypes.byref(n)), "moeq_adapters_workspace_size")
     return n.value
 
 

@@ -366,6 +366,108 @@ moeq_status moeq_route_mass(const moeq_routing *r, int32_t T, int32_t E, int32_t
                             const float *edges, int32_t n_edges, float *mass, int32_t *bucket,
                             hipStream_t stream);
 
+/*
+ * moeq_scoring — how moeq_route_scored turns logits into a choice of experts
+ * and their gates.  Per token, with logits l over E experts:
+ *   scores   s_e = softmax(l)_e over all E, or 1 / (1 + exp(-l_e))
+ *   choice   c_e = s_e + bias_e, formed in 64 bits; without a bias the
+ *            choices are in the order of the logits.  The bias (as balancing
+ *            the experts' load leaves it) changes the choice, not the gates.
+ *   groups   E / groups consecutive experts each; a group counts as much as
+ *            its largest choice (MOEQ_GROUP_MAX) or as the sum of its two
+ *            largest (MOEQ_GROUP_TOP2; without a bias, of its two largest
+ *            scores); the top_groups largest groups stay, ties to the lower
+ *            group.
+ *   experts  the k largest choices within those groups, by descending
+ *            choice, ties to the lower expert id
+ *   gates    g_j = scale * s_j, with renorm scale * s_j / sum_i s_i over the k
+ *            chosen (0 where that sum is 0)
+ * A logit of -infinity (or NaN) takes its expert out: score 0, chosen only
+ * when no other expert is left in the token's groups, the lowest id first.
+ * Where all logits of a token are so, it gets experts 0, 1, ... and gates 0.
+ * A softmax of logits of +infinity shares the weight among these.  An expert
+ * with a NaN choice (a NaN bias) is chosen as one of -infinity.
+ *   score MOEQ_SCORE_*; renorm 0 or 1; scale finite; bias DEVICE [E] fp32 or
+ *   NULL; 1 <= top_groups <= groups <= 64, groups divides E, top_groups *
+ *   E / groups >= k; MOEQ_GROUP_TOP2 needs two experts a group (with one group
+ *   the choice among groups is none, and group_score is not looked at).
+ */
+#define MOEQ_SCORE_SOFTMAX 0
+#define MOEQ_SCORE_SIGMOID 1
+#define MOEQ_GROUP_MAX 0
+#define MOEQ_GROUP_TOP2 1
+typedef struct {
+  int32_t score, renorm;
+  float scale;
+  const float *bias;
+  int32_t groups, top_groups, group_score;
+} moeq_scoring;
+
+/*
+ * moeq_route_scored — routing by scores, into the same arrays as moeq_route
+ * (topk_ids by descending choice, topk_gates as above) with the same counting
+ * sort and the same workspace (moeq_route_workspace_size).
+ *   logits DEVICE [T, E] of dtype MOEQ_F16, MOEQ_BF16 or MOEQ_F32, rows ld
+ *   elements apart, aligned to its elements.  0 <= T < 2^22, T * k <= 2^29,
+ *   1 <= k <= E <= 256.
+ */
+moeq_status moeq_route_scored(const moeq_scoring *d, const void *logits, int64_t ld, int32_t dtype, int32_t T,
+                              int32_t E, int32_t k, const moeq_routing *out, void *ws, size_t ws_bytes,
+                              hipStream_t stream);
+
+/*
+ * moeq_route_scored_grad — gradient of the logits from that of the gates.
+ * The choice of experts has none (bias and groups are not looked at), with
+ * e_j = ids[t][j] and dg = d_gates:
+ *   v_j = scale * dg_j, with renorm scale * (dg_j - sum_i dg_i s_i / S) / S, S = sum_i s_i
+ *   softmax:  d_l_e = s_e * (sum_{j: e_j = e} v_j - sum_i v_i s_i)
+ *   sigmoid:  d_l_e = s_e * (1 - s_e) * sum_{j: e_j = e} v_j
+ * (fp32, rounded once to dtype; the chosen experts' scores in 64 bits).  A
+ * logit of -infinity or NaN gets 0; an id outside [0, E) is no expert.
+ *   logits, d_logits DEVICE [T, E] of dtype, rows ld and ldd elements apart;
+ *   ids DEVICE [T, k] int32; d_gates DEVICE [T, k] fp32.  d_logits may be
+ *   logits (in place); no other operands may overlap.
+ */
+moeq_status moeq_route_scored_grad(const moeq_scoring *d, const void *logits, int64_t ld, int32_t dtype, int32_t T,
+                                   int32_t E, int32_t k, const int32_t *ids, const float *d_gates, void *d_logits,
+                                   int64_t ldd, hipStream_t stream);
+
+/*
+ * moeq_combine — the experts' rows back to their tokens:
+ *   out[t] = base[t] + sum_{j < k} gates[t][j] * rows[pair_pos[t * k + j]]
+ * in slot order after the base, fp32 sums rounded once to out_dtype.  Without
+ * gates the rows are summed as they are (the gradient of rows that were
+ * gathered for k experts each).  A pair whose position lies outside [0, P)
+ * adds nothing.
+ *   rows DEVICE [P, N] of dtype MOEQ_F16, MOEQ_BF16 or MOEQ_F32; pair_pos
+ *   DEVICE [T * k] int32 (of a moeq_routing); gates DEVICE [T, k] fp32 or NULL;
+ *   base DEVICE [T, N] of out_dtype or NULL (zeros); out DEVICE [T, N] of
+ *   out_dtype: dtype or MOEQ_F32, any of the three for rows of MOEQ_F32.
+ *   Rows ldr, ldb, ldo elements apart, aligned to their elements; 0 <= T <
+ *   2^22, 0 <= P <= 2^29, T * k <= 2^29, 1 <= k <= 256, 1 <= N <= 2^20.  out may
+ *   be base (in place); no other operands may overlap.
+ */
+moeq_status moeq_combine(const void *rows, int64_t ldr, int32_t P, int32_t dtype, const int32_t *pair_pos,
+                         const float *gates, int32_t T, int32_t k, int32_t N, const void *base, int64_t ldb, void *out,
+                         int64_t ldo, int32_t out_dtype, hipStream_t stream);
+
+/*
+ * moeq_combine_grad — gradients of the rows and the gates from that of out
+ * (dy, of any dtype that moeq_combine takes for it; it is also base's):
+ *   d_rows[pair_pos[p]] = gates[p] * dy[p / k],  rounded once to dtype
+ *   d_gates[p] = sum_n dy[p / k, n] * rows[pair_pos[p], n],  fp32, fixed order
+ * Rows that no pair points at are left as they were; a pair whose position
+ * lies outside [0, P) writes no row and gets d_gates 0.  No position may occur
+ * twice.
+ *   gates NULL: ones (d_gates must be NULL).  rows and d_gates NULL: the
+ *   gates' gradient is not wanted.  d_rows DEVICE [P, N] of dtype; the rest
+ *   as above; outputs may not overlap inputs.
+ */
+moeq_status moeq_combine_grad(const void *dy, int64_t ldy, int32_t dy_dtype, const int32_t *pair_pos,
+                              const float *gates, int32_t T, int32_t k, int32_t N, const void *rows, int64_t ldr,
+                              int32_t P, int32_t dtype, void *d_rows, int64_t ldd, float *d_gates,
+                              hipStream_t stream);
+
 /* ---------------------------------------------------------- expert FFN -- */
 
 typedef enum {
@@ -544,6 +646,46 @@ moeq_status moeq_linear_i8_workspace_size(int32_t T, int32_t K, size_t *bytes);
 moeq_status moeq_linear_i8(const moeq_groups *g, const void *x, int64_t ldx, int32_t dtype, const int8_t *wq,
                            int64_t ldw, int64_t stride_w, const float *sw, int32_t N, int32_t K, void *y,
                            int64_t ldy, int32_t y_dtype, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------ adapters of requests -- */
+
+/*
+ * moeq_adapters_set — low-rank adapters that requests bring along, beside one
+ * linear layer [N, K] that all of them share (in 16 bits, 8 bits or packed):
+ * adapter i adds scale_i * B_i (A_i x) to the layer's output.
+ *   a DEVICE n matrices A_i [R, K], rows lda, matrices stride_a elements apart;
+ *   b DEVICE n matrices B_i [N, R], rows ldb, matrices stride_b elements apart;
+ *   both of dtype MOEQ_F16 or MOEQ_BF16; scale DEVICE [n] fp32 or NULL (ones);
+ *   ranks DEVICE [n] int32 or NULL (R): the first ranks[i] rows of A_i and
+ *   columns of B_i count, the others are not looked at (a rank outside
+ *   [0, R] is taken as the nearer end).
+ *   1 <= n <= 2^20, 1 <= R <= 256, 1 <= N, K <= 2^20.
+ */
+typedef struct {
+  const void *a, *b;
+  int64_t lda, stride_a, ldb, stride_b;
+  const float *scale;
+  const int32_t *ranks;
+  int32_t n, R, N, K, dtype;
+} moeq_adapters_set;
+
+/*
+ * moeq_adapters — out[r] = y[r] + scale_i * B_i (A_i x[r]), i = ids[r], for T
+ * rows; out[r] = y[r] where ids[r] lies outside [0, n) (a row without an
+ * adapter; its x is not read).  Rows of one adapter need not stand together,
+ * but are served in fewer passes over its matrices where they do.  A_i x is
+ * summed in fp32 and kept to 22 bits, the rest is fp32, rounded once.
+ *   x DEVICE [T, K] of the adapters' dtype; ids DEVICE [T] int32; y, out
+ *   DEVICE [T, N] of y_dtype (the adapters' dtype or MOEQ_F32); rows ldx, ldy,
+ *   ldo elements apart, aligned to their elements; 0 <= T < 2^22.  out may be
+ *   y (in place); no other operands may overlap.
+ *   ws DEVICE, 16-byte aligned, at least moeq_adapters_workspace_size bytes,
+ *   for this call alone while it runs.
+ */
+moeq_status moeq_adapters_workspace_size(int32_t T, int32_t R, int32_t K, size_t *bytes);
+moeq_status moeq_adapters(const moeq_adapters_set *s, const void *x, int64_t ldx, const int32_t *ids, int32_t T,
+                          const void *y, int64_t ldy, void *out, int64_t ldo, int32_t y_dtype, void *ws,
+                          size_t ws_bytes, hipStream_t stream);
 
 /* --------------------------------------------------- norms around a block -- */
 

@@ -53,3 +53,37 @@ def code_i8(x):
             scales[r] = a / np.float32(127)
             codes[r] = np.rint(x[r] / scales[r]).astype(np.int8)
     return codes, scales
+
+
+def combine(rows, pos, gates, base, T, k):
+    """(out [T, N], sum of its terms' magnitudes): each token's base and its
+    pairs' rows, weighted by the gates (None: ones); positions outside the
+    rows add nothing."""
+    rows = np.asarray(rows, dtype=np.float64)
+    out = np.zeros((T, rows.shape[1])) if base is None else np.array(base, dtype=np.float64)
+    mag = np.abs(out)
+    for t in range(T):
+        for j in range(k):
+            at = pos[t * k + j]
+            if 0 <= at < len(rows):
+                v = rows[at] * (1.0 if gates is None else float(gates[t, j]))
+                out[t] += v
+                mag[t] += np.abs(v)
+    return out, mag
+
+
+def combine_grad(dy, pos, gates, rows, P, d_rows0):
+    """(d_rows, d_gates, magnitudes of d_gates' sums); rows that no pair
+    points at stay d_rows0."""
+    T, k = gates.shape
+    d_rows = np.array(d_rows0, dtype=np.float64)
+    d_gates, mag = np.zeros((T, k)), np.zeros((T, k))
+    for t in range(T):
+        for j in range(k):
+            at = pos[t * k + j]
+            if 0 <= at < P:
+                d_rows[at] = float(gates[t, j]) * dy[t]
+                if rows is not None:
+                    d_gates[t, j] = dy[t] @ rows[at]
+                    mag[t, j] = np.abs(dy[t]) @ np.abs(rows[at])
+    return d_rows, d_gates, mag

@@ -1,0 +1,237 @@
+"""The adapters of many requests against the fp64 form.
+
+Bounds, per output: half a step of its type; K + 1 fp32 roundings of z = A x
+(of |A| |x|, through |B|), what z is kept to (2^-16 of the row's largest z
+beside 16-bit outputs, 2^-22 beside 32-bit ones, through |B|), R + 3 fp32
+roundings of the sum over the rank and the additions.
+"""
+
+import numpy as np
+import pytest
+
+from oracle import requests
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+TYPES = [(F16, F16), (F16, F32), (BF16, BF16), (BF16, F32)]
+IDS = lambda v: "-".join(str(d).split(".")[-1] for d in v) if isinstance(v, tuple) and isinstance(v[0], torch.dtype) else str(v)
+
+
+def _np(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+class Case:
+    def __init__(self, T, n, R, K, N, types=(F16, F16), seed=0, order="mixed"):
+        g = torch.Generator().manual_seed(seed)
+        rand = lambda *s: torch.randn(s, generator=g)
+        self.T, self.n, self.R, self.K, self.N = T, n, R, K, N
+        dt, ydt = types
+        self.x, self.y = rand(T, K).to(dt), (3 * rand(T, N)).to(ydt)
+        self.a, self.b = (rand(n, R, K) * K ** -0.5).to(dt), (0.2 * rand(n, N, R)).to(dt)
+        self.ids = torch.randint(-1, n, (T,), generator=g).int()
+        if order == "runs":
+            self.ids = self.ids.sort().values
+        self.scale = 0.5 + torch.rand((n,), generator=g)
+        self.ranks = torch.randint(0, R + 1, (n,), generator=g).int()
+
+    def check(self, got, scale=None, ranks=None):
+        ref, worst, mag = requests.adapters(_np(self.x), _np(self.a), _np(self.b), self.ids.tolist(), _np(self.y),
+                                            None if scale is None else scale.tolist(), None if ranks is None else ranks.tolist())
+        dtype = got.dtype
+        kept = 2.0 ** -22 if dtype == F32 else 2.0 ** -16
+        tol = (1.01 * torch.finfo(dtype).eps / 2 * np.abs(ref) + (self.K + 1) * 2.0 ** -24 * mag + kept * worst
+               + (self.R + 3) * 2.0 ** -24 * (mag + np.abs(_np(self.y))) + (2.0 ** -25 if dtype == F16 else 2.0 ** -126))
+        bad = ~(np.abs(_np(got) - ref) <= tol)
+        assert not bad.any(), (int(bad.sum()), float(np.nanmax(np.abs(_np(got) - ref) / tol)))
+        none = (self.ids < 0) | (self.ids >= self.n)
+        assert torch.equal(got.cpu()[none], self.y[none])
+
+    def call(self, **kw):
+        from bit_quantized_moe_token_amd import moeq
+        kw = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in kw.items()}
+        return moeq.adapters(self.x.cuda(), self.a.cuda(), self.b.cuda(), self.ids.cuda(), self.y.cuda(), **kw)
+
+
+SIZES = [(1, 1, 1, 1, 1), (1, 4, 16, 4096, 512), (1, 2, 32, 512, 4096), (2, 3, 8, 64, 64), (7, 5, 13, 100, 77),
+         (16, 16, 16, 256, 256), (17, 2, 64, 256, 130), (33, 40, 4, 136, 264), (64, 9, 33, 1000, 757), (100, 3, 128, 72, 48),
+         (5, 2, 256, 300, 40), (40, 1, 7, 2053, 33), (130, 4, 24, 96, 1032), (3, 3, 100, 31, 2050), (257, 6, 16, 128, 128)]
+
+
+@pytest.mark.parametrize("types", TYPES, ids=IDS)
+@pytest.mark.parametrize("size", SIZES, ids=str)
+def test_sizes(types, size):
+    for order in ("mixed", "runs"):
+        c = Case(*size, types=types, order=order)
+        c.check(c.call())
+        c.check(c.call(scale=c.scale, ranks=c.ranks), c.scale, c.ranks)
+
+
+@pytest.mark.parametrize("types", TYPES, ids=IDS)
+def test_longer_batches(types):
+    for T, order in ((700, "runs"), (1025, "mixed"), (2000, "runs")):
+        c = Case(T, 5, 16, 264, 328, types=types, order=order)
+        c.check(c.call(scale=c.scale), c.scale)
+
+
+@pytest.mark.parametrize("types", TYPES, ids=IDS)
+@pytest.mark.parametrize("T", [3, 150])
+def test_strides_and_alignment(types, T):
+    """Rows, matrices and bases of no alignment beyond their elements', with
+    NaN all around; in place."""
+    from bit_quantized_moe_token_amd import moeq
+
+    def inside(t, pad, at):
+        wide = torch.full((*t.shape[:-1], t.shape[-1] + pad), float("nan"), dtype=t.dtype, device="cuda")
+        wide[..., at:at + t.shape[-1]] = t.cuda()
+        return wide[..., at:at + t.shape[-1]]
+
+    for R, K, N in ((16, 128, 96), (11, 125, 99)):
+        c = Case(T, 3, R, K, N, types=types)
+        big = torch.full((7, R + 2, K + 1), float("nan"), dtype=types[0], device="cuda")
+        a = big[1::2, 1:R + 1, 1:]                      # every second matrix
+        a.copy_(c.a)
+        x, b, y, out = inside(c.x, 3, 1), inside(c.b, 5, 2), inside(c.y, 7, 3), inside(torch.zeros_like(c.y), 4, 1)
+        assert moeq.adapters(x, a, b, c.ids.cuda(), y, scale=c.scale.cuda(), out=out) is out
+        c.check(out, c.scale)
+        whole = torch.as_strided(out, (T, N + 4), (N + 4, 1), out.storage_offset() - 1)
+        assert torch.isnan(whole[:, 0]).all() and torch.isnan(whole[:, N + 1:]).all()
+        before = y._version
+        moeq.adapters(x, a, b, c.ids.cuda(), y, scale=c.scale.cuda(), out=y)
+        assert torch.equal(y, out) and y._version > before
+
+
+def test_rows_without_an_adapter_and_unused_parts_are_not_read():
+    """x of rows without an adapter, factors beyond the rank and matrices that
+    no row uses may hold anything."""
+    for T in (5, 90):
+        c = Case(T, 4, 20, 72, 56)
+        c.ids[::3] = -1
+        c.ids[1::3] = torch.tensor([4, 2 ** 30, -9])[torch.arange(len(c.ids[1::3])) % 3].int()
+        c.ids[2::3] = (torch.arange(len(c.ids[2::3])) % 2 * 2).int()
+        c.ranks = torch.tensor([5, 9, 20, 3]).int()
+        want = c.call(ranks=c.ranks)
+        c.check(want, None, c.ranks)
+        c.x[(c.ids < 0) | (c.ids > 3)] = float("nan")
+        c.a[0, 5:], c.b[0, :, 5:] = float("nan"), float("inf")
+        c.a[1], c.b[3] = float("nan"), float("nan")
+        assert torch.equal(c.call(ranks=c.ranks), want)
+        c.ranks = torch.tensor([-3, 0, 2 ** 30, 5]).int()                        # ends of the range
+        c.a[0] = float("nan")
+        got = c.call(ranks=c.ranks)
+        c.a, c.b, c.x = (torch.nan_to_num(v, 0, 0, 0) for v in (c.a, c.b, c.x))
+        c.check(got, None, c.ranks)
+
+
+@pytest.mark.parametrize("types", TYPES, ids=IDS)
+def test_magnitudes(types):
+    """z far above and below what 16 bits hold, in one batch."""
+    c = Case(40, 3, 16, 64, 64, types=types)
+    c.a[0] *= 2.0 ** 9
+    c.a[1] *= 2.0 ** -9
+    c.x[::2] *= 2.0 ** 10 if types[0] == BF16 else 2.0 ** 5
+    c.x[1::2] *= 2.0 ** -10 if types[0] == BF16 else 2.0 ** -5
+    c.b *= 2.0 ** -4
+    c.a[2, 1:] *= 2.0 ** -9                     # one large z among small ones
+    s = torch.tensor([2.0 ** -12, 2.0 ** 12, 1.0])
+    c.check(c.call(scale=s), s)
+    c.x[:] = 0
+    c.check(c.call())
+
+
+def test_infinities_stay_in_their_rows():
+    for T in (4, 60):
+        c = Case(T, 2, 8, 64, 40)
+        c.ids[:] = torch.arange(T) % 2
+        want = c.call()
+        c.x[1, 5], c.x[2, 7] = float("inf"), float("nan")
+        got = c.call()
+        keep = [r for r in range(T) if r not in (1, 2)]
+        assert torch.equal(got[keep], want[keep])
+        assert not torch.isfinite(got[1]).any() and torch.isnan(got[2]).all()
+
+
+def test_empty_and_repeated():
+    from bit_quantized_moe_token_amd import moeq
+    c = Case(60, 5, 16, 200, 120)
+    assert moeq.adapters(c.x[:0].cuda(), c.a.cuda(), c.b.cuda(), c.ids[:0].cuda(), c.y[:0].cuda()).shape == (0, 120)
+    ref = c.call()
+    ws = torch.full((moeq.adapters_workspace_size(60, 16, 200),), 255, dtype=torch.uint8).cuda()
+    for _ in range(3):
+        assert torch.equal(c.call(ws=ws), ref)               # whatever the workspace held
+    c.ids[:] = -1
+    assert torch.equal(c.call().cpu(), c.y)
+
+
+def test_adapters_beyond_32_bit_offsets():
+    """An adapter whose matrices begin beyond 2^32 bytes and elements."""
+    from bit_quantized_moe_token_amd import moeq
+    n, R, K, N = 40, 128, 1 << 20, 64
+    a = torch.zeros((n, R, K), dtype=F16, device="cuda")               # 10.7 GB
+    b = torch.zeros((n, N, R), dtype=F16, device="cuda")
+    g = torch.Generator().manual_seed(0)
+    x = torch.randint(-2, 3, (2, K), generator=g).half()
+    last = torch.zeros(R, K)
+    last[:, -8:] = torch.randint(-2, 3, (R, 8), generator=g).float()
+    last[:, :8] = torch.randint(-2, 3, (R, 8), generator=g).float()
+    a[n - 1] = last.half().cuda()
+    bl = torch.randint(-2, 3, (N, R), generator=g).float()
+    b[n - 1] = bl.half().cuda()
+    ids = torch.tensor([n - 1, 0]).int()
+    got = moeq.adapters(x.cuda(), a, b, ids.cuda(), torch.zeros(2, N).cuda())
+    want = bl @ (last @ x[0].float())
+    assert torch.equal(got[0].cpu(), want) and (got[1] == 0).all()     # whole numbers: exact
+
+
+def test_refusals():
+    from bit_quantized_moe_token_amd import moeq
+    c = Case(4, 2, 8, 16, 24)
+    good = dict(x=c.x.cuda(), a=c.a.cuda(), b=c.b.cuda(), ids=c.ids.cuda(), y=c.y.cuda())
+    moeq.adapters(**good)
+    for bad, e in ((dict(x=c.x), TypeError), (dict(x=good["x"].float()), TypeError), (dict(a=good["a"].bfloat16()), TypeError),
+                   (dict(b=good["b"][:, :, :7]), ValueError), (dict(b=good["b"][:1]), ValueError),
+                   (dict(a=good["a"][0]), ValueError), (dict(x=good["x"][:, :15]), ValueError),
+                   (dict(ids=good["ids"].long()), TypeError),
+                   (dict(ids=good["ids"][:3]), ValueError), (dict(y=good["y"][:, :23]), ValueError),
+                   (dict(y=good["y"].bfloat16()), TypeError), (dict(scale=torch.ones(3).cuda()), ValueError),
+                   (dict(scale=torch.ones(2).half().cuda()), TypeError), (dict(ranks=torch.ones(2).cuda()), TypeError),
+                   (dict(out=torch.zeros(4, 24).cuda()), TypeError), (dict(out=torch.zeros(3, 24).half().cuda()), ValueError),
+                   (dict(a=good["a"].transpose(1, 2).contiguous().transpose(1, 2)), ValueError),
+                   (dict(ws=torch.zeros(64)), TypeError)):
+        with pytest.raises(e):
+            moeq.adapters(**dict(good, **bad))
+    with pytest.raises(moeq.MoeqError):
+        moeq.adapters(**good, ws=torch.zeros(16, dtype=torch.uint8).cuda())
+    with pytest.raises(moeq.MoeqError):
+        moeq.adapters(**good, out=good["y"][:1].expand(4, 24))
+
+
+def test_two_streams_and_captured_calls():
+    sets = [Case(T, 7, 16, 512, 640, seed=T, types=(BF16, BF16)) for T in (3, 48, 900)]
+    from bit_quantized_moe_token_amd import moeq
+    ops = [[t.cuda() for t in (c.x, c.a, c.b, c.ids, c.y)] for c in sets]
+    ref = [moeq.adapters(*o).clone() for o in ops]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in sets], []
+    for _ in range(3):
+        for o, st in zip(ops, streams):
+            with torch.cuda.stream(st):
+                got.append(moeq.adapters(*o))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert torch.equal(g, ref[i % 3])
+    graphs = []
+    for o in ops:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = moeq.adapters(*o)
+        graphs.append((g, out))
+    for _ in range(3):
+        for (g, out), o, r in zip(graphs, ops, ref):
+            out.zero_()
+            torch.cuda.synchronize()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, r) and torch.equal(moeq.adapters(*o), r)
