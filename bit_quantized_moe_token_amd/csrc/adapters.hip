@@ -8,10 +8,8 @@ namespace moeq {
 constexpr int kAdaptersMaxR = 256;
 constexpr int kAdaptersMaxN = 1 << 20;
 
-constexpr int kThreads = 256, kWaves = kThreads / kWave;
 constexpr int kRows = 16;        // rows (tokens) of an MFMA tile
 constexpr int kChunk = 64;       // columns of x and A that a wave takes at a time: 128 bytes of a row
-constexpr int kCols = 256;       // outputs of a workgroup of the second kernel: 64 a wave
 
 struct AdapterArgs {
   const void *x, *a, *b, *y;
@@ -22,7 +20,8 @@ struct AdapterArgs {
   int64_t ldx, lda, stride_a, ldb, stride_b, ldy, ldo;
   int T, n, R, N, K;
   int splits, per;       // parts of K, chunks of each
-  int slots;             // workgroups that share the adapters of a tile
+  int width;             // outputs of a workgroup of the second kernel
+  int tiles, parts, slots;   // the grid: tiles of rows, parts of K or N, workgroups that share the adapters of a tile
 };
 
 template <int TY> struct Frag;
@@ -88,309 +87,473 @@ struct Tile {
   }
 };
 
-// Partial sums of z = A_i x over one part of K.  One workgroup per tile of
-// 16 TM rows, part of K and slot; the waves take chunks of the part in turn,
-// each the products of 16 TM rows with 16 NT rows of A_i, read straight into
-// operand registers (an element of either feeds 16 products: nothing is gained
-// by LDS).  Lane l takes columns 16 (l / 16) .. + 15 of a chunk, two MFMA steps
-// of eight, so that four lanes read a row's 128 bytes.  Rows of the tile with
-// another adapter (or none), and rows of A_i beyond its rank, read a valid row
-// instead: they only reach outputs that are not stored.
-template <int TY, int TM, int NT>
-__global__ void __launch_bounds__(kThreads)
+// A workgroup's place.  Workgroups are dealt to the eight XCDs in turn; each
+// XCD gets consecutive tiles, which mostly use the same few adapters, so that
+// these stay in its L2.
+struct Place {
+  int tile, part, slot;
+  __device__ __forceinline__ Place(const AdapterArgs &a) {
+    const int each = gridDim.x / 8, at = (blockIdx.x % 8) * each + blockIdx.x / 8;
+    const int per = a.parts * a.slots;
+    tile = at / per;          // (beyond the last: no work)
+    part = at % per / a.slots;
+    slot = at % a.slots;
+  }
+};
+static dim3 place_grid(const AdapterArgs &a) { return dim3((a.tiles * a.parts * a.slots + 7) / 8 * 8); }
+
+// What a workgroup takes of the adapters of its tile: every slots-th of them.
+struct Turn {
+  int left;
+  __device__ __forceinline__ Turn(const Place &p) : left(p.slot) {}
+  __device__ __forceinline__ bool mine(const AdapterArgs &a) {
+    const bool m = left == 0;
+    left = m ? a.slots - 1 : left - 1;
+    return m;
+  }
+};
+
+// The terms of z and each row's power of two.
+template <int TM, int NT, int TERMS>
+struct ZTerms {
+  static constexpr int RP = (NT + 1) / 2 * 32;   // ranks, whole MFMA steps
+  __attribute__((aligned(16))) uint16_t z[TERMS][TM * kRows][RP + 8];
+  float up[TM * kRows];
+};
+
+// Row r = tid / 16, ranks 16 q + tid % 16 (v[q]; 0 from the rank on): brought
+// to a power of two near 1 per row and split into TERMS 16-bit numbers, whose
+// products with B_i are exact in the MFMA.  Two terms keep 22 bits of z's
+// largest in fp16 and 16 in bf16, more than a 16-bit output shows; an fp32
+// output takes three.
+template <int TY, int TM, int NT, int TERMS>
+__device__ __forceinline__ void put_terms(ZTerms<TM, NT, TERMS> &s, int r, const float (&v)[NT], int rank) {
+  const int j = threadIdx.x & 15;
+  float top = 0.f;
+#pragma unroll
+  for (int q = 0; q < NT; ++q) {
+    const float f = q * kRows + j < rank ? __builtin_fabsf(v[q]) : 0.f;
+    if (f < __builtin_inff()) top = __builtin_fmaxf(top, f);
+  }
+  top = dpp_row_max(top);
+  const int e = top > 0.f ? std::max(ilogb_f32(top), -120) : 0;   // (2^e and 2^-e are normal numbers)
+  if (j == 0) s.up[r] = __builtin_ldexpf(1.f, e);
+#pragma unroll
+  for (int q = 0; q < ZTerms<TM, NT, TERMS>::RP / kRows; ++q) {
+    float rest = 0.f;
+    if (q < NT && q * kRows + j < rank) rest = __builtin_ldexpf(v[q < NT ? q : 0], -e);
+#pragma unroll
+    for (int t = 0; t < TERMS; ++t) {
+      const uint32_t bits = Val<TY>::put(rest);
+      s.z[t][r][q * kRows + j] = (uint16_t)bits;
+      // (an infinity or NaN is in the first term whole)
+      rest = __builtin_fabsf(rest) < __builtin_inff() ? rest - Val<TY>::get(bits) : 0.f;
+    }
+  }
+}
+
+// Both kernels: an MFMA operand's lanes lie in 16 different rows, and such a
+// load keeps the address path busy four times as long as one along the rows
+// (64 clocks for 1 KB against 16), which bounds a stream of them.  So every
+// operand comes along its rows, eight lanes to 128 bytes, and changes places in
+// a part of LDS that belongs to its wave alone: no barriers, since the LDS
+// operations of a wave stay in order.
+constexpr int kAdapterWaves = 4, kAdapterThreads = kAdapterWaves * kWave;
+
+// Between LDS accesses of one wave that may not change places (the hardware
+// keeps their order; this keeps the compiler to it).
+__device__ __forceinline__ void lds_order() { asm volatile("" ::: "memory"); }
+
+// [rows][64] 16-bit values, 128 bytes a row, in pieces of 16 bytes: piece p of
+// row r stands at p ^ (r % 8), so that neither side has bank conflicts.
+template <int ROWS>
+struct Stage {
+  __attribute__((aligned(16))) uint8_t b[ROWS * 128];
+  __device__ __forceinline__ void put(int r, int p, u32x4 v) { *(u32x4 *)(b + r * 128 + (p ^ (r & 7)) * 16) = v; }
+  // MFMA operand: row 16 t + lane % 16, columns 32 h + 8 (lane / 16) ..
+  __device__ __forceinline__ u32x4 get(int t, int h) const {
+    const int lane = threadIdx.x & 63, r = lane & 15;
+    return *(const u32x4 *)(b + (t * kRows + r) * 128 + ((h * 4 + (lane >> 4)) ^ (r & 7)) * 16);
+  }
+};
+
+// Sixty-four outputs of 16 rows in fp32.
+struct OutTile {
+  float v[kRows][64 + 4];
+};
+
+// Sums of a tile's z over the waves: 16 NT ranks.
+template <int TM, int NT>
+using Red = float[kAdapterWaves][TM * kRows][NT * kRows + 4];
+
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
+// Partial sums of z = A_i x over one part of K, 16 NT ranks from j0: one
+// workgroup per tile of 16 TM rows, part, group of ranks and slot.  The waves
+// take chunks of 64 columns in turn, each the products of 16 TM rows with
+// 16 NT rows of A_i, with D - 1 chunks under way while one is multiplied (as
+// many as leave room for four workgroups on a CU).  Rows of the tile with
+// another adapter (or none), and rows of A_i beyond R, read a valid row
+// instead: they only reach sums that are not stored.
+template <int TY, int TM, int NT, int D>
+__global__ void __launch_bounds__(kAdapterThreads, TM + NT < 3 ? 4 : TM + NT < 6 ? 3 : 2)
 adapters_down_kernel(AdapterArgs a) {
-  __shared__ float red[kWaves][TM * kRows][kRows + 4];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, g = lane >> 4;
-  const int r0 = blockIdx.x * (TM * kRows);
-  const int c0 = blockIdx.y * a.per, c1 = std::min(c0 + a.per, (a.K + kChunk - 1) / kChunk);
+  constexpr int NW = kAdapterWaves, GR = NT * kRows;
+  constexpr int XI = TM * 2, AI = NT * 2;       // loads of 1 KB: a chunk of x and of A
+  union Part {
+    Stage<kRows *(TM + NT)> in[NW];
+    Red<TM, NT> red;
+  };
+  __shared__ Part part;
+  const Place place(a);
+  const int r0 = place.tile * (TM * kRows), tid = threadIdx.x, lane = tid & 63, wave = wave_id(), l16 = lane & 15, g = lane >> 4;
+  if (place.tile >= a.tiles) return;
+  const int j0 = place.part / a.splits * GR, split = place.part % a.splits;
+  const int c0 = split * a.per, chunks = std::min(c0 + a.per, (a.K + kChunk - 1) / kChunk) - c0;
   Tile<TM> tile;
   tile.load(a, r0);
-  int slot = 0, row = 0;
-  for (int cur = tile.next(row); cur >= 0; cur = tile.next(row)) {
-    const bool mine = slot == (int)blockIdx.z;
-    slot = slot + 1 == a.slots ? 0 : slot + 1;
-    if (!mine) continue;
-    const int rank = rank_of(a, cur);
-    if (!rank) continue;
-    const uint8_t *xp[TM], *ap[NT];
+  auto &st = part.in[wave];
+  const int pr = lane >> 3, pc = lane & 7;   // row and piece of a load along the rows
+  int row = 0;
+  Turn turn(place);
+  Tile<TM> left = tile;
+  // chunks from one that differs from tile to tile: rows are often a power of
+  // two apart, and workgroups in step would read the same few memory channels
+  const int first = c0 + place.tile * 5 % chunks, end = c0 + chunks;
+  for (int cur = left.next(row); cur >= 0; cur = left.next(row)) {
+    if (!turn.mine(a)) continue;
+    const uint8_t *xp[XI], *ap[AI];
 #pragma unroll
-    for (int m = 0; m < TM; ++m)
-      xp[m] = (const uint8_t *)a.x + ((r0 + (tile.id[m] == cur ? m * kRows + l16 : row)) * a.ldx + g * 16) * 2;
+    for (int i = 0; i < XI; ++i) {
+      const int r = i * 8 + pr;
+      const bool mine = __shfl(tile.id[i / 2], r & 15, kWave) == cur;
+      xp[i] = (const uint8_t *)a.x + ((r0 + (mine ? r : row)) * a.ldx + pc * 8) * 2;
+    }
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int j = t * kRows + l16;
-      ap[t] = (const uint8_t *)a.a + (cur * a.stride_a + (j < rank ? j : 0) * a.lda + g * 16) * 2;
+    for (int i = 0; i < AI; ++i) {
+      const int j = j0 + i * 8 + pr;
+      ap[i] = (const uint8_t *)a.a + (cur * a.stride_a + (j < a.R ? j : 0) * a.lda + pc * 8) * 2;
     }
     f32x4 acc[TM][NT];
 #pragma unroll
     for (int m = 0; m < TM; ++m)
 #pragma unroll
       for (int t = 0; t < NT; ++t) acc[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const auto step = [&](const u32x4 (&x)[TM][2], const u32x4 (&w)[NT][2]) {
+    const auto fetch = [&](int i, u32x4 (&x)[XI], u32x4 (&w)[AI]) {   // the part's i-th chunk
+      const int at = first + i, c = at < end ? at : at - chunks;
+      if ((c + 1) * kChunk <= a.K) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+        for (int q = 0; q < XI; ++q) x[q] = load8(xp[q] + c * (kChunk * 2));
 #pragma unroll
-        for (int m = 0; m < TM; ++m)
+        for (int q = 0; q < AI; ++q) w[q] = load8(ap[q] + c * (kChunk * 2));
+      } else {   // the last columns
+        const int n = a.K - c * kChunk - pc * 8;
 #pragma unroll
-          for (int t = 0; t < NT; ++t) acc[m][t] = Frag<TY>::mfma(w[t][h], x[m][h], acc[m][t]);
-    };
-    const int whole = std::min(c1, a.K / kChunk);
-    const auto fetch = [&](int c, u32x4 (&x)[TM][2], u32x4 (&w)[NT][2]) {
+        for (int q = 0; q < XI; ++q) x[q] = load8(xp[q] + c * (kChunk * 2), n);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int m = 0; m < TM; ++m) x[m][h] = load8(xp[m] + c * (kChunk * 2) + h * 16);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) w[t][h] = load8(ap[t] + c * (kChunk * 2) + h * 16);
+        for (int q = 0; q < AI; ++q) w[q] = load8(ap[q] + c * (kChunk * 2), n);
       }
     };
-    int c = c0 + wave;
-    if constexpr (NT <= 4)
-      for (; c + kWaves < whole; c += 2 * kWaves) {   // two chunks in flight
-        u32x4 x0[TM][2], w0[NT][2], x1[TM][2], w1[NT][2];
-        fetch(c, x0, w0);
-        fetch(c + kWaves, x1, w1);
-        step(x0, w0);
-        step(x1, w1);
-      }
-    for (; c < whole; c += kWaves) {
-      u32x4 x[TM][2], w[NT][2];
-      fetch(c, x, w);
-      step(x, w);
-    }
-    if (c < c1) {   // the last columns
-      u32x4 x[TM][2], w[NT][2];
+    const auto step = [&](const u32x4 (&x)[XI], const u32x4 (&w)[AI]) {
+#pragma unroll
+      for (int q = 0; q < XI; ++q) st.put(q * 8 + pr, pc, x[q]);
+#pragma unroll
+      for (int q = 0; q < AI; ++q) st.put((XI + q) * 8 + pr, pc, w[q]);
+      lds_order();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int n = a.K - c * kChunk - g * 16 - h * 8;
+        u32x4 xf[TM];
 #pragma unroll
-        for (int m = 0; m < TM; ++m) x[m][h] = load8(xp[m] + c * (kChunk * 2) + h * 16, n);
+        for (int m = 0; m < TM; ++m) xf[m] = st.get(m, h);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) w[t][h] = load8(ap[t] + c * (kChunk * 2) + h * 16, n);
-      }
-      step(x, w);
-    }
-    // the waves' sums, 16 ranks at a time, in wave order
-    float *z = a.z + ((int64_t)blockIdx.y * a.T + r0) * a.R;
+        for (int t = 0; t < NT; ++t) {
+          const u32x4 af = st.get(TM + t, h);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      if (t * kRows >= rank) continue;
-      __syncthreads();
-#pragma unroll
-      for (int m = 0; m < TM; ++m) *(f32x4 *)&red[wave][m * kRows + l16][g * 4] = acc[m][t];
-      __syncthreads();
-#pragma unroll
-      for (int m = 0; m < TM; ++m) {
-        const int r = m * kRows + (tid >> 4), j = tid & 15;
-        const int id = __shfl(tile.id[m], tid >> 4, kWave);
-        if (id == cur && t * kRows + j < rank) {
-          float s = red[0][r][j];
-#pragma unroll
-          for (int w = 1; w < kWaves; ++w) s += red[w][r][j];
-          z[(int64_t)r * a.R + t * kRows + j] = s;
+          for (int m = 0; m < TM; ++m) acc[m][t] = Frag<TY>::mfma(af, xf[m], acc[m][t]);
         }
       }
+      lds_order();
+    };
+    u32x4 x[D][XI], w[D][AI];
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d)
+      if (wave + d * NW < chunks) fetch(wave + d * NW, x[d], w[d]);
+    for (int i = wave; i < chunks; i += D * NW) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        if (i + (d + D - 1) * NW < chunks) fetch(i + (d + D - 1) * NW, x[(d + D - 1) % D], w[(d + D - 1) % D]);
+        if (i + d * NW < chunks) step(x[d], w[d]);
+      }
     }
+    // the waves' sums, in wave order
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < TM; ++m)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) *(f32x4 *)&part.red[wave][m * kRows + l16][t * kRows + g * 4] = acc[m][t];
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < TM; ++m) {
+      const int r = m * kRows + (tid >> 4);
+      const bool mine = __shfl(tile.id[m], tid >> 4, kWave) == cur;
+      float *z = a.z + ((int64_t)split * a.T + r0 + r) * a.R;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int j = t * kRows + (tid & 15);
+        float v = part.red[0][r][j];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) v += part.red[w][r][j];
+        if (mine && j0 + j < a.R) z[j0 + j] = v;
+      }
+    }
+    __syncthreads();
   }
 }
 
-// out = y + scale_i B_i z.  One workgroup per tile of 16 TM rows, 256 outputs
-// and slot.  z is summed over the parts of K, brought to a power of two near 1
-// per row and split into TERMS 16-bit numbers, whose products with B_i are
-// exact in the MFMA: two terms keep 22 bits of it in fp16 and 16 in bf16, more
-// than a 16-bit output shows; an fp32 output takes three.  The MFMA's rows
-// are outputs, dealt so that a lane ends with 16 consecutive ones of one row.
-template <int TY, int TO, int TM, int NT>
-__global__ void __launch_bounds__(kThreads)
+// out = y + scale_i B_i z: one workgroup per tile of 16 rows, `width` outputs
+// and slot.  The waves take 64 outputs in turn (MFMA rows 16 t + m are outputs
+// n0 + 16 t + m, columns the rows); the next turn's y and the next step's B (64
+// ranks of one adapter) are loaded meanwhile.
+template <int TY, int TO, int RM>
+__global__ void __launch_bounds__(kAdapterThreads, (RM <= 32 ? 4 : RM <= 128 ? 3 : 2) - (TO == MOEQ_F32 && RM != 256))
 adapters_up_kernel(AdapterArgs a) {
-  constexpr int TERMS = TO == MOEQ_F32 ? 3 : 2;
-  constexpr int RP = (NT + 1) / 2 * 32, LD = RP + 8;
-  __shared__ __attribute__((aligned(16))) uint16_t zs[TERMS][TM * kRows][LD];
-  __shared__ int s_exp[TM * kRows];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, g = lane >> 4;
-  const int r0 = blockIdx.x * (TM * kRows), n0 = blockIdx.y * kCols + wave * 64;
-  Tile<TM> tile;
+  constexpr int NW = kAdapterWaves, TERMS = TO == MOEQ_F32 ? 3 : 2, NT = RM / kRows;
+  constexpr int PB = std::min(RM / 8, 8), BI = PB;   // pieces of a row of B; loads of 64 rows
+  union Part {                              // of one wave, in turn
+    Stage<64> in;
+    OutTile out;
+  };
+  __shared__ Part part[NW];
+  __shared__ ZTerms<1, NT, TERMS> zt;
+  const Place place(a);
+  const int r0 = place.tile * kRows, tid = threadIdx.x, lane = tid & 63, wave = wave_id(), l16 = lane & 15, g = lane >> 4;
+  const int pr = lane >> 3, pc = lane & 7;
+  if (place.tile >= a.tiles) return;
+  Tile<1> tile;
   tile.load(a, r0);
-  // the rows that this workgroup writes: those of its share of the adapters,
-  // and slot 0 those without one
-  bool own[TM];
-#pragma unroll
-  for (int m = 0; m < TM; ++m) own[m] = blockIdx.z == 0 && tile.id[m] < 0 && r0 + m * kRows + l16 < a.T;
-  int slot = 0, row = 0;
-  for (int cur = tile.next(row); cur >= 0; cur = tile.next(row)) {
-    if (slot == (int)blockIdx.z) {
-#pragma unroll
-      for (int m = 0; m < TM; ++m) own[m] |= tile.id[m] == cur;
-    }
-    slot = slot + 1 == a.slots ? 0 : slot + 1;
+  // this workgroup's adapters (lane q: the q-th of them) and rows
+  int cur_of = -1, count = 0, row = 0;
+  bool own = place.slot == 0 && tile.id[0] < 0 && r0 + l16 < a.T;
+  {
+    Turn turn(place);
+    for (int cur = tile.next(row); cur >= 0; cur = tile.next(row))
+      if (turn.mine(a)) {
+        own |= tile.id[0] == cur;
+        if (lane == count) cur_of = cur;
+        ++count;
+      }
   }
-  bool any = false;
+  if (!__ballot(own)) return;
+  const int n1 = std::min(a.N, (place.part + 1) * a.width);
+  const uint8_t *yp[2];
+  uint8_t *op[2];
+  bool mine[2], plain[2];
 #pragma unroll
-  for (int m = 0; m < TM; ++m) any |= own[m];
-  if (!__ballot(any)) return;
-  Oct<TO> y[TM][2];
+  for (int h = 0; h < 2; ++h) {   // y and out along their rows: row pr + 8 h, outputs n0 + 8 pc ..
+    const int r = h * 8 + pr;
+    mine[h] = __shfl((int)own, r, kWave);
+    plain[h] = __shfl(tile.id[0], r, kWave) < 0;
+    yp[h] = (const uint8_t *)a.y + ((r0 + r) * a.ldy + pc * 8) * Val<TO>::size;
+    op[h] = (uint8_t *)a.out + ((r0 + r) * a.ldo + pc * 8) * Val<TO>::size;
+  }
+  const auto load_y = [&](int n0, Oct<TO> (&y)[2]) {
 #pragma unroll
-  for (int m = 0; m < TM; ++m)
+    for (int h = 0; h < 2; ++h)
+      if (mine[h]) y[h].load(yp[h], n0, a.N - n0 - pc * 8);
+  };
+  const int pb = lane % PB;
+  const auto load_b = [&](int n0, int q, int k, u32x4 (&w)[BI]) {   // 64 ranks from k of the q-th adapter
+    const int cur = __builtin_amdgcn_readlane(cur_of, q), n = rank_of(a, cur) - k - pb * 8;
+    const uint8_t *base = (const uint8_t *)a.b + (cur * a.stride_b + k + pb * 8) * 2;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = n0 + g * 16 + h * 8;
-      if (own[m] && c < a.N) y[m][h].load(a.y, (r0 + m * kRows + l16) * a.ldy + c, a.N - c);
+    for (int i = 0; i < BI; ++i) {
+      const int c = std::min(n0 + i * (64 / PB) + lane / PB, a.N - 1);
+      w[i] = load8(base + c * a.ldb * 2, n);
     }
-  // z of row m * 16 + tid / 16, ranks tid % 16 + 16 q
+  };
+  constexpr int DN = NW * 64;   // from turn to turn of a wave
+  const int first = place.part * a.width + wave * 64;
+  Oct<TO> y[2], yn[2];
+  u32x4 w[BI];
+  if (first < n1) {
+    load_y(first, y);
+    if (count) load_b(first, 0, 0, w);
+  }
+  {
+    const int id = __shfl(tile.id[0], tid >> 4, kWave), j = tid & 15;
+    float v[NT];
 #pragma unroll
-  for (int m = 0; m < TM; ++m) {
-    const int r = m * kRows + (tid >> 4), id = __shfl(tile.id[m], tid >> 4, kWave);
-    const int rank = id >= 0 ? rank_of(a, id) : 0;
-    float v[RP / kRows], top = 0.f;
+    for (int q = 0; q < NT; ++q) v[q] = 0.f;
+    if (id >= 0) {
+      const float *z = a.z + (int64_t)(r0 + (tid >> 4)) * a.R + j;
+      constexpr int B = NT <= 2 ? 8 : NT <= 4 ? 4 : 2;   // parts of K loaded at a time
+      for (int s = 0; s < a.splits; s += B) {
+        float part[B][NT];
 #pragma unroll
-    for (int q = 0; q < RP / kRows; ++q) {
-      const int j = (tid & 15) + q * kRows;
-      v[q] = 0.f;
-      if (j < rank) {
-        const float *p = a.z + (int64_t)(r0 + r) * a.R + j;
-        v[q] = p[0];
-        for (int s = 1; s < a.splits; ++s) v[q] += p[(int64_t)s * a.T * a.R];
+        for (int u = 0; u < B; ++u)
+#pragma unroll
+          for (int q = 0; q < NT; ++q)
+            part[u][q] = s + u < a.splits && q * kRows + j < a.R ? z[(int64_t)(s + u) * a.T * a.R + q * kRows] : 0.f;
+#pragma unroll
+        for (int u = 0; u < B; ++u)
+#pragma unroll
+          for (int q = 0; q < NT; ++q) v[q] += part[u][q];
       }
-      const float f = __builtin_fabsf(v[q]);
-      if (f < __builtin_inff()) top = __builtin_fmaxf(top, f);
-    }
-    top = dpp_row_max(top);
-    const int e = top > 0.f ? ilogb_f32(top) : 0;
-    if ((tid & 15) == 0) s_exp[r] = e;
+      if (a.scale) {
+        const float f = a.scale[id];
 #pragma unroll
-    for (int q = 0; q < RP / kRows; ++q) {
-      float rest = __builtin_ldexpf(v[q], -e);
-#pragma unroll
-      for (int t = 0; t < TERMS; ++t) {
-        const uint32_t bits = Val<TY>::put(rest);
-        zs[t][r][(tid & 15) + q * kRows] = (uint16_t)bits;
-        // (an infinity or NaN is in the first term whole)
-        rest = __builtin_fabsf(rest) < __builtin_inff() ? rest - Val<TY>::get(bits) : 0.f;
+        for (int q = 0; q < NT; ++q) v[q] *= f;
       }
     }
+    put_terms<TY>(zt, tid >> 4, v, id >= 0 ? rank_of(a, id) : 0);
   }
   __syncthreads();
-  f32x4 sum[TM][4];
-  tile.restart();
-  slot = 0;
-  bool served[TM];
-  float factor[TM];
-  int expo[TM];
+  Stage<64> &st = part[wave].in;
+  OutTile &ot = part[wave].out;
+  float up[2];
 #pragma unroll
-  for (int m = 0; m < TM; ++m) {
-    served[m] = false;
-    expo[m] = s_exp[m * kRows + l16];
-    factor[m] = 0.f;
+  for (int h = 0; h < 2; ++h) up[h] = zt.up[h * 8 + pr];
+  for (int n0 = first; n0 < n1; n0 += DN) {
+    const bool more = n0 + DN < n1;
+    if (more) load_y(n0 + DN, yn);
+    // the products with each adapter go to the rows that use it
+    f32x4 res[4];
+    for (int q = 0; q < count; ++q) {
+      const int cur = __builtin_amdgcn_readlane(cur_of, q), rank = rank_of(a, cur);
+      f32x4 acc[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) sum[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
-  for (int cur = tile.next(row); cur >= 0; cur = tile.next(row)) {
-    const bool mine = slot == (int)blockIdx.z;
-    slot = slot + 1 == a.slots ? 0 : slot + 1;
-    if (!mine) continue;
-    const int rank = rank_of(a, cur);
-    if (!rank) continue;
-    const uint8_t *bp[4];
+      for (int t = 0; t < 4; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+      int k = 0;
+      do {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      // row l16 of MFMA tile t is output 16 (l16 / 4) + 4 t + l16 % 4
-      const int c = std::min(n0 + (l16 >> 2) * 16 + t * 4 + (l16 & 3), a.N - 1);
-      bp[t] = (const uint8_t *)a.b + (cur * a.stride_b + c * a.ldb + g * 8) * 2;
-    }
-    f32x4 acc[TM][4];
+        for (int i = 0; i < BI; ++i) st.put(i * (64 / PB) + lane / PB, pb, w[i]);
+        lds_order();
+        if (RM > 64 && k + 64 < rank) load_b(n0, q, k + 64, w);
+        else if (q + 1 < count) load_b(n0, q + 1, 0, w);
+        else if (more) load_b(n0 + DN, 0, 0, w);
 #pragma unroll
-    for (int m = 0; m < TM; ++m)
+        for (int h = 0; h < (RM > 32 ? 2 : 1); ++h) {
+          if (h && k + 32 >= rank) continue;
+          u32x4 bf[4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) acc[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+          for (int t = 0; t < 4; ++t) {
+            bf[t] = st.get(t, h);
+            if (RM == 16 && g >= 2) bf[t] = u32x4{0, 0, 0, 0};   // (no such ranks)
+          }
 #pragma unroll
-    for (int k = 0; k < RP; k += 32) {
-      if (k >= rank) continue;
-      u32x4 w[4];
-      if (k + 32 <= rank) {
+          for (int e = 0; e < TERMS; ++e) {
+            const u32x4 z = *(const u32x4 *)&zt.z[e][l16][k + h * 32 + g * 8];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) w[t] = load8(bp[t] + k * 2);
-      } else {
-#pragma unroll
-        for (int t = 0; t < 4; ++t) w[t] = load8(bp[t] + k * 2, rank - k - g * 8);
-      }
-#pragma unroll
-      for (int m = 0; m < TM; ++m)
-#pragma unroll
-        for (int q = 0; q < TERMS; ++q) {
-          const u32x4 z = *(const u32x4 *)&zs[q][m * kRows + l16][k + g * 8];
-#pragma unroll
-          for (int t = 0; t < 4; ++t) acc[m][t] = Frag<TY>::mfma(w[t], z, acc[m][t]);
+            for (int t = 0; t < 4; ++t) acc[t] = Frag<TY>::mfma(bf[t], z, acc[t]);
+          }
         }
+        lds_order();
+        k += 64;
+      } while (RM > 64 && k < rank);
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) res[t][i] = q == 0 || tile.id[0] == cur ? acc[t][i] : res[t][i];
     }
-    const float f = a.scale ? a.scale[cur] : 1.f;
+    if (count) {
 #pragma unroll
-    for (int m = 0; m < TM; ++m)
-      if (tile.id[m] == cur) {
-        served[m] = true;
-        factor[m] = f;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) sum[m][t] = acc[m][t];
-      }
-  }
-#pragma unroll
-  for (int m = 0; m < TM; ++m)
+      for (int t = 0; t < 4; ++t) *(f32x4 *)&ot.v[l16][t * kRows + g * 4] = res[t];
+      lds_order();
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int c = n0 + g * 16 + h * 8;
-      if (!own[m] || c >= a.N) continue;
-      float v[8];
+      f32x4 d[2];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float d = factor[m] * __builtin_ldexpf(sum[m][h * 2 + (i >> 2)][i & 3], expo[m]);
-        v[i] = served[m] ? y[m][h][i] + d : y[m][h][i];
+      for (int i = 0; i < 2; ++i) d[i] = *(const f32x4 *)&ot.v[h * 8 + pr][pc * 8 + i * 4];
+      const int n = a.N - n0 - pc * 8;
+      if (!mine[h] || n <= 0) continue;
+      if (!plain[h]) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __builtin_fmaf(d[i >> 2][i & 3], up[h], y[h][i]);
+        y[h].pack(v);
       }
-      Oct<TO> o;
-      o.pack(v);
-      o.store(a.out, (r0 + m * kRows + l16) * a.ldo + c, a.N - c);
+      y[h].store(op[h], n0, n);
     }
+    lds_order();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) y[h] = yn[h];
+  }
 }
 
-// How a call is cut: rows per workgroup, parts of K.
+// How a call is cut: rows per workgroup of the first kernel (16 tm), ranks it
+// forms at a time (16 nt), parts of K.
 struct AdapterPlan {
-  int tm, splits, per;
+  int tm, nt, groups, splits, per;
 };
+#ifndef DW
+#define DW 512
+#endif
+#ifndef UW
+#define UW 1024
+#endif
+#ifndef TMT
+#define TMT 2048
+#endif
 static AdapterPlan adapter_plan(int T, int R, int K) {
   AdapterPlan p;
-  p.tm = T >= 512 && R <= 64 ? 4 : 1;
-  const int tiles = (T + p.tm * kRows - 1) / (p.tm * kRows), chunks = (K + kChunk - 1) / kChunk;
-  const int most = std::min(16, (chunks + kWaves - 1) / kWaves);
-  p.splits = std::max(1, std::min(most, 256 / std::max(tiles, 1)));
+  p.tm = T >= TMT ? 2 : 1;
+  p.nt = R <= 16 ? 1 : R <= 32 ? 2 : 4;
+  p.groups = (R + p.nt * kRows - 1) / (p.nt * kRows);
+  const int tiles = std::max(1, (T + p.tm * kRows - 1) / (p.tm * kRows)) * p.groups, chunks = (K + kChunk - 1) / kChunk;
+  const int most = std::min(16, (chunks + kAdapterWaves - 1) / kAdapterWaves);
+  p.splits = std::max(1, std::min(most, DW / tiles));
   p.per = (chunks + p.splits - 1) / p.splits;
   p.splits = (chunks + p.per - 1) / p.per;
   return p;
 }
 
-template <int TY, int TO, int TM, int NT>
-static void launch_adapters(AdapterArgs a, hipStream_t s) {
-  const int tiles = (a.T + TM * kRows - 1) / (TM * kRows), cols = (a.N + kCols - 1) / kCols;
-  const int most = std::min(a.n, TM * kRows);
-  a.slots = std::max(1, std::min(most, 2048 / (tiles * a.splits)));
-  hipLaunchKernelGGL((adapters_down_kernel<TY, TM, NT>), dim3(tiles, a.splits, a.slots), dim3(kThreads), 0, s, a);
-  a.slots = (int)std::max((int64_t)1, std::min((int64_t)most, 4096 / ((int64_t)tiles * cols)));
-  hipLaunchKernelGGL((adapters_up_kernel<TY, TO, TM, NT>), dim3(tiles, cols, a.slots), dim3(kThreads), 0, s, a);
+// Workgroups that share a tile's adapters: as many as a tile can use, as long
+// as the grid stays within what the card holds at a time (most of them have no
+// work where rows of one adapter stand together).
+static int adapter_slots(const AdapterArgs &a, int rows) {
+  const int64_t wgs = (int64_t)a.tiles * a.parts;
+  return (int)std::max((int64_t)1, std::min((int64_t)std::min(std::min(a.n, a.T), rows), 1024 / wgs));
+}
+
+template <int TY, int TM, int NT, int D>
+static void launch_down(AdapterArgs a, const AdapterPlan &p, hipStream_t s) {
+  a.tiles = (a.T + TM * kRows - 1) / (TM * kRows);
+  a.parts = p.splits * p.groups;
+  a.slots = adapter_slots(a, TM * kRows);
+  hipLaunchKernelGGL((adapters_down_kernel<TY, TM, NT, D>), place_grid(a), dim3(kAdapterThreads), 0, s, a);
+}
+
+template <int TY, int TO, int RM>
+static void launch_up(AdapterArgs a, hipStream_t s) {
+  a.tiles = (a.T + kRows - 1) / kRows;
+  const int turn = kAdapterWaves * 64, turns = (a.N + turn - 1) / turn;
+  const int parts = std::max(1, std::min(turns, UW / a.tiles));
+  a.width = (turns + parts - 1) / parts * turn;
+  a.parts = (a.N + a.width - 1) / a.width;
+  a.slots = adapter_slots(a, kRows);
+  hipLaunchKernelGGL((adapters_up_kernel<TY, TO, RM>), place_grid(a), dim3(kAdapterThreads), 0, s, a);
 }
 
 template <int TY, int TO>
-static void launch_adapters_r(AdapterArgs a, hipStream_t s) {
+static void launch_adapters(AdapterArgs a, hipStream_t s) {
   const AdapterPlan p = adapter_plan(a.T, a.R, a.K);
   a.splits = p.splits;
   a.per = p.per;
-  if (p.tm == 4) {
-    if (a.R <= 16) launch_adapters<TY, TO, 4, 1>(a, s);
-    else if (a.R <= 32) launch_adapters<TY, TO, 4, 2>(a, s);
-    else launch_adapters<TY, TO, 4, 4>(a, s);
+  if (p.tm == 2) {
+    if (p.nt == 1) launch_down<TY, 2, 1, 3>(a, p, s);
+    else if (p.nt == 2) launch_down<TY, 2, 2, 2>(a, p, s);
+    else launch_down<TY, 2, 4, 2>(a, p, s);
   } else {
-    if (a.R <= 16) launch_adapters<TY, TO, 1, 1>(a, s);
-    else if (a.R <= 32) launch_adapters<TY, TO, 1, 2>(a, s);
-    else if (a.R <= 64) launch_adapters<TY, TO, 1, 4>(a, s);
-    else if (a.R <= 128) launch_adapters<TY, TO, 1, 8>(a, s);
-    else launch_adapters<TY, TO, 1, 16>(a, s);
+    if (p.nt == 1) launch_down<TY, 1, 1, 4>(a, p, s);
+    else if (p.nt == 2) launch_down<TY, 1, 2, 3>(a, p, s);
+    else launch_down<TY, 1, 4, 2>(a, p, s);
   }
+  if (a.R <= 16) launch_up<TY, TO, 16>(a, s);
+  else if (a.R <= 32) launch_up<TY, TO, 32>(a, s);
+  else if (a.R <= 64) launch_up<TY, TO, 64>(a, s);
+  else if (a.R <= 128) launch_up<TY, TO, 128>(a, s);
+  else launch_up<TY, TO, 256>(a, s);
 }
 
 static size_t adapters_workspace(int T, int R, int K) { return (size_t)adapter_plan(T, R, K).splits * T * R * 4; }
@@ -435,7 +598,7 @@ MOEQ_API moeq_status moeq_adapters(const moeq_adapters_set *s, const void *x, in
   MOEQ_TRY(check_matrix(who, "out", out, ldo, s->N, y_dtype));
   if (!ids || ((uintptr_t)ids & 3)) return fail(MOEQ_ERR_INVALID, "%s: null or misaligned ids", who);
   const size_t need = adapters_workspace(T, s->R, s->K);
-  if (!ws || ((uintptr_t)ws & 15)) return fail(MOEQ_ERR_INVALID, "%s: null or misaligned workspace", who);
+  if (need && (!ws || ((uintptr_t)ws & 15))) return fail(MOEQ_ERR_INVALID, "%s: null or misaligned workspace", who);
   if (ws_bytes < need) return fail(MOEQ_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", who, ws_bytes, need);
   AdapterArgs a{};
   a.x = x;
@@ -461,11 +624,11 @@ MOEQ_API moeq_status moeq_adapters(const moeq_adapters_set *s, const void *x, in
   a.K = s->K;
   prof_begin("adapters", stream);
   if (s->dtype == MOEQ_F16) {
-    if (y_dtype == MOEQ_F16) launch_adapters_r<MOEQ_F16, MOEQ_F16>(a, stream);
-    else launch_adapters_r<MOEQ_F16, MOEQ_F32>(a, stream);
+    if (y_dtype == MOEQ_F16) launch_adapters<MOEQ_F16, MOEQ_F16>(a, stream);
+    else launch_adapters<MOEQ_F16, MOEQ_F32>(a, stream);
   } else {
-    if (y_dtype == MOEQ_BF16) launch_adapters_r<MOEQ_BF16, MOEQ_BF16>(a, stream);
-    else launch_adapters_r<MOEQ_BF16, MOEQ_F32>(a, stream);
+    if (y_dtype == MOEQ_BF16) launch_adapters<MOEQ_BF16, MOEQ_BF16>(a, stream);
+    else launch_adapters<MOEQ_BF16, MOEQ_F32>(a, stream);
   }
   prof_end("adapters", stream);
   return check_launch("adapters");

@@ -155,10 +155,11 @@ def test_infinities_stay_in_their_rows():
 
 def test_empty_and_repeated():
     from bit_quantized_moe_token_amd import moeq
-    c = Case(60, 5, 16, 200, 120)
+    c = Case(60, 5, 160, 200, 120)
     assert moeq.adapters(c.x[:0].cuda(), c.a.cuda(), c.b.cuda(), c.ids[:0].cuda(), c.y[:0].cuda()).shape == (0, 120)
     ref = c.call()
-    ws = torch.full((moeq.adapters_workspace_size(60, 16, 200),), 255, dtype=torch.uint8).cuda()
+    ws = torch.full((moeq.adapters_workspace_size(60, 160, 200),), 255, dtype=torch.uint8).cuda()
+    assert ws.numel()
     for _ in range(3):
         assert torch.equal(c.call(ws=ws), ref)               # whatever the workspace held
     c.ids[:] = -1
@@ -203,7 +204,7 @@ def test_refusals():
         with pytest.raises(e):
             moeq.adapters(**dict(good, **bad))
     with pytest.raises(moeq.MoeqError):
-        moeq.adapters(**good, ws=torch.zeros(16, dtype=torch.uint8).cuda())
+        Case(4, 2, 256, 16, 24).call(ws=torch.zeros(16, dtype=torch.uint8))
     with pytest.raises(moeq.MoeqError):
         moeq.adapters(**good, out=good["y"][:1].expand(4, 24))
 

@@ -103,7 +103,7 @@ def test_combine_without_work(L):
     assert _cgrad(L, dg=4098) == 1 and _cgrad(L, base=None) == 1
 
 
-def _adapters(L, a=P, lda=64, sa=64 * 8, b=P, ldb=8, sb=8 * 32, scale=P, ranks=P, n=3, R=8, N=32, K=64, dt=0, x=P, ldx=64,
+def _adapters(L, a=P, lda=64, sa=64 * 256, b=P, ldb=256, sb=256 * 32, scale=P, ranks=P, n=3, R=256, N=32, K=64, dt=0, x=P, ldx=64,
               ids=P, T=4, y=P, ldy=32, out=P, ldo=32, ydt=0, ws=P, size=1 << 20):
     from bit_quantized_moe_token_amd import _lib
     s = _lib.AdaptersSet(a, b, lda, sa, ldb, sb, scale, ranks, n, R, N, K, dt)
@@ -112,7 +112,7 @@ def _adapters(L, a=P, lda=64, sa=64 * 8, b=P, ldb=8, sb=8 * 32, scale=P, ranks=P
 
 @pytest.mark.parametrize("bad,status", [
     (dict(a=None), 1), (dict(a=4097), 1), (dict(lda=63), 1), (dict(sa=-1), 1), (dict(b=None), 1), (dict(b=4097), 1),
-    (dict(ldb=7), 1), (dict(sb=-1), 1), (dict(scale=4098), 1), (dict(ranks=4098), 1), (dict(n=0), 1),
+    (dict(ldb=255), 1), (dict(sb=-1), 1), (dict(scale=4098), 1), (dict(ranks=4098), 1), (dict(n=0), 1),
     (dict(n=(1 << 20) + 1), 2), (dict(R=0), 1), (dict(R=257, ldb=257), 2), (dict(N=0), 1), (dict(N=(1 << 20) + 1), 2),
     (dict(K=0), 1), (dict(K=(1 << 20) + 1), 2), (dict(dt=1), 1), (dict(ydt=2), 1), (dict(x=None), 1), (dict(ldx=63), 1),
     (dict(ids=None), 1), (dict(ids=4097), 1), (dict(T=-1), 1), (dict(T=1 << 22), 2), (dict(y=None), 1), (dict(ldy=31), 1),
@@ -126,7 +126,7 @@ def test_adapters_sizes(L):
     n = ctypes.c_size_t(0)
     assert L.moeq_adapters(None, P, 64, P, 4, P, 32, P, 32, 0, P, 1 << 20, None) == 1
     assert _adapters(L, T=0, x=None, ids=None, y=None, out=None, ws=None, size=0) == 0
-    assert L.moeq_adapters_workspace_size(4, 8, 64, ctypes.byref(n)) == 0 and n.value >= 4 * 8 * 4
+    assert L.moeq_adapters_workspace_size(4, 256, 64, ctypes.byref(n)) == 0 and n.value >= 4 * 256 * 4
     assert _adapters(L, size=n.value - 1) == 3
     for bad, status in (((-1, 8, 64), 1), ((4, 0, 64), 1), ((4, 257, 64), 2), ((4, 8, 0), 1), ((1 << 22, 8, 64), 2)):
         assert L.moeq_adapters_workspace_size(*bad, ctypes.byref(n)) == status
