@@ -37,12 +37,29 @@ template <> struct Frag<MOEQ_BF16> {
   }
 };
 
-// Eight 16-bit values at p, of which the first n exist (zeros behind them).
+// Eight 16-bit values at p.
 __device__ __forceinline__ u32x4 load8(const uint8_t *p) { return *(const __attribute__((address_space(1))) u32x4_a2 *)p; }
-__device__ __forceinline__ u32x4 load8(const uint8_t *p, int n) {
-  Oct<MOEQ_F16> o;
-  o.load(p, 0, n);
-  return u32x4{o.w[0], o.w[1], o.w[2], o.w[3]};
+
+// Values col .. col + 7 of a row of `len` that begins at p, zeros from `valid`
+// (<= len) on.  Near the end of the row the last eight of it are loaded and
+// moved down, so that nothing behind it is touched.
+__device__ __forceinline__ u32x4 load8(const uint8_t *p, int col, int len, int valid) {
+  u32x4 v = {0, 0, 0, 0};
+  if (len < 8) {
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+      if (col + j < valid) v[j / 2] |= (uint32_t)gld<uint16_t>(p + (col + j) * 2) << (16 * (j & 1));
+    return v;
+  }
+  if (col >= valid) return v;
+  const int at = std::min(col, len - 8), down = col - at, n = valid - col;
+  v = load8(p + at * 2);
+  if (down & 4) v = u32x4{v[2], v[3], 0, 0};
+  if (down & 2) v = u32x4{v[1], v[2], v[3], 0};
+  if (down & 1) v = u32x4{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = n >= 2 * i + 2 ? v[i] : n == 2 * i + 1 ? v[i] & 0xffffu : 0;
+  return v;
 }
 
 __device__ __forceinline__ int rank_of(const AdapterArgs &a, int id) {
@@ -196,7 +213,7 @@ __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane
 // another adapter (or none), and rows of A_i beyond R, read a valid row
 // instead: they only reach sums that are not stored.
 template <int TY, int TM, int NT, int D>
-__global__ void __launch_bounds__(kAdapterThreads, TM + NT < 3 ? 4 : TM + NT < 6 ? 3 : 2)
+__global__ void __launch_bounds__(kAdapterThreads, TM + NT < 3 ? 4 : NT < 4 ? 3 : 2)
 adapters_down_kernel(AdapterArgs a) {
   constexpr int NW = kAdapterWaves, GR = NT * kRows;
   constexpr int XI = TM * 2, AI = NT * 2;       // loads of 1 KB: a chunk of x and of A
@@ -219,7 +236,8 @@ adapters_down_kernel(AdapterArgs a) {
   Tile<TM> left = tile;
   // chunks from one that differs from tile to tile: rows are often a power of
   // two apart, and workgroups in step would read the same few memory channels
-  const int first = c0 + place.tile * 5 % chunks, end = c0 + chunks;
+  const int whole = std::min(c0 + chunks, a.K / kChunk) - c0, end = c0 + whole;
+  const int first = c0 + (whole > 0 ? place.tile * 5 % whole : 0);
   for (int cur = left.next(row); cur >= 0; cur = left.next(row)) {
     if (!turn.mine(a)) continue;
     const uint8_t *xp[XI], *ap[AI];
@@ -239,20 +257,12 @@ adapters_down_kernel(AdapterArgs a) {
     for (int m = 0; m < TM; ++m)
 #pragma unroll
       for (int t = 0; t < NT; ++t) acc[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const auto fetch = [&](int i, u32x4 (&x)[XI], u32x4 (&w)[AI]) {   // the part's i-th chunk
-      const int at = first + i, c = at < end ? at : at - chunks;
-      if ((c + 1) * kChunk <= a.K) {
+    const auto fetch = [&](int i, u32x4 (&x)[XI], u32x4 (&w)[AI]) {   // the i-th whole chunk
+      const int c = first + i < end ? first + i : first + i - whole;
 #pragma unroll
-        for (int q = 0; q < XI; ++q) x[q] = load8(xp[q] + c * (kChunk * 2));
+      for (int q = 0; q < XI; ++q) x[q] = load8(xp[q] + c * (kChunk * 2));
 #pragma unroll
-        for (int q = 0; q < AI; ++q) w[q] = load8(ap[q] + c * (kChunk * 2));
-      } else {   // the last columns
-        const int n = a.K - c * kChunk - pc * 8;
-#pragma unroll
-        for (int q = 0; q < XI; ++q) x[q] = load8(xp[q] + c * (kChunk * 2), n);
-#pragma unroll
-        for (int q = 0; q < AI; ++q) w[q] = load8(ap[q] + c * (kChunk * 2), n);
-      }
+      for (int q = 0; q < AI; ++q) w[q] = load8(ap[q] + c * (kChunk * 2));
     };
     const auto step = [&](const u32x4 (&x)[XI], const u32x4 (&w)[AI]) {
 #pragma unroll
@@ -277,13 +287,21 @@ adapters_down_kernel(AdapterArgs a) {
     u32x4 x[D][XI], w[D][AI];
 #pragma unroll
     for (int d = 0; d < D - 1; ++d)
-      if (wave + d * NW < chunks) fetch(wave + d * NW, x[d], w[d]);
-    for (int i = wave; i < chunks; i += D * NW) {
+      if (wave + d * NW < whole) fetch(wave + d * NW, x[d], w[d]);
+    for (int i = wave; i < whole; i += D * NW) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
-        if (i + (d + D - 1) * NW < chunks) fetch(i + (d + D - 1) * NW, x[(d + D - 1) % D], w[(d + D - 1) % D]);
-        if (i + d * NW < chunks) step(x[d], w[d]);
+        if (i + (d + D - 1) * NW < whole) fetch(i + (d + D - 1) * NW, x[(d + D - 1) % D], w[(d + D - 1) % D]);
+        if (i + d * NW < whole) step(x[d], w[d]);
       }
+    }
+    if (whole < chunks && whole % NW == wave) {   // the last columns, by the wave whose turn it is
+      const int col = end * kChunk + pc * 8;
+#pragma unroll
+      for (int q = 0; q < XI; ++q) x[0][q] = load8(xp[q] - pc * 16, col, a.K, a.K);
+#pragma unroll
+      for (int q = 0; q < AI; ++q) w[0][q] = load8(ap[q] - pc * 16, col, a.K, a.K);
+      step(x[0], w[0]);
     }
     // the waves' sums, in wave order
     __syncthreads();
@@ -315,7 +333,7 @@ adapters_down_kernel(AdapterArgs a) {
 // n0 + 16 t + m, columns the rows); the next turn's y and the next step's B (64
 // ranks of one adapter) are loaded meanwhile.
 template <int TY, int TO, int RM>
-__global__ void __launch_bounds__(kAdapterThreads, (RM <= 32 ? 4 : RM <= 128 ? 3 : 2) - (TO == MOEQ_F32 && RM != 256))
+__global__ void __launch_bounds__(kAdapterThreads, RM == 16 && TO != MOEQ_F32 ? 4 : RM > 32 && TO == MOEQ_F32 ? 2 : 3)
 adapters_up_kernel(AdapterArgs a) {
   constexpr int NW = kAdapterWaves, TERMS = TO == MOEQ_F32 ? 3 : 2, NT = RM / kRows;
   constexpr int PB = std::min(RM / 8, 8), BI = PB;   // pieces of a row of B; loads of 64 rows
@@ -345,30 +363,33 @@ adapters_up_kernel(AdapterArgs a) {
   }
   if (!__ballot(own)) return;
   const int n1 = std::min(a.N, (place.part + 1) * a.width);
-  const uint8_t *yp[2];
-  uint8_t *op[2];
+  // y and out along their rows: row pr + 8 h, outputs n0 + 8 pc ..
+  const uint8_t *yp = (const uint8_t *)a.y + ((r0 + pr) * a.ldy + pc * 8) * Val<TO>::size;
+  uint8_t *op = (uint8_t *)a.out + ((r0 + pr) * a.ldo + pc * 8) * Val<TO>::size;
   bool mine[2], plain[2];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {   // y and out along their rows: row pr + 8 h, outputs n0 + 8 pc ..
-    const int r = h * 8 + pr;
-    mine[h] = __shfl((int)own, r, kWave);
-    plain[h] = __shfl(tile.id[0], r, kWave) < 0;
-    yp[h] = (const uint8_t *)a.y + ((r0 + r) * a.ldy + pc * 8) * Val<TO>::size;
-    op[h] = (uint8_t *)a.out + ((r0 + r) * a.ldo + pc * 8) * Val<TO>::size;
+  for (int h = 0; h < 2; ++h) {
+    mine[h] = __shfl((int)own, h * 8 + pr, kWave);
+    plain[h] = __shfl(tile.id[0], h * 8 + pr, kWave) < 0;
   }
   const auto load_y = [&](int n0, Oct<TO> (&y)[2]) {
+    const int n = n0 + 64 <= a.N ? 8 : a.N - n0 - pc * 8;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      if (mine[h]) y[h].load(yp[h], n0, a.N - n0 - pc * 8);
+      if (mine[h]) y[h].load(yp, h * 8 * a.ldy + n0, n);
   };
   const int pb = lane % PB;
   const auto load_b = [&](int n0, int q, int k, u32x4 (&w)[BI]) {   // 64 ranks from k of the q-th adapter
-    const int cur = __builtin_amdgcn_readlane(cur_of, q), n = rank_of(a, cur) - k - pb * 8;
-    const uint8_t *base = (const uint8_t *)a.b + (cur * a.stride_b + k + pb * 8) * 2;
+    const int cur = __builtin_amdgcn_readlane(cur_of, q), rank = rank_of(a, cur);
+    const uint8_t *base = (const uint8_t *)a.b + (cur * a.stride_b + n0 * a.ldb) * 2;
+    if (n0 + 64 <= a.N && k + PB * 8 <= rank) {
+      const uint8_t *at = base + (lane / PB * a.ldb + k + pb * 8) * 2;
 #pragma unroll
-    for (int i = 0; i < BI; ++i) {
-      const int c = std::min(n0 + i * (64 / PB) + lane / PB, a.N - 1);
-      w[i] = load8(base + c * a.ldb * 2, n);
+      for (int i = 0; i < BI; ++i) w[i] = load8(at + i * (64 / PB) * a.ldb * 2);
+    } else {
+#pragma unroll
+      for (int i = 0; i < BI; ++i)
+        w[i] = load8(base + std::min(i * (64 / PB) + lane / PB, a.N - 1 - n0) * a.ldb * 2, k + pb * 8, a.R, rank);
     }
   };
   constexpr int DN = NW * 64;   // from turn to turn of a wave
@@ -410,9 +431,6 @@ adapters_up_kernel(AdapterArgs a) {
   __syncthreads();
   Stage<64> &st = part[wave].in;
   OutTile &ot = part[wave].out;
-  float up[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) up[h] = zt.up[h * 8 + pr];
   for (int n0 = first; n0 < n1; n0 += DN) {
     const bool more = n0 + DN < n1;
     if (more) load_y(n0 + DN, yn);
@@ -428,9 +446,8 @@ adapters_up_kernel(AdapterArgs a) {
 #pragma unroll
         for (int i = 0; i < BI; ++i) st.put(i * (64 / PB) + lane / PB, pb, w[i]);
         lds_order();
-        if (RM > 64 && k + 64 < rank) load_b(n0, q, k + 64, w);
-        else if (q + 1 < count) load_b(n0, q + 1, 0, w);
-        else if (more) load_b(n0 + DN, 0, 0, w);
+        const bool on = RM > 64 && k + 64 < rank, other = q + 1 < count;
+        if (on || other || more) load_b(on || other ? n0 : n0 + DN, on ? q : other ? q + 1 : 0, on ? k + 64 : 0, w);
 #pragma unroll
         for (int h = 0; h < (RM > 32 ? 2 : 1); ++h) {
           if (h && k + 32 >= rank) continue;
@@ -465,15 +482,16 @@ adapters_up_kernel(AdapterArgs a) {
       f32x4 d[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) d[i] = *(const f32x4 *)&ot.v[h * 8 + pr][pc * 8 + i * 4];
-      const int n = a.N - n0 - pc * 8;
+      const int n = n0 + 64 <= a.N ? 8 : a.N - n0 - pc * 8;
       if (!mine[h] || n <= 0) continue;
       if (!plain[h]) {
+        const float up = zt.up[h * 8 + pr];
         float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __builtin_fmaf(d[i >> 2][i & 3], up[h], y[h][i]);
+        for (int i = 0; i < 8; ++i) v[i] = __builtin_fmaf(d[i >> 2][i & 3], up, y[h][i]);
         y[h].pack(v);
       }
-      y[h].store(op[h], n0, n);
+      y[h].store(op, h * 8 * a.ldo + n0, n);
     }
     lds_order();
 #pragma unroll
@@ -481,28 +499,21 @@ adapters_up_kernel(AdapterArgs a) {
   }
 }
 
+constexpr int kLongBatch = 2048;
+
 // How a call is cut: rows per workgroup of the first kernel (16 tm), ranks it
 // forms at a time (16 nt), parts of K.
 struct AdapterPlan {
   int tm, nt, groups, splits, per;
 };
-#ifndef DW
-#define DW 512
-#endif
-#ifndef UW
-#define UW 1024
-#endif
-#ifndef TMT
-#define TMT 2048
-#endif
 static AdapterPlan adapter_plan(int T, int R, int K) {
   AdapterPlan p;
-  p.tm = T >= TMT ? 2 : 1;
+  p.tm = T >= kLongBatch ? 2 : 1;
   p.nt = R <= 16 ? 1 : R <= 32 ? 2 : 4;
   p.groups = (R + p.nt * kRows - 1) / (p.nt * kRows);
   const int tiles = std::max(1, (T + p.tm * kRows - 1) / (p.tm * kRows)) * p.groups, chunks = (K + kChunk - 1) / kChunk;
   const int most = std::min(16, (chunks + kAdapterWaves - 1) / kAdapterWaves);
-  p.splits = std::max(1, std::min(most, DW / tiles));
+  p.splits = std::max(1, std::min(most, 512 / tiles));
   p.per = (chunks + p.splits - 1) / p.splits;
   p.splits = (chunks + p.per - 1) / p.per;
   return p;
@@ -510,8 +521,10 @@ static AdapterPlan adapter_plan(int T, int R, int K) {
 
 // Workgroups that share a tile's adapters: as many as a tile can use, as long
 // as the grid stays within what the card holds at a time (most of them have no
-// work where rows of one adapter stand together).
+// work where rows of one adapter stand together, as they mostly do in long
+// batches: from kLongBatch rows on there are none).
 static int adapter_slots(const AdapterArgs &a, int rows) {
+  if (a.T >= kLongBatch) return 1;
   const int64_t wgs = (int64_t)a.tiles * a.parts;
   return (int)std::max((int64_t)1, std::min((int64_t)std::min(std::min(a.n, a.T), rows), 1024 / wgs));
 }
@@ -528,7 +541,7 @@ template <int TY, int TO, int RM>
 static void launch_up(AdapterArgs a, hipStream_t s) {
   a.tiles = (a.T + kRows - 1) / kRows;
   const int turn = kAdapterWaves * 64, turns = (a.N + turn - 1) / turn;
-  const int parts = std::max(1, std::min(turns, UW / a.tiles));
+  const int parts = std::max(1, std::min(turns, (RM == 16 ? 1024 : 768) / a.tiles));
   a.width = (turns + parts - 1) / parts * turn;
   a.parts = (a.N + a.width - 1) / a.width;
   a.slots = adapter_slots(a, kRows);
