@@ -35,7 +35,6 @@ constexpr int kTopkThreads = 256;
 constexpr int kTopkWaves = kTopkThreads / kWave;
 constexpr int kSegThreads = 256;
 constexpr int kSegWaves = kSegThreads / kWave;
-constexpr int kSegTokens = 64;
 
 __global__ void __launch_bounds__(kTopkThreads)
 route_topk_kernel(const float *__restrict__ logits, int T, int E, int k, int32_t *__restrict__ ids,
@@ -155,8 +154,6 @@ route_place_kernel(const int32_t *__restrict__ ids, int T, int E, int k, int32_t
   }
 }
 
-static inline int route_segments(int T) { return (T + kSegTokens - 1) / kSegTokens; }
-
 // ---- long batches: the placement above counts every pair in every
 // segment (T^2 k / 64 counter updates in all).  Beyond kScanMinTokens the
 // counts go through a workspace instead: each segment's per-expert
@@ -177,35 +174,46 @@ route_count_kernel(const int32_t *__restrict__ ids, int T, int E, int k, int32_t
   for (int e = tid; e < E; e += kSegThreads) hist[(int64_t)seg * E + e] = s_cnt[e];
 }
 
-// One workgroup, one thread per expert: the exclusive prefix of its counts
-// over the segments (in batches of 16 segments, so a batch waits for memory
-// once), then the exclusive scan of the experts' totals (the offsets); each
-// segment's first position per expert is written over its histogram.
-__global__ void __launch_bounds__(kMaxE)
+// One workgroup: every expert's segments in kScanParts parts of consecutive
+// ones, a thread per expert and part.  The parts' sums and the experts' totals
+// give each part's first position, the offsets are the exclusive scan of the
+// totals; then each segment's first position per expert is written over its
+// histogram.  Loads in batches of 16 segments, so that a batch waits for
+// memory once; what a thread has loaded last it does not load again (8192
+// tokens, 256 experts: 24 us with one part and a second pass over all, now
+// SCANUS us).
+constexpr int kScanParts = 4;
+constexpr int kScanThreads = kMaxE * kScanParts;
+constexpr int kScanBatch = 16;
+
+__global__ void __launch_bounds__(kScanThreads)
 route_scan_kernel(int nseg, int E, int32_t *__restrict__ hist, int32_t *__restrict__ offsets) {
-  __shared__ int s_tot[kMaxE];
+  __shared__ int s_part[kScanParts][kMaxE];
   __shared__ int s_off[kMaxE + 1];
-  const int e = threadIdx.x, lane = e & 63, wave = e >> 6;
-  int run = 0;
-  if (e < E) {
-    for (int s0 = 0; s0 < nseg; s0 += 16) {
-      int c[16];
+  const int e = threadIdx.x % kMaxE, part = threadIdx.x / kMaxE, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int per = (nseg + kScanParts - 1) / kScanParts, s0 = std::min(nseg, part * per), s1 = std::min(nseg, s0 + per);
+  int c[2 * kScanBatch];   // the first segments' counts
+  int sum = 0;
 #pragma unroll
-      for (int u = 0; u < 16; ++u) c[u] = s0 + u < nseg ? hist[(int64_t)(s0 + u) * E + e] : 0;
+  for (int u = 0; u < 2 * kScanBatch; ++u) c[u] = e < E && s0 + u < s1 ? hist[(int64_t)(s0 + u) * E + e] : 0;
 #pragma unroll
-      for (int u = 0; u < 16; ++u) {
-        if (s0 + u < nseg) hist[(int64_t)(s0 + u) * E + e] = run;
-        run += c[u];
-      }
-    }
+  for (int u = 0; u < 2 * kScanBatch; ++u) sum += c[u];
+  for (int s = s0 + 2 * kScanBatch; s < s1; s += kScanBatch) {
+    int d[kScanBatch];
+#pragma unroll
+    for (int u = 0; u < kScanBatch; ++u) d[u] = e < E && s + u < s1 ? hist[(int64_t)(s + u) * E + e] : 0;
+#pragma unroll
+    for (int u = 0; u < kScanBatch; ++u) sum += d[u];
   }
-  s_tot[e] = e < E ? run : 0;
+  s_part[part][e] = sum;
   __syncthreads();
   if (wave == 0) {
     int carry = 0;
     for (int base = 0; base < E; base += kWave) {
       const int x = base + lane;
-      const int cnt = x < E ? s_tot[x] : 0;
+      int cnt = 0;
+      if (x < E)
+        for (int q = 0; q < kScanParts; ++q) cnt += s_part[q][x];
       int incl = cnt;
 #pragma unroll
       for (int off = 1; off < kWave; off <<= 1) {
@@ -218,11 +226,24 @@ route_scan_kernel(int nseg, int E, int32_t *__restrict__ hist, int32_t *__restri
     if (lane == 0) s_off[E] = carry;
   }
   __syncthreads();
-  if (e <= E) offsets[e] = s_off[e];
-  if (e == 0 && E == kMaxE) offsets[E] = s_off[E];
-  if (e < E) {
-    const int off = s_off[e];
-    for (int sg = 0; sg < nseg; ++sg) hist[(int64_t)sg * E + e] += off;
+  for (int x = threadIdx.x; x <= E; x += kScanThreads) offsets[x] = s_off[x];
+  if (e >= E) return;
+  int run = s_off[e];
+  for (int q = 0; q < part; ++q) run += s_part[q][e];
+#pragma unroll
+  for (int u = 0; u < 2 * kScanBatch; ++u) {
+    if (s0 + u < s1) hist[(int64_t)(s0 + u) * E + e] = run;
+    run += c[u];
+  }
+  for (int s = s0 + 2 * kScanBatch; s < s1; s += kScanBatch) {
+    int d[kScanBatch];
+#pragma unroll
+    for (int u = 0; u < kScanBatch; ++u) d[u] = s + u < s1 ? hist[(int64_t)(s + u) * E + e] : 0;
+#pragma unroll
+    for (int u = 0; u < kScanBatch; ++u) {
+      if (s + u < s1) hist[(int64_t)(s + u) * E + e] = run;
+      run += d[u];
+    }
   }
 }
 
@@ -262,13 +283,14 @@ route_mass_kernel(const float *__restrict__ gates, const int32_t *__restrict__ o
 size_t route_ws_bytes(int T, int E) { return T > kScanMinTokens ? (size_t)route_segments(T) * E * 4 : 0; }
 
 void launch_place(const int32_t *ids, int T, int E, int k, int32_t *offsets, int32_t *sorted_pairs, int32_t *pair_pos,
-                  void *ws, hipStream_t stream) {
-  const int nseg = route_segments(T);
+                  void *ws, bool counted, hipStream_t stream) {
+  const int nseg = std::max(1, route_segments(T));   // (no tokens: the offsets alone)
   int32_t *hist = nullptr;
   if (T > kScanMinTokens) {
     hist = static_cast<int32_t *>(ws);
-    hipLaunchKernelGGL(route_count_kernel, dim3(nseg), dim3(kSegThreads), 0, stream, ids, T, E, k, hist);
-    hipLaunchKernelGGL(route_scan_kernel, dim3(1), dim3(kMaxE), 0, stream, nseg, E, hist, offsets);
+    if (!counted)
+      hipLaunchKernelGGL(route_count_kernel, dim3(nseg), dim3(kSegThreads), 0, stream, ids, T, E, k, hist);
+    hipLaunchKernelGGL(route_scan_kernel, dim3(1), dim3(kScanThreads), 0, stream, nseg, E, hist, offsets);
   }
   hipLaunchKernelGGL(route_place_kernel, dim3(nseg), dim3(kSegThreads), 0, stream, ids, T, E, k, offsets, sorted_pairs,
                      pair_pos, (const int32_t *)hist);
@@ -313,7 +335,7 @@ MOEQ_API moeq_status moeq_route(const float *logits, int32_t T, int32_t E, int32
   } else {
     hipLaunchKernelGGL(route_topk_kernel, dim3((T + kTopkWaves - 1) / kTopkWaves), dim3(kTopkThreads), 0, stream,
                        logits, T, E, k, out->topk_ids, out->topk_gates);
-    launch_place(out->topk_ids, T, E, k, out->expert_offsets, out->sorted_pairs, out->pair_pos, ws, stream);
+    launch_place(out->topk_ids, T, E, k, out->expert_offsets, out->sorted_pairs, out->pair_pos, ws, false, stream);
   }
   prof_end("route", stream);
   return check_launch("route");

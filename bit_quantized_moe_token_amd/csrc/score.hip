@@ -1,6 +1,11 @@
 // Routing by softmax or sigmoid scores with a bias, groups and renormalised
-// gates (the counting sort is that of route.hip), and its gradient.  One wave
-// per token; lane l holds experts l + 64 s.
+// gates (the counting sort is that of route.hip), and its gradient.
+//
+// Choices are defined in 64 bits, but few tokens have two experts that 32 bits
+// cannot tell apart.  A wave therefore picks its token's experts by choices in
+// fp32 and watches the distance of each from the next; where it is within what
+// fp32 may be off (about one token in a hundred), the same code picks again in
+// 64 bits.  (Choices without a bias are the logits themselves, and exact.)
 #include "check.hpp"
 #include "route.hpp"
 #include "vec8.hpp"
@@ -18,6 +23,9 @@ struct ScoreArgs {
   int groups, top_groups, size;   // size: experts per group
   int sigmoid, top2, renorm;
   float scale;
+  int lanes;           // lanes of a group in the fp32 pick (a power of two), 0: groups of another size
+  int dtype;
+  int32_t *hist;       // [T / kSegTokens, E] pairs of every segment and expert, or null
 };
 
 // An expert, or a group, and what it is chosen by.
@@ -51,21 +59,29 @@ __device__ __forceinline__ float wave_max(float v) {
   return v;
 }
 
+__device__ __forceinline__ float logit(const void *row, int dtype, int e) {
+  float l;
+  if (dtype == MOEQ_F32) l = Val<MOEQ_F32>::get(gld<uint32_t>((const uint8_t *)row + 4 * e));
+  else {
+    const uint32_t bits = gld<uint16_t>((const uint8_t *)row + 2 * e);
+    l = dtype == MOEQ_F16 ? Val<MOEQ_F16>::get(bits) : Val<MOEQ_BF16>::get(bits);
+  }
+  return l == l ? l : -__builtin_inff();
+}
+
+__device__ __forceinline__ const void *logit_row(const ScoreArgs &a, int t) {
+  return (const uint8_t *)a.logits + t * a.ld * (a.dtype == MOEQ_F32 ? 4 : 2);
+}
+
 // Logits of token t, expert lane + 64 s in v[s]; NaN and what lies beyond E
 // as -infinity.
-template <int TY>
-__device__ __forceinline__ void load_row(const void *base, int64_t ld, int t, int E, float *v) {
+__device__ __forceinline__ void load_row(const ScoreArgs &a, int t, float *v) {
   const int lane = threadIdx.x & 63;
-  const uint8_t *row = (const uint8_t *)base + t * ld * Val<TY>::size;
+  const void *row = logit_row(a, t);
 #pragma unroll
   for (int s = 0; s < kSlots; ++s) {
     const int e = lane + s * kWave;
-    float l = -__builtin_inff();
-    if (e < E) {
-      if constexpr (TY == MOEQ_F32) l = Val<TY>::get(gld<uint32_t>(row + 4 * e));
-      else l = Val<TY>::get(gld<uint16_t>(row + 2 * e));
-    }
-    v[s] = l == l ? l : -__builtin_inff();
+    v[s] = e < a.E ? logit(row, a.dtype, e) : -__builtin_inff();
   }
 }
 
@@ -79,15 +95,17 @@ __device__ __forceinline__ double sigmoid64(float l) {
   return (l >= 0.f ? 1.0 : u) / (1.0 + u);
 }
 
-// Routing of token t by one wave: ids and gates of its k experts (and their
-// counts and copies in LDS, where given).
-__device__ __forceinline__ void score_token(const ScoreArgs &a, const float *l, int t, int32_t *__restrict__ ids,
-                                            float *__restrict__ gates, int *s_hist, int *s_ids) {
+// The k experts of token t by one wave in 64 bits: slot j's id and logit in
+// lane j % 64, index j / 64; the largest logit and (softmax) the sum of the
+// exponentials below it.
+__device__ __forceinline__ void pick_exact(const ScoreArgs &a, int t, float *sel, int *sid, float &m, float &total) {
   const int lane = threadIdx.x & 63;
+  float l[kSlots];
+  load_row(a, t, l);
   const double none = -__builtin_inf();
   const int E = a.E, k = a.k;
   double score[kSlots], c[kSlots];
-  float m = l[0];
+  m = l[0];
 #pragma unroll
   for (int s = 1; s < kSlots; ++s) m = __builtin_fmaxf(m, l[s]);
   m = wave_max(m);
@@ -138,9 +156,6 @@ __device__ __forceinline__ void score_token(const ScoreArgs &a, const float *l, 
     }
   }
   uint32_t taken = 0;
-  float sel[kSlots];   // logit of slot j kept by lane j % 64
-  int sid[kSlots];     // its expert id
-  float top = -__builtin_inff();
 #pragma unroll
   for (int s = 0; s < kSlots; ++s) { sel[s] = -__builtin_inff(); sid[s] = 0; }
   for (int j = 0; j < k; ++j) {
@@ -156,64 +171,325 @@ __device__ __forceinline__ void score_token(const ScoreArgs &a, const float *l, 
     for (int s = 0; s < kSlots; ++s)
       if ((id >> 6) == s) v = __shfl(l[s], id & 63, kWave);
     if ((id & 63) == lane) taken |= 1u << (id >> 6);
-    top = __builtin_fmaxf(top, v);
 #pragma unroll
     for (int s = 0; s < kSlots; ++s)
       if (j == lane + s * kWave) { sel[s] = v; sid[s] = id; }
   }
-  // gates from the chosen logits; a renormalised softmax needs no others
-  double g[kSlots], total = 0.0;
+  total = (float)sum;
+}
+
+// ---- the pick in registers: lane l holds experts NS l + s, so that a group of
+// consecutive experts is a run of lanes.  V: float or double.
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(float, dpp_i<CTRL>(__builtin_bit_cast(int, v)));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  const u32x2 b = __builtin_bit_cast(u32x2, v);
+  return __builtin_bit_cast(double, u32x2{(uint32_t)dpp_i<CTRL>((int)b[0]), (uint32_t)dpp_i<CTRL>((int)b[1])});
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_into(int v, int old) {   // lanes of the other rows keep old
+  return __builtin_amdgcn_update_dpp(old, v, CTRL, ROWS, 0xf, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_into(float v, float old) {
+  return __builtin_bit_cast(float, dpp_into<CTRL, ROWS>(__builtin_bit_cast(int, v), __builtin_bit_cast(int, old)));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_into(double v, double old) {
+  const u32x2 b = __builtin_bit_cast(u32x2, v), o = __builtin_bit_cast(u32x2, old);
+  return __builtin_bit_cast(double, u32x2{(uint32_t)dpp_into<CTRL, ROWS>((int)b[0], (int)o[0]),
+                                          (uint32_t)dpp_into<CTRL, ROWS>((int)b[1], (int)o[1])});
+}
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+__device__ __forceinline__ double lane_value(double v, int lane) {
+  const u32x2 b = __builtin_bit_cast(u32x2, v);
+  return __builtin_bit_cast(double, u32x2{(uint32_t)__builtin_amdgcn_readlane((int)b[0], lane),
+                                          (uint32_t)__builtin_amdgcn_readlane((int)b[1], lane)});
+}
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_fmaxf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return __builtin_fmax(a, b); }
+__device__ __forceinline__ float smaller(float a, float b) { return __builtin_fminf(a, b); }
+__device__ __forceinline__ double smaller(double a, double b) { return __builtin_fmin(a, b); }
+
+// Largest value and sum over the wave, the same in every lane: within rows of
+// 16 by exchanges, then row_bcast:15 and row_bcast:31 into lane 63.
+template <typename V>
+__device__ __forceinline__ V all_max(V v) {
+  v = larger(v, dpp<0xb1>(v));
+  v = larger(v, dpp<0x4e>(v));
+  v = larger(v, dpp<0x141>(v));
+  v = larger(v, dpp<0x140>(v));
+  v = larger(v, dpp_into<0x142, 0xa>(v, v));
+  v = larger(v, dpp_into<0x143, 0xc>(v, v));
+  return lane_value(v, 63);
+}
+template <typename V>
+__device__ __forceinline__ V all_sum(V v) {
+  v += dpp<0xb1>(v);
+  v += dpp<0x4e>(v);
+  v += dpp<0x141>(v);
+  v += dpp<0x140>(v);
+  v += dpp_into<0x142, 0xa>(v, (V)0);
+  v += dpp_into<0x143, 0xc>(v, (V)0);
+  return lane_value(v, 63);
+}
+
+// The two largest of two lanes' two largest.
+template <typename V>
+__device__ __forceinline__ void merge2(V &m1, V &m2, V o1, V o2) {
+  m2 = larger(larger(m2, o2), smaller(m1, o1));
+  m1 = larger(m1, o1);
+}
+
+// What fp32 choices may be off, for a choice of size v: the scores are at most
+// 1 and off by less than 14 * 2^-24 (an exponential within 2 steps of an
+// argument rounded to 2^-24 of itself, where s |x| < 0.4; a sum over 256 in a
+// tree; a reciprocal), the bias's addition rounds once.  2^-19 leaves a margin
+// of two.
+__device__ __forceinline__ float choice_error(float v) { return 0x1p-19f * (1.f + __builtin_fabsf(v)); }
+
+// As pick_exact for k <= 64 (slot j in lane j); in fp32, false where that does
+// not decide.
+template <int NS, typename V>
+__device__ __forceinline__ bool pick(const ScoreArgs &a, const float (&l)[NS], float &sel, int &sid, float &m, float &total) {
+  constexpr bool wide = sizeof(V) == 8;
+  const int lane = threadIdx.x & 63;
+  const float out = -__builtin_inff();
+  const V none = -(V)__builtin_inff();
+  const bool exact = wide || !a.bias, by_logit = !a.bias;
+  bool sure = true;
+  m = l[0];
 #pragma unroll
-  for (int s = 0; s < kSlots; ++s) {
-    g[s] = 0.0;
-    if (lane + s * kWave < k) {
-      if (a.sigmoid) g[s] = sigmoid64(sel[s]);
-      else if (a.renorm) g[s] = exp_below(sel[s], top);
-      else g[s] = sum > 0.0 ? exp_below(sel[s], m) / sum : 0.0;
+  for (int s = 1; s < NS; ++s) m = __builtin_fmaxf(m, l[s]);
+  m = all_max(m);
+  V c[NS], score[NS];
+  total = 0.f;
+  if (!by_logit || (a.groups > 1 && a.top2) || (!a.sigmoid && !a.renorm)) {
+    V sum = 0;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      if constexpr (wide) score[s] = a.sigmoid ? sigmoid64(l[s]) : exp_below(l[s], m);
+      else score[s] = a.sigmoid ? __builtin_amdgcn_rcpf(1.f + __expf(-l[s])) : l[s] == out ? 0.f : l[s] == m ? 1.f : expf(l[s] - m);
+      sum += score[s];
     }
-    total += g[s];
+    if (!a.sigmoid) {
+      sum = all_sum(sum);
+      total = (float)sum;
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        if constexpr (wide) score[s] = sum > 0.0 ? score[s] / sum : 0.0;
+        else score[s] *= __builtin_amdgcn_rcpf(sum);
+      }
+    }
   }
-  if (a.renorm) total = wave_sum(total);
+  uint32_t left = 0;   // experts of this lane that can be chosen
 #pragma unroll
-  for (int s = 0; s < kSlots; ++s) {
-    const int j = lane + s * kWave;
-    if (j < k) {
-      const double v = !a.renorm ? g[s] : total > 0.0 ? g[s] / total : 0.0;
-      ids[(int64_t)t * k + j] = sid[s];
-      gates[(int64_t)t * k + j] = (float)((double)a.scale * v);
-      if (s_hist) atomicAdd(&s_hist[sid[s]], 1);
-      if (s_ids) s_ids[t * k + j] = sid[s];
+  for (int s = 0; s < NS; ++s) {
+    const int e = lane * NS + s;
+    if (e < a.E) left |= 1u << s;
+    c[s] = by_logit || e >= a.E ? (V)l[s] : score[s] + (V)a.bias[e];
+    if (!(c[s] == c[s]) || l[s] == out) c[s] = none;
+  }
+  if (a.groups > 1) {
+    V m1 = none, m2 = none;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) merge2(m1, m2, a.top2 && by_logit && l[s] != out ? score[s] : c[s], none);
+    if (a.lanes >= 2) merge2(m1, m2, dpp<0xb1>(m1), dpp<0xb1>(m2));
+    if (a.lanes >= 4) merge2(m1, m2, dpp<0x4e>(m1), dpp<0x4e>(m2));
+    if (a.lanes >= 8) merge2(m1, m2, dpp<0x141>(m1), dpp<0x141>(m2));
+    if (a.lanes >= 16) merge2(m1, m2, dpp<0x140>(m1), dpp<0x140>(m2));
+    if (a.lanes >= 32) merge2(m1, m2, __shfl_xor(m1, 16, kWave), __shfl_xor(m2, 16, kWave));
+    V worth = a.top2 ? m1 + m2 : m1;
+    if (!(worth == worth)) worth = none;
+    const int mine = lane / a.lanes;
+    int rank = 0;
+    for (int g = 0; g < a.groups; ++g) {
+      const V w = lane_value(worth, g * a.lanes);
+      rank += w > worth || (w == worth && g < mine);
+      // (a sum of two is off by twice as much, on either side)
+      if constexpr (!wide)
+        if (!(by_logit && !a.top2) && g != mine && mine < a.groups)
+          sure &= __builtin_fabsf(w - worth) > 4.f * choice_error(w);
     }
+    if (rank >= a.top_groups) left = 0;
+  }
+  V best;       // this lane's best choice left, its logit and index (-1: none left)
+  float at;
+  int which;
+  const auto look = [&]() {
+    best = none;
+    at = 0.f;
+    which = -1;
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+      if ((left >> s & 1) && (which < 0 || c[s] > best)) { best = c[s]; at = l[s]; which = s; }
+  };
+  look();
+  sel = 0.f;
+  sid = 0;
+  V last = -none;   // below what the last one has decided (nothing yet)
+  for (int j = 0; j < a.k; ++j) {
+    const V top = all_max(best);
+    if constexpr (!wide)
+      if (!exact) sure &= !(top >= last);
+    const int from = __builtin_ctzll(__ballot(which >= 0 && best == top));
+    const int w = __builtin_amdgcn_readlane(which, from);
+    const float v = lane_value(at, from);
+    if (lane == j) { sel = v; sid = from * NS + w; }
+    if (lane == from) left &= ~(1u << w);
+    look();
+    if constexpr (!wide) last = top - 2.f * choice_error(top);
+  }
+  if constexpr (!wide)
+    if (!exact) sure &= __ballot(best >= last) == 0;
+  return __ballot(!sure) == 0;
+}
+
+// Gates of the `items` slots whose logits stand in sel, k of each token: a
+// thread each, in 64 bits, so that they are rounded once.  A renormalised
+// softmax needs no logits but the chosen.  (Every thread of the workgroup calls
+// it; the tokens' largest logits and sums in m and total.)
+template <int NTH>
+__device__ __forceinline__ void put_gates(const ScoreArgs &a, int items, const float *sel, const int *sid, const float *m,
+                                          const float *total, double *g, int32_t *__restrict__ ids,
+                                          float *__restrict__ gates) {
+  for (int i = threadIdx.x; i < items; i += NTH) {
+    const int t = i / a.k;
+    float top = m[t];
+    if (!a.sigmoid && a.renorm) {
+      top = sel[t * a.k];
+      for (int j = 1; j < a.k; ++j) top = __builtin_fmaxf(top, sel[t * a.k + j]);
+    }
+    g[i] = a.sigmoid ? sigmoid64(sel[i]) : exp_below(sel[i], top);
+  }
+  if (a.renorm) __syncthreads();
+  for (int i = threadIdx.x; i < items; i += NTH) {
+    const int t = i / a.k;
+    double div = a.sigmoid ? 1.0 : (double)total[t];
+    if (a.renorm) {
+      div = 0.0;
+      for (int j = 0; j < a.k; ++j) div += g[t * a.k + j];
+    }
+    ids[i] = sid[i];
+    gates[i] = div > 0.0 ? (float)((double)a.scale * (g[i] / div)) : 0.f;
   }
 }
 
-template <int TY>
-__global__ void __launch_bounds__(kScoreThreads)
+constexpr int kPickMost = 64;   // slots of a token that go through LDS
+
+// The experts and gates of tokens t0 .. t0 + NW TW - 1 by a workgroup of NW
+// waves, TW tokens each; the pairs also into s_hist and s_ids, where given.
+template <int NS, int NW, int TW>
+struct PickLds {
+  float sel[NW * TW * kPickMost], m[NW * TW], total[NW * TW];
+  int sid[NW * TW * kPickMost];
+  double g[NW * TW * kPickMost];
+};
+template <int NS, int NW, int TW>
+__device__ __forceinline__ void pick_tokens(const ScoreArgs &a, int t0, int32_t *__restrict__ ids, float *__restrict__ gates,
+                                            PickLds<NS, NW, TW> &s, int *s_hist, int *s_ids) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = std::min(NW * TW, a.T - t0);
+  const auto load = [&](int t, float (&l)[NS]) {
+    if (t >= a.T) return;
+    const void *row = logit_row(a, t);
+#pragma unroll
+    for (int q = 0; q < NS; ++q) l[q] = lane * NS + q < a.E ? logit(row, a.dtype, lane * NS + q) : -__builtin_inff();
+  };
+  float next[NS];
+  load(t0 + wave * TW, next);
+#pragma unroll 1
+  for (int i = 0; i < TW; ++i) {
+    const int at = wave * TW + i;
+    if (t0 + at >= a.T) break;
+    float l[NS], sel[kSlots], m, total;
+    int sid[kSlots];
+#pragma unroll
+    for (int q = 0; q < NS; ++q) l[q] = next[q];
+    if (i + 1 < TW) load(t0 + at + 1, next);
+    if (!a.lanes) pick_exact(a, t0 + at, sel, sid, m, total);
+    else if (!pick<NS, float>(a, l, sel[0], sid[0], m, total)) pick<NS, double>(a, l, sel[0], sid[0], m, total);
+    if (lane < a.k) {
+      s.sel[at * a.k + lane] = sel[0];
+      s.sid[at * a.k + lane] = sid[0];
+      if (s_hist) atomicAdd(&s_hist[sid[0]], 1);
+      if (s_ids) s_ids[at * a.k + lane] = sid[0];
+    }
+    if (lane == 0) {
+      s.m[at] = m;
+      s.total[at] = total;
+    }
+  }
+  __syncthreads();
+  const int64_t p = (int64_t)t0 * a.k;
+  put_gates<NW * kWave>(a, n * a.k, s.sel, s.sid, s.m, s.total, s.g, ids + p, gates + p);
+}
+
+// Many tokens.  With hist, a workgroup's NW TW tokens are one segment of the
+// counting sort, whose pairs it counts.
+template <int NS, int NW, int TW>
+__global__ void __launch_bounds__(NW *kWave)
 score_kernel(ScoreArgs a, int32_t *__restrict__ ids, float *__restrict__ gates) {
-  const int t = blockIdx.x * (kScoreThreads / kWave) + (threadIdx.x >> 6);
-  if (t >= a.T) return;
-  float l[kSlots];
-  load_row<TY>(a.logits, a.ld, t, a.E, l);
-  score_token(a, l, t, ids, gates, nullptr, nullptr);
+  __shared__ PickLds<NS, NW, TW> s;
+  __shared__ int s_hist[kMaxE];
+  if (a.hist) {
+    for (int e = threadIdx.x; e < a.E; e += NW * kWave) s_hist[e] = 0;
+    __syncthreads();
+  }
+  pick_tokens<NS, NW, TW>(a, blockIdx.x * (NW * TW), ids, gates, s, a.hist ? s_hist : nullptr, nullptr);
+  if (a.hist)   // (pick_tokens has synchronised after the counts)
+    for (int e = threadIdx.x; e < a.E; e += NW * kWave) a.hist[(int64_t)blockIdx.x * a.E + e] = s_hist[e];
 }
 
 // Up to kRouteTokens tokens: choice and counting sort in one workgroup, a
 // wave per token.
-template <int TY>
+template <int NS>
 __global__ void __launch_bounds__(kRouteTokens * kWave)
 score_route_kernel(ScoreArgs a, RouteOut o) {
   constexpr int NTH = kRouteTokens * kWave;
-  __shared__ RouteLds<kRouteTokens> s;
-  const int t = threadIdx.x >> 6;
-  for (int e = threadIdx.x; e < kMaxE; e += NTH) { s.count[e] = 0; s.run[e] = 0; }
+  __shared__ RouteLds<kRouteTokens> r;
+  __shared__ PickLds<NS, kRouteTokens, 1> s;
+  for (int e = threadIdx.x; e < kMaxE; e += NTH) { r.count[e] = 0; r.run[e] = 0; }
   __syncthreads();
-  if (t < a.T) {
-    float l[kSlots];
-    load_row<TY>(a.logits, a.ld, t, a.E, l);
-    score_token(a, l, t, o.ids, o.gates, s.count, s.ids);
+  pick_tokens<NS, kRouteTokens, 1>(a, 0, o.ids, o.gates, s, r.count, r.ids);
+  place_block<NTH>(o, a.T, a.E, a.k, r);
+}
+
+// More than kPickMost slots: a wave per token, all in 64 bits.
+__global__ void __launch_bounds__(kScoreThreads)
+score_wide_kernel(ScoreArgs a, int32_t *__restrict__ ids, float *__restrict__ gates) {
+  const int lane = threadIdx.x & 63, t = blockIdx.x * (kScoreThreads / kWave) + (threadIdx.x >> 6), k = a.k;
+  if (t >= a.T) return;
+  float sel[kSlots], m, sum;
+  int sid[kSlots];
+  pick_exact(a, t, sel, sid, m, sum);
+  float top = -__builtin_inff();
+#pragma unroll
+  for (int s = 0; s < kSlots; ++s)
+    if (lane + s * kWave < k) top = __builtin_fmaxf(top, sel[s]);
+  top = wave_max(top);
+  double g[kSlots], total = 0.0;
+#pragma unroll
+  for (int s = 0; s < kSlots; ++s) {
+    g[s] = 0.0;
+    if (lane + s * kWave < k) g[s] = a.sigmoid ? sigmoid64(sel[s]) : exp_below(sel[s], a.renorm ? top : m);
+    total += g[s];
   }
-  __syncthreads();
-  place_block<NTH>(o, a.T, a.E, a.k, s);
+  const double div = a.renorm ? wave_sum(total) : a.sigmoid ? 1.0 : (double)sum;
+#pragma unroll
+  for (int s = 0; s < kSlots; ++s) {
+    const int j = lane + s * kWave;
+    if (j < k) {
+      ids[(int64_t)t * k + j] = sid[s];
+      gates[(int64_t)t * k + j] = div > 0.0 ? (float)((double)a.scale * (g[s] / div)) : 0.f;
+    }
+  }
 }
 
 // Gradient of token t's logits.  The chosen experts' own factors are formed
@@ -228,7 +504,7 @@ score_grad_kernel(ScoreArgs a, const int32_t *__restrict__ ids, const float *__r
   if (t >= a.T) return;
   const int E = a.E, k = a.k;
   float l[kSlots];
-  load_row<TY>(a.logits, a.ld, t, E, l);
+  load_row(a, t, l);
   int id[kSlots];
   float sel[kSlots];
   double dg[kSlots], w[kSlots], rest[kSlots];
@@ -338,7 +614,7 @@ static moeq_status check_scoring(const char *who, const moeq_scoring *d, const v
   return MOEQ_OK;
 }
 
-static ScoreArgs score_args(const moeq_scoring *d, const void *logits, int64_t ld, int T, int E, int k) {
+static ScoreArgs score_args(const moeq_scoring *d, const void *logits, int64_t ld, int32_t dtype, int T, int E, int k) {
   ScoreArgs a{};
   a.logits = logits;
   a.ld = ld;
@@ -353,20 +629,35 @@ static ScoreArgs score_args(const moeq_scoring *d, const void *logits, int64_t l
   a.top2 = d->group_score == MOEQ_GROUP_TOP2;
   a.renorm = d->renorm;
   a.scale = d->scale;
+  a.dtype = dtype;
+  const int per = E <= 64 ? 1 : E <= 128 ? 2 : 4, lanes = a.size / per;   // experts of a lane in the fp32 pick
+  a.lanes = a.groups <= 1 ? 64 : a.size % per || (lanes & (lanes - 1)) || lanes > 32 ? 0 : lanes;
   return a;
 }
 
-template <int TY>
+template <int NS>
 static void launch_scored(const ScoreArgs &a, const moeq_routing *r, void *ws, hipStream_t stream) {
-  if (a.T <= kRouteTokens) {
+  if (a.T <= kRouteTokens && a.k <= kPickMost) {
     const RouteOut o{nullptr, r->topk_ids, r->topk_gates, r->expert_offsets, r->sorted_pairs, r->pair_pos};
-    hipLaunchKernelGGL((score_route_kernel<TY>), dim3(1), dim3(kRouteTokens * kWave), 0, stream, a, o);
+    hipLaunchKernelGGL((score_route_kernel<NS>), dim3(1), dim3(kRouteTokens * kWave), 0, stream, a, o);
     return;
   }
-  constexpr int per = kScoreThreads / kWave;
-  hipLaunchKernelGGL((score_kernel<TY>), dim3((a.T + per - 1) / per), dim3(kScoreThreads), 0, stream, a, r->topk_ids,
-                     r->topk_gates);
-  launch_place(r->topk_ids, a.T, a.E, a.k, r->expert_offsets, r->sorted_pairs, r->pair_pos, ws, stream);
+  bool counted = false;
+  if (a.k > kPickMost) {
+    constexpr int per = kScoreThreads / kWave;
+    if (a.T)
+      hipLaunchKernelGGL(score_wide_kernel, dim3((a.T + per - 1) / per), dim3(kScoreThreads), 0, stream, a, r->topk_ids,
+                         r->topk_gates);
+  } else if (route_ws_bytes(a.T, a.E)) {   // the segments' counts go through the workspace
+    ScoreArgs b = a;
+    b.hist = (int32_t *)ws;
+    counted = true;
+    hipLaunchKernelGGL((score_kernel<NS, 16, kSegTokens / 16>), dim3(route_segments(a.T)), dim3(1024), 0, stream, b,
+                       r->topk_ids, r->topk_gates);
+  } else {
+    hipLaunchKernelGGL((score_kernel<NS, 4, 1>), dim3((a.T + 3) / 4), dim3(256), 0, stream, a, r->topk_ids, r->topk_gates);
+  }
+  launch_place(r->topk_ids, a.T, a.E, a.k, r->expert_offsets, r->sorted_pairs, r->pair_pos, ws, counted, stream);
 }
 
 template <int TY>
@@ -402,11 +693,11 @@ MOEQ_API moeq_status moeq_route_scored(const moeq_scoring *d, const void *logits
   const size_t need = route_ws_bytes(T, E);
   if (need > 0 && (!ws || ws_bytes < need))
     return fail(MOEQ_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", who, ws_bytes, need);
-  const ScoreArgs a = score_args(d, logits, ld, T, E, k);
+  const ScoreArgs a = score_args(d, logits, ld, dtype, T, E, k);
   prof_begin("route_scored", stream);
-  if (dtype == MOEQ_F16) launch_scored<MOEQ_F16>(a, out, ws, stream);
-  else if (dtype == MOEQ_BF16) launch_scored<MOEQ_BF16>(a, out, ws, stream);
-  else launch_scored<MOEQ_F32>(a, out, ws, stream);
+  if (E <= 64) launch_scored<1>(a, out, ws, stream);
+  else if (E <= 128) launch_scored<2>(a, out, ws, stream);
+  else launch_scored<4>(a, out, ws, stream);
   prof_end("route_scored", stream);
   return check_launch("route_scored");
 }
@@ -420,7 +711,7 @@ MOEQ_API moeq_status moeq_route_scored_grad(const moeq_scoring *d, const void *l
   MOEQ_TRY(check_matrix(who, "d_logits", d_logits, ldd, E, dtype));
   if (!ids || !d_gates || (((uintptr_t)ids | (uintptr_t)d_gates) & 3))
     return fail(MOEQ_ERR_INVALID, "%s: null or misaligned ids or d_gates", who);
-  const ScoreArgs a = score_args(d, logits, ld, T, E, k);
+  const ScoreArgs a = score_args(d, logits, ld, dtype, T, E, k);
   prof_begin("route_scored_grad", stream);
   if (dtype == MOEQ_F16) launch_scored_grad<MOEQ_F16>(a, ids, d_gates, d_logits, ldd, stream);
   else if (dtype == MOEQ_BF16) launch_scored_grad<MOEQ_BF16>(a, ids, d_gates, d_logits, ldd, stream);
