@@ -187,7 +187,9 @@ constexpr int kScanThreads = kMaxE * kScanParts;
 constexpr int kScanBatch = 16;
 
 __global__ void __launch_bounds__(kScanThreads)
-route_scan_kernel(int nseg, int E, int32_t *__restrict__ hist, int32_t *__restrict__ offsets) {
+route_scan_kernel(int nseg, int E, int32_t *__restrict__ hist, int32_t *__restrict__ offsets, int halves) {
+  // (halves: a word holds the counts of its segment's halves, 16 bits each)
+  const auto count = [&](int v) { return halves ? (v & 0xffff) + (v >> 16) : v; };
   __shared__ int s_part[kScanParts][kMaxE];
   __shared__ int s_off[kMaxE + 1];
   const int e = threadIdx.x % kMaxE, part = threadIdx.x / kMaxE, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -197,13 +199,13 @@ route_scan_kernel(int nseg, int E, int32_t *__restrict__ hist, int32_t *__restri
 #pragma unroll
   for (int u = 0; u < 2 * kScanBatch; ++u) c[u] = e < E && s0 + u < s1 ? hist[(int64_t)(s0 + u) * E + e] : 0;
 #pragma unroll
-  for (int u = 0; u < 2 * kScanBatch; ++u) sum += c[u];
+  for (int u = 0; u < 2 * kScanBatch; ++u) sum += c[u] = count(c[u]);
   for (int s = s0 + 2 * kScanBatch; s < s1; s += kScanBatch) {
     int d[kScanBatch];
 #pragma unroll
     for (int u = 0; u < kScanBatch; ++u) d[u] = e < E && s + u < s1 ? hist[(int64_t)(s + u) * E + e] : 0;
 #pragma unroll
-    for (int u = 0; u < kScanBatch; ++u) sum += d[u];
+    for (int u = 0; u < kScanBatch; ++u) sum += count(d[u]);
   }
   s_part[part][e] = sum;
   __syncthreads();
@@ -242,7 +244,7 @@ route_scan_kernel(int nseg, int E, int32_t *__restrict__ hist, int32_t *__restri
 #pragma unroll
     for (int u = 0; u < kScanBatch; ++u) {
       if (s + u < s1) hist[(int64_t)(s + u) * E + e] = run;
-      run += d[u];
+      run += count(d[u]);
     }
   }
 }
@@ -283,14 +285,14 @@ route_mass_kernel(const float *__restrict__ gates, const int32_t *__restrict__ o
 size_t route_ws_bytes(int T, int E) { return T > kScanMinTokens ? (size_t)route_segments(T) * E * 4 : 0; }
 
 void launch_place(const int32_t *ids, int T, int E, int k, int32_t *offsets, int32_t *sorted_pairs, int32_t *pair_pos,
-                  void *ws, bool counted, hipStream_t stream) {
+                  void *ws, bool halves, hipStream_t stream) {
   const int nseg = std::max(1, route_segments(T));   // (no tokens: the offsets alone)
   int32_t *hist = nullptr;
   if (T > kScanMinTokens) {
     hist = static_cast<int32_t *>(ws);
-    if (!counted)
+    if (!halves)
       hipLaunchKernelGGL(route_count_kernel, dim3(nseg), dim3(kSegThreads), 0, stream, ids, T, E, k, hist);
-    hipLaunchKernelGGL(route_scan_kernel, dim3(1), dim3(kScanThreads), 0, stream, nseg, E, hist, offsets);
+    hipLaunchKernelGGL(route_scan_kernel, dim3(1), dim3(kScanThreads), 0, stream, nseg, E, hist, offsets, (int)halves);
   }
   hipLaunchKernelGGL(route_place_kernel, dim3(nseg), dim3(kSegThreads), 0, stream, ids, T, E, k, offsets, sorted_pairs,
                      pair_pos, (const int32_t *)hist);

@@ -223,12 +223,13 @@ __device__ __forceinline__ void route_block(const RouteOut &o, int T, int E, int
 }
 
 // The counting sort of T * k pairs by their experts ids (kernels of
-// route.hip); ws: route_ws_bytes bytes, which (where there are any) hold each
-// segment's pairs of every expert, [route_segments(T), E], if counted.
+// route.hip); ws: route_ws_bytes bytes, which (where there are any) hold the
+// pairs of each half segment and expert, 16 bits, [route_segments(T), E, 2], if
+// halves.
 constexpr int kSegTokens = 64;
 static inline int route_segments(int T) { return (T + kSegTokens - 1) / kSegTokens; }
 size_t route_ws_bytes(int T, int E);
 void launch_place(const int32_t *ids, int T, int E, int k, int32_t *offsets, int32_t *sorted_pairs, int32_t *pair_pos,
-                  void *ws, bool counted, hipStream_t stream);
+                  void *ws, bool halves, hipStream_t stream);
 
 }  // namespace moeq

@@ -25,7 +25,7 @@ struct ScoreArgs {
   float scale;
   int lanes;           // lanes of a group in the fp32 pick (a power of two), 0: groups of another size
   int dtype;
-  int32_t *hist;       // [T / kSegTokens, E] pairs of every segment and expert, or null
+  uint16_t *hist;      // [segments, E, 2] pairs of every half segment and expert, or null
 };
 
 // An expert, or a group, and what it is chosen by.
@@ -95,10 +95,10 @@ __device__ __forceinline__ double sigmoid64(float l) {
   return (l >= 0.f ? 1.0 : u) / (1.0 + u);
 }
 
-// The k experts of token t by one wave in 64 bits: slot j's id and logit in
-// lane j % 64, index j / 64; the largest logit and (softmax) the sum of the
-// exponentials below it.
-__device__ __forceinline__ void pick_exact(const ScoreArgs &a, int t, float *sel, int *sid, float &m, float &total) {
+// The k experts of token t by one wave in 64 bits: slot j's id in lane j % 64,
+// index j / 64; the largest logit and (softmax) the sum of the exponentials
+// below it.
+__device__ __forceinline__ void pick_exact(const ScoreArgs &a, int t, int *sid, float &m, float &total) {
   const int lane = threadIdx.x & 63;
   float l[kSlots];
   load_row(a, t, l);
@@ -157,7 +157,7 @@ __device__ __forceinline__ void pick_exact(const ScoreArgs &a, int t, float *sel
   }
   uint32_t taken = 0;
 #pragma unroll
-  for (int s = 0; s < kSlots; ++s) { sel[s] = -__builtin_inff(); sid[s] = 0; }
+  for (int s = 0; s < kSlots; ++s) sid[s] = 0;
   for (int j = 0; j < k; ++j) {
     Cand64 b{none, 0x7fffffff};
 #pragma unroll
@@ -166,14 +166,10 @@ __device__ __forceinline__ void pick_exact(const ScoreArgs &a, int t, float *sel
       if (e < E && !((taken >> s) & 1u) && (a.groups == 1 || ((kept >> (e / a.size)) & 1))) b = better(b, Cand64{c[s], e});
     }
     const int id = wave_best(b).id;
-    float v = 0.f;
-#pragma unroll
-    for (int s = 0; s < kSlots; ++s)
-      if ((id >> 6) == s) v = __shfl(l[s], id & 63, kWave);
     if ((id & 63) == lane) taken |= 1u << (id >> 6);
 #pragma unroll
     for (int s = 0; s < kSlots; ++s)
-      if (j == lane + s * kWave) { sel[s] = v; sid[s] = id; }
+      if (j == lane + s * kWave) sid[s] = id;
   }
   total = (float)sum;
 }
@@ -247,23 +243,34 @@ __device__ __forceinline__ void merge2(V &m1, V &m2, V o1, V o2) {
   m1 = larger(m1, o1);
 }
 
-// What fp32 choices may be off, for a choice of size v: the scores are at most
-// 1 and off by less than 14 * 2^-24 (an exponential within 2 steps of an
-// argument rounded to 2^-24 of itself, where s |x| < 0.4; a sum over 256 in a
-// tree; a reciprocal), the bias's addition rounds once.  2^-19 leaves a margin
-// of two.
-__device__ __forceinline__ float choice_error(float v) { return 0x1p-19f * (1.f + __builtin_fabsf(v)); }
+// What fp32 choices may be off, for a choice of size v, in units of 2^-24: a
+// sigmoid 4 (the exponential within 2 of an argument rounded to |l| of itself,
+// where s (1 - s) |l| < 0.23; 1 for the sum, 2 for the reciprocal), a softmax
+// 14 (2 of the exponential, 9 additions, 2 of the reciprocal, 1 of the product;
+// what the arguments' rounding adds to both sides is below s |ln s| each), the
+// bias's addition |v|.  Twice that, rounded up to 8 and 32.
+__device__ __forceinline__ float choice_error(const ScoreArgs &a, float v) {
+  return (a.sigmoid ? 0x1p-21f : 0x1p-19f) * (1.f + __builtin_fabsf(v));
+}
 
-// As pick_exact for k <= 64 (slot j in lane j); in fp32, false where that does
-// not decide.
-template <int NS, typename V>
-__device__ __forceinline__ bool pick(const ScoreArgs &a, const float (&l)[NS], float &sel, int &sid, float &m, float &total) {
-  constexpr bool wide = sizeof(V) == 8;
+template <int NS>
+__device__ __forceinline__ void load_run(const ScoreArgs &a, int t, float (&l)[NS]) {
+  const int lane = threadIdx.x & 63;
+  const void *row = logit_row(a, t);
+#pragma unroll
+  for (int s = 0; s < NS; ++s) l[s] = lane * NS + s < a.E ? logit(row, a.dtype, lane * NS + s) : -__builtin_inff();
+}
+
+// As pick_exact, for k <= 64 (slot j in lane j).
+template <int NS>
+__device__ __forceinline__ void pick_wide(const ScoreArgs &a, int t, int &sid, float &m, float &total) {
+  using V = double;
+  float l[NS];
+  load_run<NS>(a, t, l);
   const int lane = threadIdx.x & 63;
   const float out = -__builtin_inff();
   const V none = -(V)__builtin_inff();
-  const bool exact = wide || !a.bias, by_logit = !a.bias;
-  bool sure = true;
+  const bool by_logit = !a.bias;
   m = l[0];
 #pragma unroll
   for (int s = 1; s < NS; ++s) m = __builtin_fmaxf(m, l[s]);
@@ -274,18 +281,14 @@ __device__ __forceinline__ bool pick(const ScoreArgs &a, const float (&l)[NS], f
     V sum = 0;
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      if constexpr (wide) score[s] = a.sigmoid ? sigmoid64(l[s]) : exp_below(l[s], m);
-      else score[s] = a.sigmoid ? __builtin_amdgcn_rcpf(1.f + __expf(-l[s])) : l[s] == out ? 0.f : l[s] == m ? 1.f : expf(l[s] - m);
+      score[s] = a.sigmoid ? sigmoid64(l[s]) : exp_below(l[s], m);
       sum += score[s];
     }
     if (!a.sigmoid) {
       sum = all_sum(sum);
       total = (float)sum;
 #pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        if constexpr (wide) score[s] = sum > 0.0 ? score[s] / sum : 0.0;
-        else score[s] *= __builtin_amdgcn_rcpf(sum);
-      }
+      for (int s = 0; s < NS; ++s) score[s] = sum > 0.0 ? score[s] / sum : 0.0;
     }
   }
   uint32_t left = 0;   // experts of this lane that can be chosen
@@ -312,63 +315,198 @@ __device__ __forceinline__ bool pick(const ScoreArgs &a, const float (&l)[NS], f
     for (int g = 0; g < a.groups; ++g) {
       const V w = lane_value(worth, g * a.lanes);
       rank += w > worth || (w == worth && g < mine);
-      // (a sum of two is off by twice as much, on either side)
-      if constexpr (!wide)
-        if (!(by_logit && !a.top2) && g != mine && mine < a.groups)
-          sure &= __builtin_fabsf(w - worth) > 4.f * choice_error(w);
     }
     if (rank >= a.top_groups) left = 0;
   }
-  V best;       // this lane's best choice left, its logit and index (-1: none left)
-  float at;
+  V best;       // this lane's best choice left, and its index (-1: none left)
   int which;
   const auto look = [&]() {
     best = none;
-    at = 0.f;
     which = -1;
 #pragma unroll
     for (int s = 0; s < NS; ++s)
-      if ((left >> s & 1) && (which < 0 || c[s] > best)) { best = c[s]; at = l[s]; which = s; }
+      if ((left >> s & 1) && (which < 0 || c[s] > best)) { best = c[s]; which = s; }
   };
   look();
-  sel = 0.f;
   sid = 0;
-  V last = -none;   // below what the last one has decided (nothing yet)
   for (int j = 0; j < a.k; ++j) {
     const V top = all_max(best);
-    if constexpr (!wide)
-      if (!exact) sure &= !(top >= last);
     const int from = __builtin_ctzll(__ballot(which >= 0 && best == top));
     const int w = __builtin_amdgcn_readlane(which, from);
-    const float v = lane_value(at, from);
-    if (lane == j) { sel = v; sid = from * NS + w; }
+    if (lane == j) sid = from * NS + w;
     if (lane == from) left &= ~(1u << w);
     look();
-    if constexpr (!wide) last = top - 2.f * choice_error(top);
   }
-  if constexpr (!wide)
-    if (!exact) sure &= __ballot(best >= last) == 0;
+}
+
+// ---- the same in fp32.  Choices are compared as integers in their order
+// (maxima of integers take one instruction a step, and no NaN is in the way);
+// kGone, below -infinity, for what cannot be chosen.
+constexpr int kGone = (int)0x80000000;
+__device__ __forceinline__ int key_of(float v) {   // (-0 counts as 0)
+  const int b = __builtin_bit_cast(int, v + 0.f);
+  return b ^ (b >> 31 & 0x7fffffff);
+}
+__device__ __forceinline__ float of_key(int k) { return __builtin_bit_cast(float, k ^ (k >> 31 & 0x7fffffff)); }
+template <int CTRL>
+__device__ __forceinline__ int max_dpp(int v) { return std::max(v, dpp_into<CTRL, 0xf>(v, kGone)); }
+__device__ __forceinline__ int all_max(int v) {
+  v = max_dpp<0xb1>(v);
+  v = max_dpp<0x4e>(v);
+  v = max_dpp<0x141>(v);
+  v = max_dpp<0x140>(v);
+  v = std::max(v, dpp_into<0x142, 0xa>(v, kGone));
+  v = std::max(v, dpp_into<0x143, 0xc>(v, kGone));
+  return __builtin_amdgcn_readlane(v, 63);
+}
+template <int CTRL>
+__device__ __forceinline__ void merge2_dpp(int &m1, int &m2) {
+  const int o1 = dpp_into<CTRL, 0xf>(m1, kGone), o2 = dpp_into<CTRL, 0xf>(m2, kGone);
+  m2 = std::max(std::max(m2, o2), std::min(m1, o1));
+  m1 = std::max(m1, o1);
+}
+
+// pick_wide's answer, or false where fp32 does not decide.  Each lane sorts
+// its experts once, so that a round only moves the winner's up.
+template <int NS>
+__device__ __forceinline__ bool pick(const ScoreArgs &a, const float (&l)[NS], int &sid, float &m, float &total) {
+  const int lane = threadIdx.x & 63;
+  const float out = -__builtin_inff();
+  const bool by_logit = !a.bias;
+  bool sure = true;
+  m = l[0];
+#pragma unroll
+  for (int s = 1; s < NS; ++s) m = __builtin_fmaxf(m, l[s]);
+  if (!a.sigmoid) m = of_key(all_max(key_of(m)));
+  float score[NS];
+  total = 0.f;
+  if (!by_logit || (a.groups > 1 && a.top2) || (!a.sigmoid && !a.renorm)) {
+    if (a.sigmoid) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s) score[s] = __builtin_amdgcn_rcpf(1.f + __expf(-l[s]));
+    } else {
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        score[s] = l[s] == out ? 0.f : l[s] == m ? 1.f : expf(l[s] - m);
+        total += score[s];
+      }
+      total = all_sum(total);
+      const float inv = __builtin_amdgcn_rcpf(total);
+#pragma unroll
+      for (int s = 0; s < NS; ++s) score[s] *= inv;
+    }
+  }
+  int c[NS], id[NS];
+#pragma unroll
+  for (int s = 0; s < NS; ++s) {
+    const int e = id[s] = lane * NS + s;
+    float v = l[s];
+    if (!by_logit && e < a.E) {
+      v = score[s] + a.bias[e];
+      if (!(v == v) || l[s] == out) v = out;
+    }
+    c[s] = e < a.E ? key_of(v) : kGone;
+  }
+  if (a.groups > 1) {
+    int m1 = kGone, m2 = kGone;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      const int k = a.top2 && by_logit ? key_of(l[s] == out ? out : score[s]) : c[s];
+      m2 = std::max(m2, std::min(m1, k));
+      m1 = std::max(m1, k);
+    }
+    if (a.lanes >= 2) merge2_dpp<0xb1>(m1, m2);
+    if (a.lanes >= 4) merge2_dpp<0x4e>(m1, m2);
+    if (a.lanes >= 8) merge2_dpp<0x141>(m1, m2);
+    if (a.lanes >= 16) merge2_dpp<0x140>(m1, m2);
+    if (a.lanes >= 32) {
+      const int o1 = __shfl_xor(m1, 16, kWave), o2 = __shfl_xor(m2, 16, kWave);
+      m2 = std::max(std::max(m2, o2), std::min(m1, o1));
+      m1 = std::max(m1, o1);
+    }
+    const int mine = lane / a.lanes;
+    int rank = 0;
+    if (by_logit && !a.top2) {
+      for (int g = 0; g < a.groups; ++g) {
+        const int w = __builtin_amdgcn_readlane(m1, g * a.lanes);
+        rank += w > m1 || (w == m1 && g < mine);
+      }
+    } else {
+      const float worth = of_key(m1) + (a.top2 ? of_key(m2) : 0.f);
+      // (a sum of two is off by twice as much, on either side; no difference
+      // of infinities and NaN is above that)
+      const float tol = 4.f * choice_error(a, worth);
+      for (int g = 0; g < a.groups; ++g) {
+        const float w = lane_value(worth, g * a.lanes);
+        rank += w > worth;
+        sure &= __builtin_fabsf(w - worth) > tol || g == mine;
+      }
+      sure |= mine >= a.groups;
+    }
+    if (rank >= a.top_groups) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s) c[s] = kGone;
+    }
+  }
+  // best first, equal ones by id
+  const auto order = [&](int x, int y) {
+    const bool turn = c[y] > c[x];
+    const int k = turn ? c[y] : c[x], i = turn ? id[y] : id[x];
+    c[y] = turn ? c[x] : c[y];
+    id[y] = turn ? id[x] : id[y];
+    c[x] = k;
+    id[x] = i;
+  };
+#pragma unroll
+  for (int n = 0; n < NS - 1; ++n)   // (neighbours only: equal ones keep their order)
+#pragma unroll
+    for (int s = 0; s < NS - 1 - n; ++s) order(s, s + 1);
+  sid = 0;
+  int last = 0x7fffffff;   // the smallest key that the last one is not surely above
+  for (int j = 0; j < a.k; ++j) {
+    const int top = all_max(c[0]);
+    if (!by_logit) sure &= top < last;
+    const int from = __builtin_ctzll(__ballot(c[0] == top));
+    const int w = __builtin_amdgcn_readlane(id[0], from);
+    if (lane == j) sid = w;
+    const bool won = lane == from;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      c[s] = won ? s + 1 < NS ? c[s + 1 < NS ? s + 1 : s] : kGone : c[s];
+      if (s + 1 < NS) id[s] = won ? id[s + 1 < NS ? s + 1 : s] : id[s];
+    }
+    const float v = of_key(top);
+    last = key_of(v - 2.f * choice_error(a, v));
+  }
+  if (!by_logit) sure &= __ballot(c[0] >= last) == 0;
   return __ballot(!sure) == 0;
 }
 
-// Gates of the `items` slots whose logits stand in sel, k of each token: a
-// thread each, in 64 bits, so that they are rounded once.  A renormalised
-// softmax needs no logits but the chosen.  (Every thread of the workgroup calls
-// it; the tokens' largest logits and sums in m and total.)
+// Gates of the `items` slots (k of each token from t0 on) whose experts stand
+// in sid: a thread each, in 64 bits, so that they are rounded once.  A
+// renormalised softmax needs no logits but the chosen.  (Every thread of the
+// workgroup calls it; the tokens' largest logits and sums in m and total.)
 template <int NTH>
-__device__ __forceinline__ void put_gates(const ScoreArgs &a, int items, const float *sel, const int *sid, const float *m,
-                                          const float *total, double *g, int32_t *__restrict__ ids,
+__device__ __forceinline__ void put_gates(const ScoreArgs &a, int t0, int items, const int *sid, const float *m,
+                                          const float *total, float *sel, double *g, int32_t *__restrict__ ids,
                                           float *__restrict__ gates) {
   for (int i = threadIdx.x; i < items; i += NTH) {
     const int t = i / a.k;
-    float top = m[t];
-    if (!a.sigmoid && a.renorm) {
-      top = sel[t * a.k];
-      for (int j = 1; j < a.k; ++j) top = __builtin_fmaxf(top, sel[t * a.k + j]);
-    }
-    g[i] = a.sigmoid ? sigmoid64(sel[i]) : exp_below(sel[i], top);
+    const float l = logit(logit_row(a, t0 + t), a.dtype, sid[i]);
+    sel[i] = l;
+    if (a.sigmoid) g[i] = sigmoid64(l);
+    else if (!a.renorm) g[i] = exp_below(l, m[t]);
   }
   if (a.renorm) __syncthreads();
+  if (a.renorm && !a.sigmoid) {
+    for (int i = threadIdx.x; i < items; i += NTH) {
+      const int t = i / a.k;
+      float top = sel[t * a.k];
+      for (int j = 1; j < a.k; ++j) top = __builtin_fmaxf(top, sel[t * a.k + j]);
+      g[i] = exp_below(sel[i], top);
+    }
+    __syncthreads();
+  }
   for (int i = threadIdx.x; i < items; i += NTH) {
     const int t = i / a.k;
     double div = a.sigmoid ? 1.0 : (double)total[t];
@@ -396,27 +534,20 @@ __device__ __forceinline__ void pick_tokens(const ScoreArgs &a, int t0, int32_t 
                                             PickLds<NS, NW, TW> &s, int *s_hist, int *s_ids) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = std::min(NW * TW, a.T - t0);
-  const auto load = [&](int t, float (&l)[NS]) {
-    if (t >= a.T) return;
-    const void *row = logit_row(a, t);
-#pragma unroll
-    for (int q = 0; q < NS; ++q) l[q] = lane * NS + q < a.E ? logit(row, a.dtype, lane * NS + q) : -__builtin_inff();
-  };
   float next[NS];
-  load(t0 + wave * TW, next);
+  if (t0 + wave * TW < a.T) load_run<NS>(a, t0 + wave * TW, next);
 #pragma unroll 1
   for (int i = 0; i < TW; ++i) {
     const int at = wave * TW + i;
     if (t0 + at >= a.T) break;
-    float l[NS], sel[kSlots], m, total;
+    float l[NS], m, total;
     int sid[kSlots];
 #pragma unroll
     for (int q = 0; q < NS; ++q) l[q] = next[q];
-    if (i + 1 < TW) load(t0 + at + 1, next);
-    if (!a.lanes) pick_exact(a, t0 + at, sel, sid, m, total);
-    else if (!pick<NS, float>(a, l, sel[0], sid[0], m, total)) pick<NS, double>(a, l, sel[0], sid[0], m, total);
+    if (i + 1 < TW && t0 + at + 1 < a.T) load_run<NS>(a, t0 + at + 1, next);
+    if (!a.lanes) pick_exact(a, t0 + at, sid, m, total);
+    else if (!pick<NS>(a, l, sid[0], m, total)) pick_wide<NS>(a, t0 + at, sid[0], m, total);
     if (lane < a.k) {
-      s.sel[at * a.k + lane] = sel[0];
       s.sid[at * a.k + lane] = sid[0];
       if (s_hist) atomicAdd(&s_hist[sid[0]], 1);
       if (s_ids) s_ids[at * a.k + lane] = sid[0];
@@ -428,11 +559,12 @@ __device__ __forceinline__ void pick_tokens(const ScoreArgs &a, int t0, int32_t 
   }
   __syncthreads();
   const int64_t p = (int64_t)t0 * a.k;
-  put_gates<NW * kWave>(a, n * a.k, s.sel, s.sid, s.m, s.total, s.g, ids + p, gates + p);
+  put_gates<NW * kWave>(a, t0, n * a.k, s.sid, s.m, s.total, s.sel, s.g, ids + p, gates + p);
 }
 
-// Many tokens.  With hist, a workgroup's NW TW tokens are one segment of the
-// counting sort, whose pairs it counts.
+// Many tokens.  With hist, a workgroup's NW TW tokens are half a segment of the
+// counting sort, whose pairs it counts (an expert at most once per token) into
+// its half of the segment's words.
 template <int NS, int NW, int TW>
 __global__ void __launch_bounds__(NW *kWave)
 score_kernel(ScoreArgs a, int32_t *__restrict__ ids, float *__restrict__ gates) {
@@ -444,7 +576,8 @@ score_kernel(ScoreArgs a, int32_t *__restrict__ ids, float *__restrict__ gates) 
   }
   pick_tokens<NS, NW, TW>(a, blockIdx.x * (NW * TW), ids, gates, s, a.hist ? s_hist : nullptr, nullptr);
   if (a.hist)   // (pick_tokens has synchronised after the counts)
-    for (int e = threadIdx.x; e < a.E; e += NW * kWave) a.hist[(int64_t)blockIdx.x * a.E + e] = s_hist[e];
+    for (int e = threadIdx.x; e < a.E; e += NW * kWave)
+      a.hist[((int64_t)(blockIdx.x >> 1) * a.E + e) * 2 + (blockIdx.x & 1)] = (uint16_t)s_hist[e];
 }
 
 // Up to kRouteTokens tokens: choice and counting sort in one workgroup, a
@@ -468,11 +601,13 @@ score_wide_kernel(ScoreArgs a, int32_t *__restrict__ ids, float *__restrict__ ga
   if (t >= a.T) return;
   float sel[kSlots], m, sum;
   int sid[kSlots];
-  pick_exact(a, t, sel, sid, m, sum);
+  pick_exact(a, t, sid, m, sum);
   float top = -__builtin_inff();
 #pragma unroll
-  for (int s = 0; s < kSlots; ++s)
-    if (lane + s * kWave < k) top = __builtin_fmaxf(top, sel[s]);
+  for (int s = 0; s < kSlots; ++s) {
+    sel[s] = lane + s * kWave < k ? logit(logit_row(a, t), a.dtype, sid[s]) : -__builtin_inff();
+    top = __builtin_fmaxf(top, sel[s]);
+  }
   top = wave_max(top);
   double g[kSlots], total = 0.0;
 #pragma unroll
@@ -650,9 +785,9 @@ static void launch_scored(const ScoreArgs &a, const moeq_routing *r, void *ws, h
                          r->topk_gates);
   } else if (route_ws_bytes(a.T, a.E)) {   // the segments' counts go through the workspace
     ScoreArgs b = a;
-    b.hist = (int32_t *)ws;
+    b.hist = (uint16_t *)ws;
     counted = true;
-    hipLaunchKernelGGL((score_kernel<NS, 16, kSegTokens / 16>), dim3(route_segments(a.T)), dim3(1024), 0, stream, b,
+    hipLaunchKernelGGL((score_kernel<NS, 16, kSegTokens / 32>), dim3(2 * route_segments(a.T)), dim3(1024), 0, stream, b,
                        r->topk_ids, r->topk_gates);
   } else {
     hipLaunchKernelGGL((score_kernel<NS, 4, 1>), dim3((a.T + 3) / 4), dim3(256), 0, stream, a, r->topk_ids, r->topk_gates);
