@@ -14,6 +14,7 @@ namespace moeq {
 
 constexpr int kMaxGroups = 64;   // one lane each
 constexpr int kScoreThreads = 256;
+constexpr int kManyTokens = 8192;   // from here on the gradient takes 16 tokens a workgroup, not 4
 
 struct ScoreArgs {
   const void *logits;
@@ -627,12 +628,141 @@ score_wide_kernel(ScoreArgs a, int32_t *__restrict__ ids, float *__restrict__ ga
   }
 }
 
-// Gradient of token t's logits.  The chosen experts' own factors are formed
-// in lane j (slot j) in 64 bits, from the logits alone; with renorm the
-// softmax's gradient is zero but for the chosen, s_e (v_e - 0).
+// Gradient of the logits of NT tokens by a workgroup of four waves.  What a
+// chosen expert gets is formed by one thread per (token, slot) in 64 bits, from
+// the chosen logits alone, and put into the token's row in LDS; the rows leave
+// along their length.  Only a softmax over all E without renorm reads (and
+// gives a gradient to) the other logits: s_e (v_e - sum_i v_i s_i) in fp32.
+// (With renorm that sum is zero.)
+template <int NT>
+struct GradLds {
+  int id[NT * kPickMost];
+  float l[NT * kPickMost], dg[NT * kPickMost], add[NT * kPickMost], m[NT], down[NT], inv[NT];
+  double w[NT * kPickMost], total[NT];
+  __attribute__((aligned(16))) float d[NT][kMaxE];
+};
+
+template <int NT>
+__global__ void __launch_bounds__(kScoreThreads)
+score_grad_kernel(ScoreArgs a, const int32_t *__restrict__ ids, const float *__restrict__ d_gates, void *out, int64_t ldd) {
+  constexpr int TW = NT / (kScoreThreads / kWave);
+  __shared__ GradLds<NT> s;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int t0 = blockIdx.x * NT, k = a.k, E = a.E, items = std::min(NT, a.T - t0) * k;
+  const bool dense = !a.sigmoid && !a.renorm;
+  for (int i = tid; i < items; i += kScoreThreads) {
+    const int64_t p = (int64_t)t0 * k + i;
+    const int id = ids[p];
+    const bool ok = (uint32_t)id < (uint32_t)E;
+    s.id[i] = ok ? id : -1;
+    s.dg[i] = d_gates[p];
+    s.l[i] = ok ? logit(logit_row(a, t0 + i / k), a.dtype, id) : -__builtin_inff();
+  }
+#pragma unroll
+  for (int i = 0; i < NT * kMaxE / 4 / kScoreThreads; ++i) *(f32x4 *)&s.d[0][(i * kScoreThreads + tid) * 4] = f32x4{0.f, 0.f, 0.f, 0.f};
+  float u[TW][4];   // dense: exponentials of experts 4 lane ..
+  if (dense) {
+#pragma unroll
+    for (int i = 0; i < TW; ++i) {
+      const int t = wave * TW + i;
+      if (t0 + t >= a.T) continue;
+      load_run<4>(a, t0 + t, u[i]);
+      const float m = of_key(all_max(key_of(__builtin_fmaxf(__builtin_fmaxf(u[i][0], u[i][1]), __builtin_fmaxf(u[i][2], u[i][3])))));
+      float sum = 0.f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float l = u[i][q];
+        u[i][q] = l == -__builtin_inff() ? 0.f : l == m ? 1.f : expf(l - m);
+        sum += u[i][q];
+      }
+      sum = all_sum(sum);
+      if (lane == 0) {
+        s.m[t] = m;
+        s.total[t] = sum;
+        s.inv[t] = sum > 0.f ? 1.f / sum : 0.f;
+      }
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < items; i += kScoreThreads) {
+    const int t = i / k;
+    double w = 0.0;
+    if (s.id[i] >= 0) {
+      if (a.sigmoid) w = sigmoid64(s.l[i]);
+      else if (dense) w = s.total[t] > 0.0 ? exp_below(s.l[i], s.m[t]) / s.total[t] : 0.0;
+      else {
+        float top = s.l[t * k];
+        for (int j = 1; j < k; ++j) top = __builtin_fmaxf(top, s.l[t * k + j]);
+        w = exp_below(s.l[i], top);
+      }
+    }
+    s.w[i] = w;
+  }
+  __syncthreads();
+  for (int i = tid; i < items; i += kScoreThreads) {
+    const int t = i / k;
+    double total = 0.0, mean = 0.0, v = 0.0;   // mean: sum_i dg_i s_i
+    if (a.renorm || dense) {
+      for (int j = 0; j < k; ++j) {
+        const double w = s.w[t * k + j];
+        total += w;
+        if (w > 0.0) mean += (double)s.dg[t * k + j] * w;
+      }
+    }
+    if (dense) {
+      v = s.id[i] >= 0 ? s.dg[i] : 0.0;
+      if (i == t * k) s.down[t] = (float)((double)a.scale * mean);
+    } else if (s.w[i] > 0.0) {
+      v = a.renorm ? ((double)s.dg[i] - mean / total) * (s.w[i] / total) : (double)s.dg[i] * s.w[i];
+      if (a.sigmoid) v *= sigmoid64(-s.l[i]);
+    }
+    s.add[i] = (float)((double)a.scale * v);
+  }
+  __syncthreads();
+  for (int i = tid; i < items; i += kScoreThreads) {   // an expert's first slot adds up all that are its
+    const int t = i / k, id = s.id[i];
+    float sum = 0.f;
+    int before = 0;
+    for (int j = 0; j < k; ++j) {
+      if (s.id[t * k + j] != id) continue;
+      sum += s.add[t * k + j];
+      before += t * k + j < i;
+    }
+    if (id >= 0 && !before) s.d[t][id] = sum;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < TW; ++i) {
+    const int t = wave * TW + i, n = E - lane * 4;
+    if (t0 + t >= a.T || n <= 0) continue;
+    f32x4 d = *(const f32x4 *)&s.d[t][lane * 4];
+    if (dense) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) d[q] = u[i][q] > 0.f ? u[i][q] * s.inv[t] * (d[q] - s.down[t]) : 0.f;
+    }
+    const int64_t at = (int64_t)(t0 + t) * ldd + lane * 4;
+    if (a.dtype == MOEQ_F32) {
+      float *o = (float *)out + at;
+      if (n >= 4) *(u32x4_a4 *)o = __builtin_bit_cast(u32x4, d);
+      else
+        for (int q = 0; q < n; ++q) o[q] = q == 0 ? d[0] : q == 1 ? d[1] : d[2];
+    } else {
+      uint16_t *o = (uint16_t *)out + at;
+      uint32_t b[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) b[q] = a.dtype == MOEQ_F16 ? Val<MOEQ_F16>::put(d[q]) : Val<MOEQ_BF16>::put(d[q]);
+      typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+      if (n >= 4) *(u32x2_a2 *)o = u32x2{b[0] | b[1] << 16, b[2] | b[3] << 16};
+      else
+        for (int q = 0; q < n; ++q) o[q] = (uint16_t)(q == 0 ? b[0] : q == 1 ? b[1] : b[2]);
+    }
+  }
+}
+
+// More than kPickMost slots: a wave per token, slot j in lane j % 64.
 template <int TY>
 __global__ void __launch_bounds__(kScoreThreads)
-score_grad_kernel(ScoreArgs a, const int32_t *__restrict__ ids, const float *__restrict__ d_gates, void *out,
+score_grad_wide_kernel(ScoreArgs a, const int32_t *__restrict__ ids, const float *__restrict__ d_gates, void *out,
                   int64_t ldd) {
   const int t = blockIdx.x * (kScoreThreads / kWave) + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
@@ -799,8 +929,8 @@ template <int TY>
 static void launch_scored_grad(const ScoreArgs &a, const int32_t *ids, const float *dg, void *out, int64_t ldd,
                                hipStream_t stream) {
   constexpr int per = kScoreThreads / kWave;
-  hipLaunchKernelGGL((score_grad_kernel<TY>), dim3((a.T + per - 1) / per), dim3(kScoreThreads), 0, stream, a, ids, dg, out,
-                     ldd);
+  hipLaunchKernelGGL((score_grad_wide_kernel<TY>), dim3((a.T + per - 1) / per), dim3(kScoreThreads), 0, stream, a, ids, dg,
+                     out, ldd);
 }
 
 }  // namespace moeq
@@ -848,7 +978,13 @@ MOEQ_API moeq_status moeq_route_scored_grad(const moeq_scoring *d, const void *l
     return fail(MOEQ_ERR_INVALID, "%s: null or misaligned ids or d_gates", who);
   const ScoreArgs a = score_args(d, logits, ld, dtype, T, E, k);
   prof_begin("route_scored_grad", stream);
-  if (dtype == MOEQ_F16) launch_scored_grad<MOEQ_F16>(a, ids, d_gates, d_logits, ldd, stream);
+  if (k <= kPickMost && T >= kManyTokens)
+    hipLaunchKernelGGL((score_grad_kernel<16>), dim3((T + 15) / 16), dim3(kScoreThreads), 0, stream, a, ids, d_gates,
+                       d_logits, ldd);
+  else if (k <= kPickMost)
+    hipLaunchKernelGGL((score_grad_kernel<4>), dim3((T + 3) / 4), dim3(kScoreThreads), 0, stream, a, ids, d_gates, d_logits,
+                       ldd);
+  else if (dtype == MOEQ_F16) launch_scored_grad<MOEQ_F16>(a, ids, d_gates, d_logits, ldd, stream);
   else if (dtype == MOEQ_BF16) launch_scored_grad<MOEQ_BF16>(a, ids, d_gates, d_logits, ldd, stream);
   else launch_scored_grad<MOEQ_F32>(a, ids, d_gates, d_logits, ldd, stream);
   prof_end("route_scored_grad", stream);
