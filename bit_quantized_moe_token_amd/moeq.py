@@ -248,20 +248,27 @@ def quantize_block(w, fmt, bits, G):
 # -------------------------------------------------------------- routing
 
 class RoutingOut:
+    """Tensors of one routing; the integer ones are parts of one buffer (an
+    allocation costs the host 1.8 us)."""
+
     def __init__(self, T, E, k, device):
         self.T, self.E, self.k = T, E, k
         P = T * k
-        self.ids = torch.empty((T, k), dtype=torch.int32, device=device)
+        ids, self.sorted_pairs, self.pair_pos, self.offsets = torch.empty(
+            (3 * P + E + 1,), dtype=torch.int32, device=device).split((P, P, P, E + 1))
+        self.ids = ids.view(T, k)
         self.gates = torch.empty((T, k), dtype=torch.float32, device=device)
-        self.offsets = torch.empty((E + 1,), dtype=torch.int32, device=device)
-        self.sorted_pairs = torch.empty((P,), dtype=torch.int32, device=device)
-        self.pair_pos = torch.empty((P,), dtype=torch.int32, device=device)
         self.c = _lib.Routing(self.ids.data_ptr(), self.gates.data_ptr(), self.offsets.data_ptr(),
                               self.sorted_pairs.data_ptr(), self.pair_pos.data_ptr())
-        n = ctypes.c_size_t(0)
-        check(lib().moeq_route_workspace_size(T, E, k, ctypes.byref(n)), "moeq_route_workspace_size")
-        self.ws = torch.empty((max(1, n.value),), dtype=torch.uint8, device=device)
-        self.ws_bytes = n.value
+        self.ws_bytes = _route_workspace_size(T, E, k)
+        self.ws = torch.empty((self.ws_bytes,), dtype=torch.uint8, device=device) if self.ws_bytes else None
+
+
+@functools.lru_cache(maxsize=1024)
+def _route_workspace_size(T, E, k):
+    n = ctypes.c_size_t(0)
+    check(lib().moeq_route_workspace_size(T, E, k, ctypes.byref(n)), "moeq_route_workspace_size")
+    return n.value
 
 
 def route(logits, k, out=None):
@@ -628,7 +635,7 @@ def route_scored(logits, k, score="softmax", bias=None, groups=1, top_groups=Non
         for t in (out.ids, out.gates, out.offsets, out.sorted_pairs, out.pair_pos):
             _written(t)
     _launch("moeq_route_scored", dev, d, logits.data_ptr(), _ld(logits), _DTYPE[logits.dtype], T, E, k, out.c,
-            out.ws.data_ptr(), out.ws_bytes)
+            _addr(out.ws), out.ws_bytes)
     return out
 
 
