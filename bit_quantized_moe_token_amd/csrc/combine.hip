@@ -2,6 +2,7 @@
 // gradients of rows and gates.
 #include "check.hpp"
 #include "vec8.hpp"
+#include "wave.hpp"
 
 namespace moeq {
 
@@ -54,47 +55,64 @@ combine_kernel(CombineArgs a) {
   o.store(a.out, t * a.ldo + c, n);
 }
 
-// One workgroup per token: for every slot its row's gradient and the product
-// of its row with dy.
+// One workgroup per token: dy is read once for SLOTS pairs at a time, whose rows
+// are all loaded before the first is used.
 template <int TR, int TO>
 __global__ void __launch_bounds__(kCombineThreads)
 combine_grad_kernel(CombineArgs a) {
-  __shared__ float part[kCombineThreads / kWave];
+  constexpr int SLOTS = TR == MOEQ_F32 ? 4 : 8, NW = kCombineThreads / kWave;
+  __shared__ float part[2][NW][SLOTS];
   const int t = blockIdx.x, tid = threadIdx.x;
-  for (int j = 0; j < a.k; ++j) {
-    const int64_t p = (int64_t)t * a.k + j;
-    const int at = a.pos[p];
-    const bool ok = (uint32_t)at < (uint32_t)a.P;
-    const float g = a.gates ? a.gates[p] : 1.f;
-    float dot = 0.f;
-    for (int c = tid * 8; ok && c < a.N; c += kCombineThreads * 8) {
+  for (int j0 = 0; j0 < a.k; j0 += SLOTS) {
+    int at[SLOTS];
+    float g[SLOTS], dot[SLOTS];
+#pragma unroll
+    for (int j = 0; j < SLOTS; ++j) {
+      const int64_t p = (int64_t)t * a.k + j0 + j;
+      const bool in = j0 + j < a.k;
+      at[j] = in ? a.pos[p] : -1;
+      g[j] = in && a.gates ? a.gates[p] : 1.f;
+      if ((uint32_t)at[j] >= (uint32_t)a.P) at[j] = -1;
+      dot[j] = 0.f;
+    }
+    for (int c = tid * 8; c < a.N; c += kCombineThreads * 8) {
       const int n = a.N - c;
       Oct<TO> d;
+      Oct<TR> r[SLOTS];
       d.load(a.tok, t * a.ldt + c, n);
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = g * d[i];
       if (a.d_gates) {
-        Oct<TR> r;
-        r.load(a.rows, at * a.ldr + c, n);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dot += d[i] * r[i];
+        for (int j = 0; j < SLOTS; ++j)
+          if (at[j] >= 0) r[j].load(a.rows, at[j] * a.ldr + c, n);
       }
-      Oct<TR> o;
-      o.pack(v);
-      o.store(a.out, at * a.ldo + c, n);
+#pragma unroll
+      for (int j = 0; j < SLOTS; ++j) {
+        if (at[j] < 0) continue;
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[i] = g[j] * d[i];
+          if (a.d_gates) dot[j] += d[i] * r[j][i];
+        }
+        Oct<TR> o;
+        o.pack(v);
+        o.store(a.out, at[j] * a.ldo + c, n);
+      }
     }
-    if (a.d_gates) {
+    if (!a.d_gates) continue;
+    // (two halves in turn: a wave may be in the next slots before all have read)
+    float (*p)[SLOTS] = part[(j0 / SLOTS) & 1];
 #pragma unroll
-      for (int m = 32; m >= 1; m >>= 1) dot += __shfl_xor(dot, m, kWave);
-      if ((tid & 63) == 0) part[tid >> 6] = dot;
-      __syncthreads();
-      if (tid == 0) {
-        float s = 0.f;
-        for (int w = 0; w < kCombineThreads / kWave; ++w) s += part[w];
-        a.d_gates[p] = s;
-      }
-      __syncthreads();
+    for (int j = 0; j < SLOTS; ++j) {
+      const float v = all_sum(dot[j]);
+      if ((tid & 63) == 0) p[tid >> 6][j] = v;
+    }
+    __syncthreads();
+    if (tid < SLOTS && j0 + tid < a.k) {
+      float v = p[0][tid];
+#pragma unroll
+      for (int w = 1; w < NW; ++w) v += p[w][tid];
+      a.d_gates[(int64_t)t * a.k + j0 + tid] = v;
     }
   }
 }
