@@ -26,6 +26,7 @@ struct CombineArgs {
 template <int TR, int TO>
 __global__ void __launch_bounds__(kCombineThreads)
 combine_kernel(CombineArgs a) {
+  constexpr int SLOTS = 4;   // rows under way at a time
   const int t = blockIdx.x * (kCombineThreads >> a.lanes) + (threadIdx.x >> a.lanes);
   const int c = ((blockIdx.y << a.lanes) + (threadIdx.x & ((1 << a.lanes) - 1))) * 8;
   const int n = a.N - c;
@@ -40,15 +41,25 @@ combine_kernel(CombineArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;
   }
-  for (int j = 0; j < a.k; ++j) {
-    const int64_t p = (int64_t)t * a.k + j;
-    const int at = a.pos[p];
-    if ((uint32_t)at >= (uint32_t)a.P) continue;
-    const float g = a.gates ? a.gates[p] : 1.f;
-    Oct<TR> r;
-    r.load(a.rows, at * a.ldr + c, n);
+  for (int j0 = 0; j0 < a.k; j0 += SLOTS) {
+    const int64_t p = (int64_t)t * a.k + j0;
+    int at[SLOTS];
+    float g[SLOTS];
+    Oct<TR> r[SLOTS];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] += g * r[i];
+    for (int j = 0; j < SLOTS; ++j) {
+      at[j] = j0 + j < a.k ? a.pos[p + j] : -1;
+      g[j] = j0 + j < a.k && a.gates ? a.gates[p + j] : 1.f;
+    }
+#pragma unroll
+    for (int j = 0; j < SLOTS; ++j)
+      if ((uint32_t)at[j] < (uint32_t)a.P) r[j].load(a.rows, at[j] * a.ldr + c, n);
+#pragma unroll
+    for (int j = 0; j < SLOTS; ++j)
+      if ((uint32_t)at[j] < (uint32_t)a.P) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] += g[j] * r[j][i];
+      }
   }
   Oct<TO> o;
   o.pack(acc);
