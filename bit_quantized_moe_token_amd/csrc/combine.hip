@@ -34,7 +34,7 @@ combine_kernel(CombineArgs a) {
   float acc[8];
   if (a.tok) {
     Oct<TO> b;
-    b.load(a.tok, t * a.ldt + c, n);
+    b.load(a.tok, t * a.ldt + c, n, true);
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = b[i];
   } else {
@@ -53,7 +53,7 @@ combine_kernel(CombineArgs a) {
     }
 #pragma unroll
     for (int j = 0; j < SLOTS; ++j)
-      if ((uint32_t)at[j] < (uint32_t)a.P) r[j].load(a.rows, at[j] * a.ldr + c, n);
+      if ((uint32_t)at[j] < (uint32_t)a.P) r[j].load(a.rows, at[j] * a.ldr + c, n, true);
 #pragma unroll
     for (int j = 0; j < SLOTS; ++j)
       if ((uint32_t)at[j] < (uint32_t)a.P) {
@@ -63,7 +63,7 @@ combine_kernel(CombineArgs a) {
   }
   Oct<TO> o;
   o.pack(acc);
-  o.store(a.out, t * a.ldo + c, n);
+  o.store(a.out, t * a.ldo + c, n, true);
 }
 
 // One workgroup per token: dy is read once for SLOTS pairs at a time, whose rows
@@ -90,11 +90,11 @@ combine_grad_kernel(CombineArgs a) {
       const int n = a.N - c;
       Oct<TO> d;
       Oct<TR> r[SLOTS];
-      d.load(a.tok, t * a.ldt + c, n);
+      d.load(a.tok, t * a.ldt + c, n, true);
       if (a.d_gates) {
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j)
-          if (at[j] >= 0) r[j].load(a.rows, at[j] * a.ldr + c, n);
+          if (at[j] >= 0) r[j].load(a.rows, at[j] * a.ldr + c, n, true);
       }
 #pragma unroll
       for (int j = 0; j < SLOTS; ++j) {
@@ -107,7 +107,7 @@ combine_grad_kernel(CombineArgs a) {
         }
         Oct<TR> o;
         o.pack(v);
-        o.store(a.out, at[j] * a.ldo + c, n);
+        o.store(a.out, at[j] * a.ldo + c, n, true);
       }
     }
     if (!a.d_gates) continue;

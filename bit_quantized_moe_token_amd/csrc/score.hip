@@ -701,7 +701,7 @@ score_grad_kernel(ScoreArgs a, const int32_t *__restrict__ ids, const float *__r
     const int64_t at = (int64_t)(t0 + t) * ldd + lane * 4;
     if (a.dtype == MOEQ_F32) {
       float *o = (float *)out + at;
-      if (n >= 4) *(u32x4_a4 *)o = __builtin_bit_cast(u32x4, d);
+      if (n >= 4) __builtin_nontemporal_store(__builtin_bit_cast(u32x4, d), (u32x4_a4 *)o);
       else
         for (int q = 0; q < n; ++q) o[q] = q == 0 ? d[0] : q == 1 ? d[1] : d[2];
     } else {
@@ -710,7 +710,7 @@ score_grad_kernel(ScoreArgs a, const int32_t *__restrict__ ids, const float *__r
 #pragma unroll
       for (int q = 0; q < 4; ++q) b[q] = a.dtype == MOEQ_F16 ? Val<MOEQ_F16>::put(d[q]) : Val<MOEQ_BF16>::put(d[q]);
       typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
-      if (n >= 4) *(u32x2_a2 *)o = u32x2{b[0] | b[1] << 16, b[2] | b[3] << 16};
+      if (n >= 4) __builtin_nontemporal_store(u32x2{b[0] | b[1] << 16, b[2] | b[3] << 16}, (u32x2_a2 *)o);
       else
         for (int q = 0; q < n; ++q) o[q] = (uint16_t)(q == 0 ? b[0] : q == 1 ? b[1] : b[2]);
     }

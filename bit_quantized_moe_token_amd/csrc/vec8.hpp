@@ -36,12 +36,14 @@ struct Oct {
   using Loose = typename Val<TY>::Loose;
   uint32_t w[W];
 
-  __device__ __forceinline__ void load(const void *base, int64_t i, int n) {
+  // (nt: non-temporal, for rows that are read, or written, once)
+  __device__ __forceinline__ void load(const void *base, int64_t i, int n, bool nt = false) {
     const uint8_t *p = (const uint8_t *)base + i * Val<TY>::size;
     if (n >= 8) {
 #pragma unroll
       for (int q = 0; q < W / 4; ++q) {
-        const u32x4 v = ((const __attribute__((address_space(1))) Loose *)p)[q];
+        const auto at = &((const __attribute__((address_space(1))) Loose *)p)[q];
+        const u32x4 v = nt ? __builtin_nontemporal_load(at) : *at;
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[4 * q + j] = v[j];
       }
@@ -77,12 +79,16 @@ struct Oct {
       else w[j] = Val<TY>::put(v[2 * j]) | (Val<TY>::put(v[2 * j + 1]) << 16);
     }
   }
-  __device__ __forceinline__ void store(void *base, int64_t i, int n) const {
+  __device__ __forceinline__ void store(void *base, int64_t i, int n, bool nt = false) const {
     uint8_t *p = (uint8_t *)base + i * Val<TY>::size;
     if (n >= 8) {
 #pragma unroll
-      for (int q = 0; q < W / 4; ++q)
-        ((__attribute__((address_space(1))) Loose *)p)[q] = u32x4{w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]};
+      for (int q = 0; q < W / 4; ++q) {
+        const auto at = &((__attribute__((address_space(1))) Loose *)p)[q];
+        const Loose v = u32x4{w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]};
+        if (nt) __builtin_nontemporal_store(v, at);
+        else *at = v;
+      }
     } else {
 #pragma unroll
       for (int j = 0; j < 7; ++j)
