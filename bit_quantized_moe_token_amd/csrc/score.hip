@@ -392,9 +392,11 @@ __device__ __forceinline__ bool pick(const ScoreArgs &a, const float (&l)[NS], i
       }
     } else {
       const float worth = of_key(m1) + (a.top2 ? of_key(m2) : 0.f);
-      // (a sum of two is off by twice as much, on either side; no difference
-      // of infinities and NaN is above that)
-      const float tol = 4.f * choice_error(a, worth);
+      // (a sum of two is off by what both are, on either side: from the largest
+      // of any group, since they may cancel; no difference of infinities and
+      // NaN is above that)
+      const float size = __builtin_fabsf(of_key(m1)) + (a.top2 ? __builtin_fabsf(of_key(m2)) : 0.f);
+      const float tol = 4.f * choice_error(a, of_key(all_max(mine < a.groups ? key_of(size) : kGone)));
       for (int g = 0; g < a.groups; ++g) {
         const float w = lane_value(worth, g * a.lanes);
         rank += w > worth;

@@ -253,6 +253,7 @@ class RoutingOut:
 
     def __init__(self, T, E, k, device):
         self.T, self.E, self.k = T, E, k
+        self.ws_bytes = _route_workspace_size(T, E, k)
         P = T * k
         ids, self.sorted_pairs, self.pair_pos, self.offsets = torch.empty(
             (3 * P + E + 1,), dtype=torch.int32, device=device).split((P, P, P, E + 1))
@@ -260,7 +261,6 @@ class RoutingOut:
         self.gates = torch.empty((T, k), dtype=torch.float32, device=device)
         self.c = _lib.Routing(self.ids.data_ptr(), self.gates.data_ptr(), self.offsets.data_ptr(),
                               self.sorted_pairs.data_ptr(), self.pair_pos.data_ptr())
-        self.ws_bytes = _route_workspace_size(T, E, k)
         self.ws = torch.empty((self.ws_bytes,), dtype=torch.uint8, device=device) if self.ws_bytes else None
 
 

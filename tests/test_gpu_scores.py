@@ -102,6 +102,19 @@ def test_ties_and_near_ties(score, tokens):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_group_sums_of_large_choices_of_opposite_sign(score):
+    """Each of a group's two choices is large and their sum is not: what fp32
+    loses of them is more than the sums differ by."""
+    T, groups = 64, 16
+    step = torch.stack([torch.randperm(groups, generator=torch.Generator().manual_seed(t)) for t in range(T)])
+    l = torch.zeros(T, groups, 2)
+    l[:, :, 0] = step * 2.0 ** (-15 if score == "sigmoid" else -11)     # sums 8e-6 apart, choices of 100 to 7.6e-6
+    size = 100.0 + torch.arange(groups) / 7
+    bias = torch.stack([size, -size], 1).flatten()
+    _check(l.view(T, -1), 4, score, bias, groups, 3, "top2", True, 1.0)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("tokens", [6, 30])
 def test_masked_and_infinite_logits(score, tokens):
     """Experts out of the choice (-infinity, NaN), rows with nothing left,
