@@ -1,5 +1,14 @@
 // Low-rank adapters of many requests beside a shared projection:
 // out[r] = y[r] + scale_i B_i (A_i x[r]), i = ids[r].
+//
+// Two kernels, z = A_i x with K in parts and out = y + scale_i B_i z, both by
+// MFMA over tiles of 16 rows: the operations are few (4096 rows of 4096, rank
+// 64: 4.3 GFLOP), the bytes of x, y and out bound long batches, latency short
+// ones.  Measured: 4096 rows of 4096 in bf16 in runs of eight adapters 25.4 us
+// for rank 16 and 36.4 us for rank 64 (101 and 109 MB: 20 and 21 us at the rate
+// of a large copy), one row of 4096 -> 14336 with rank 32 7.7 us, 64 rows of 32
+// adapters of rank 16 13.6 us.  What is left in long batches is A_i and B_i
+// from L2 through LDS for every 16 (32) rows.
 #include "check.hpp"
 #include "vec8.hpp"
 
@@ -170,9 +179,9 @@ __device__ __forceinline__ void put_terms(ZTerms<TM, NT, TERMS> &s, int r, const
 }
 
 // Both kernels: an MFMA operand's lanes lie in 16 different rows, and such a
-// load keeps the address path busy four times as long as one along the rows
-// (64 clocks for 1 KB against 16), which bounds a stream of them.  So every
-// operand comes along its rows, eight lanes to 128 bytes, and changes places in
+// load keeps the address path busy up to four times as long as one along the
+// rows (1 KB from the caches: 77 clocks against 29), which bounds a stream of
+// them.  So every operand comes along its rows, eight lanes to 128 bytes, and changes places in
 // a part of LDS that belongs to its wave alone: no barriers, since the LDS
 // operations of a wave stay in order.
 constexpr int kAdapterWaves = 4, kAdapterThreads = kAdapterWaves * kWave;
@@ -499,10 +508,14 @@ adapters_up_kernel(AdapterArgs a) {
   }
 }
 
-constexpr int kLongBatch = 2048;
-
 // How a call is cut: rows per workgroup of the first kernel (16 tm), ranks it
-// forms at a time (16 nt), parts of K.
+// forms at a time (16 nt), parts of K.  Thirty-two rows read A_i half as often
+// (4096 rows of 4096: 25.4 against 26.3 us for rank 16, 37.4 against 38.8 for
+// 64) but leave few workgroups of short batches (256 rows: 17.1 us against
+// 13.7).  K is cut into as many parts as give two workgroups a CU, each wave at
+// least one chunk (one workgroup a CU: 4096 rows of rank 64 70 us where these
+// took 59, four: 59).
+constexpr int kLongBatch = 2048;
 struct AdapterPlan {
   int tm, nt, groups, splits, per;
 };
@@ -520,20 +533,22 @@ static AdapterPlan adapter_plan(int T, int R, int K) {
 }
 
 // Workgroups that share a tile's adapters: as many as a tile can use, as long
-// as the grid stays within what the card holds at a time (most of them have no
-// work where rows of one adapter stand together, as they mostly do in long
-// batches: from kLongBatch rows on there are none).
-static int adapter_slots(const AdapterArgs &a, int rows) {
-  if (a.T >= kLongBatch) return 1;
+// as the grid stays within the workgroups that the card holds at a time, 256
+// times what the kernel's registers leave a CU: most of them have no work where
+// rows of one adapter stand together, and beyond that they are in the way of
+// those that have (1024 rows of rank 64 in runs of one adapter: 18.8 us with one
+// a tile, 24 with two; 64 rows of 32 adapters of rank 16 in any order: 13.6 us
+// with 16, 27.7 with one).
+static int adapter_slots(const AdapterArgs &a, int rows, int most) {
   const int64_t wgs = (int64_t)a.tiles * a.parts;
-  return (int)std::max((int64_t)1, std::min((int64_t)std::min(std::min(a.n, a.T), rows), 1024 / wgs));
+  return (int)std::max((int64_t)1, std::min((int64_t)std::min(std::min(a.n, a.T), rows), most / wgs));
 }
 
 template <int TY, int TM, int NT, int D>
 static void launch_down(AdapterArgs a, const AdapterPlan &p, hipStream_t s) {
   a.tiles = (a.T + TM * kRows - 1) / (TM * kRows);
   a.parts = p.splits * p.groups;
-  a.slots = adapter_slots(a, TM * kRows);
+  a.slots = adapter_slots(a, TM * kRows, NT == 1 ? 1024 : NT == 2 ? 768 : 512);
   hipLaunchKernelGGL((adapters_down_kernel<TY, TM, NT, D>), place_grid(a), dim3(kAdapterThreads), 0, s, a);
 }
 
@@ -542,11 +557,11 @@ static void launch_up(AdapterArgs a, hipStream_t s) {
   a.tiles = (a.T + kRows - 1) / kRows;
   const int turn = kAdapterWaves * 64, turns = (a.N + turn - 1) / turn;
   // one round of what the card holds at a time, but no more than eight turns a
-  // workgroup (8192 rows of 14336, rank 32: 157 us against 218 in one round)
+  // workgroup (8192 rows of 14336, rank 32: 163 us against 218 in one round)
   const int parts = std::max((turns + 7) / 8, std::min(turns, (RM == 16 ? 1024 : 768) / a.tiles));
   a.width = (turns + parts - 1) / parts * turn;
   a.parts = (a.N + a.width - 1) / a.width;
-  a.slots = adapter_slots(a, kRows);
+  a.slots = adapter_slots(a, kRows, RM == 16 ? 1024 : 768);
   hipLaunchKernelGGL((adapters_up_kernel<TY, TO, RM>), place_grid(a), dim3(kAdapterThreads), 0, s, a);
 }
 

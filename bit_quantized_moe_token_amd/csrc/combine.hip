@@ -1,5 +1,8 @@
 // The experts' rows back to their tokens, weighted by the gates, and the
-// gradients of rows and gates.
+// gradients of rows and gates.  Both are bound by their bytes: 4096 tokens of
+// six rows of 2048 in bf16 23 us (134 MB, 5.8 TB/s), their gradients 40 us
+// (218 MB, 5.4 TB/s).  Rows are read, and outputs written, once and past the
+// caches (with ordinary loads and stores 25.6 and 46 us).
 #include "check.hpp"
 #include "vec8.hpp"
 #include "wave.hpp"
@@ -22,11 +25,12 @@ struct CombineArgs {
 };
 
 // TR: type of the rows, TO: of base and out.  2^lanes threads along a row,
-// eight columns each.
+// eight columns each; four rows under way at a time (decoding steps and long
+// batches: 3.0 and 25.4 us, one at a time 3.0 and 27.2, eight 3.2 and 24.7).
 template <int TR, int TO>
 __global__ void __launch_bounds__(kCombineThreads)
 combine_kernel(CombineArgs a) {
-  constexpr int SLOTS = 4;   // rows under way at a time
+  constexpr int SLOTS = 4;
   const int t = blockIdx.x * (kCombineThreads >> a.lanes) + (threadIdx.x >> a.lanes);
   const int c = ((blockIdx.y << a.lanes) + (threadIdx.x & ((1 << a.lanes) - 1))) * 8;
   const int n = a.N - c;

@@ -181,7 +181,7 @@ route_count_kernel(const int32_t *__restrict__ ids, int T, int E, int k, int32_t
 // histogram.  Loads in batches of 16 segments, so that a batch waits for
 // memory once; what a thread has loaded last it does not load again (8192
 // tokens, 256 experts: 24 us with one part and a second pass over all, now
-// SCANUS us).
+// 8 us).
 constexpr int kScanParts = 4;
 constexpr int kScanThreads = kMaxE * kScanParts;
 constexpr int kScanBatch = 16;

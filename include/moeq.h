@@ -674,7 +674,9 @@ typedef struct {
  * rows; out[r] = y[r] where ids[r] lies outside [0, n) (a row without an
  * adapter; its x is not read).  Rows of one adapter need not stand together,
  * but are served in fewer passes over its matrices where they do.  A_i x is
- * summed in fp32 and kept to 22 bits, the rest is fp32, rounded once.
+ * summed in fp32; of each row of it 16 bits (22 of fp16 adapters) below its
+ * largest value go on beside a 16-bit y, 24 beside MOEQ_F32; the rest is
+ * fp32, rounded once.
  *   x DEVICE [T, K] of the adapters' dtype; ids DEVICE [T] int32; y, out
  *   DEVICE [T, N] of y_dtype (the adapters' dtype or MOEQ_F32); rows ldx, ldy,
  *   ldo elements apart, aligned to their elements; 0 <= T < 2^22.  out may be
