@@ -179,8 +179,8 @@ __device__ __forceinline__ void put_terms(ZTerms<TM, NT, TERMS> &s, int r, const
 }
 
 // Both kernels: an MFMA operand's lanes lie in 16 different rows, and such a
-// load keeps the address path busy up to four times as long as one along the
-// rows (1 KB from the caches: 77 clocks against 29), which bounds a stream of
+// load keeps the address path busy 2.6 times as long as one along the rows (1 KB
+// from the caches: 77 clocks of 2.4 GHz against 29), which bounds a stream of
 // them.  So every operand comes along its rows, eight lanes to 128 bytes, and changes places in
 // a part of LDS that belongs to its wave alone: no barriers, since the LDS
 // operations of a wave stay in order.
@@ -243,10 +243,7 @@ adapters_down_kernel(AdapterArgs a) {
   int row = 0;
   Turn turn(place);
   Tile<TM> left = tile;
-  // chunks from one that differs from tile to tile: rows are often a power of
-  // two apart, and workgroups in step would read the same few memory channels
-  const int whole = std::min(c0 + chunks, a.K / kChunk) - c0, end = c0 + whole;
-  const int first = c0 + (whole > 0 ? place.tile * 5 % whole : 0);
+  const int whole = std::min(c0 + chunks, a.K / kChunk) - c0;
   for (int cur = left.next(row); cur >= 0; cur = left.next(row)) {
     if (!turn.mine(a)) continue;
     const uint8_t *xp[XI], *ap[AI];
@@ -267,7 +264,7 @@ adapters_down_kernel(AdapterArgs a) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) acc[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
     const auto fetch = [&](int i, u32x4 (&x)[XI], u32x4 (&w)[AI]) {   // the i-th whole chunk
-      const int c = first + i < end ? first + i : first + i - whole;
+      const int c = c0 + i;
 #pragma unroll
       for (int q = 0; q < XI; ++q) x[q] = load8(xp[q] + c * (kChunk * 2));
 #pragma unroll
@@ -305,7 +302,7 @@ adapters_down_kernel(AdapterArgs a) {
       }
     }
     if (whole < chunks && whole % NW == wave) {   // the last columns, by the wave whose turn it is
-      const int col = end * kChunk + pc * 8;
+      const int col = (c0 + whole) * kChunk + pc * 8;
 #pragma unroll
       for (int q = 0; q < XI; ++q) x[0][q] = load8(xp[q] - pc * 16, col, a.K, a.K);
 #pragma unroll

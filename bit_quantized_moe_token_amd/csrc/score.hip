@@ -4,7 +4,7 @@
 // Choices are defined in 64 bits, but few tokens have two experts that 32 bits
 // cannot tell apart.  A wave therefore picks its token's experts by choices in
 // fp32 and watches the distance of each from the next; where it is within what
-// fp32 may be off (about one token in a hundred), the same code picks again in
+// fp32 may be off (0.2 to 1.2 tokens in a hundred), the same code picks again in
 // 64 bits.  (Choices without a bias are the logits themselves, and exact.)
 //
 // Up to 16 tokens one launch does all (16 tokens of 128 experts: 7 us); more are

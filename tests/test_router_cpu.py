@@ -4,10 +4,15 @@ closed forms, differences and brute force."""
 
 import ctypes
 import itertools
+import os
+import re
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
 
+from bit_quantized_moe_token_amd import build
 from oracle import products, requests, scores
 
 P = 4096
@@ -221,3 +226,17 @@ def test_adapters_as_dense_matrices():
     assert np.allclose(out[[1, 4]], y[[1, 4]])
     assert np.allclose(out[0], y[0] + 2 * (b[2] @ a[2]) @ x[0])
     assert np.allclose(out[2], y[2] + 0.5 * (b[0][:, :2] @ a[0][:2]) @ x[2])
+
+
+@pytest.mark.skipif(not os.path.exists(build.HIPCC) and not shutil.which(build.HIPCC), reason="no compiler")
+@pytest.mark.parametrize("name,kernels", [("score", 9), ("combine", 9), ("adapters", 20)])
+def test_kernels_use_no_scratch(name, kernels):
+    """Choices, rows and MFMA operands are held in registers: the compiler
+    reports no scratch for any kernel."""
+    src = os.path.join(build.CSRC, name + ".hip")
+    r = subprocess.run([build.HIPCC, *build.CFLAGS, "-Rpass-analysis=kernel-resource-usage", "-S", "--cuda-device-only", src,
+                        "-o", os.devnull], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
+    found = re.findall(r"Function Name: (\S+).*?ScratchSize \[bytes/lane\]: (\d+)", r.stderr, re.S)
+    assert len(found) >= kernels
+    assert not [n for n, size in found if int(size)]
