@@ -11,6 +11,7 @@
 // from L2 through LDS for every 16 (32) rows.
 #include "check.hpp"
 #include "vec8.hpp"
+#include "wave.hpp"
 
 namespace moeq {
 
@@ -185,10 +186,6 @@ __device__ __forceinline__ void put_terms(ZTerms<TM, NT, TERMS> &s, int r, const
 // a part of LDS that belongs to its wave alone: no barriers, since the LDS
 // operations of a wave stay in order.
 constexpr int kAdapterWaves = 4, kAdapterThreads = kAdapterWaves * kWave;
-
-// Between LDS accesses of one wave that may not change places (the hardware
-// keeps their order; this keeps the compiler to it).
-__device__ __forceinline__ void lds_order() { asm volatile("" ::: "memory"); }
 
 // [rows][64] 16-bit values, 128 bytes a row, in pieces of 16 bytes: piece p of
 // row r stands at p ^ (r % 8), so that neither side has bank conflicts.

@@ -594,41 +594,59 @@ score_wide_kernel(ScoreArgs a, int32_t *__restrict__ ids, float *__restrict__ ga
 }
 
 // Gradient of the logits of four tokens by a workgroup of four waves.  What a
-// chosen expert gets is formed by one thread per (token, slot) in 64 bits, from
-// the chosen logits alone, and put into the token's row in LDS; the rows leave
-// along their length.  Only a softmax over all E without renorm reads (and
-// gives a gradient to) the other logits: s_e (v_e - sum_i v_i s_i) in fp32.
-// (With renorm that sum is zero.)  16384 tokens of 256 experts: 11.4 us with
-// renorm (write-bound: 17 MB out, 8 MB of lines of chosen logits in), 16.7 us
-// over all E (instructions: an exponential and the row's sums); 16 tokens a
-// workgroup 11.0 and 24 us.
+// chosen expert gets is formed by one thread per (token, slot) in 64 bits and
+// put into the token's row in LDS; the rows leave along their length.  Only a
+// softmax over all E without renorm reads (and gives a gradient to) the other
+// logits.
+//
+// Where one expert has nearly all the weight, v_e - sum_i v_i s_i is what is
+// left of two nearly equal numbers.  What the experts bring is therefore taken
+// relative to c, what the one of the largest weight brings (0 if that is not a
+// chosen one), so that no term is larger than the differences that count:
+//   renorm:  d_j = scale (x_j - sum_i w_i x_i / S) w_j / S,  x_j = dg_j - c, S = sum_i w_i
+//   over all E (x_e: sum of dg_j over e's slots, less c; S: sum of all weights, R: of those not chosen):
+//            d_l_e = scale (x_e - (sum_i w_i x_i - R c) / S) w_e / S
+// with R summed by itself: an entry is off by what its terms are, however small
+// it is beside them.  The others' entries are products in fp32.
+//
+// 16384 tokens of 256 experts, top-8: 10.6 us (sigmoid 11.1) with renorm for 17
+// MB out and 8 MB of lines of chosen logits in, 16.5 us over all E (34 MB and an
+// exponential per expert).  That is 2.0 to 2.4 TB/s: bound by the latency of
+// the phases between four barriers, in which a token's k slots keep few lanes
+// busy, not by bytes.
 constexpr int kGradTokens = 4;
 struct GradLds {
   static constexpr int NT = kGradTokens;
   int id[NT * kPickMost];
-  float l[NT * kPickMost], dg[NT * kPickMost], add[NT * kPickMost], m[NT], down[NT], inv[NT];
-  double w[NT * kPickMost], total[NT];
+  float l[NT * kPickMost], dg[NT * kPickMost], add[NT * kPickMost], m[NT], rest[NT], down[NT], inv[NT];
+  double w[NT * kPickMost], wx[NT * kPickMost];
   __attribute__((aligned(16))) float d[NT][kMaxE];
 };
+static_assert(kGradTokens * kPickMost <= kScoreThreads, "a thread per slot");
 
 __global__ void __launch_bounds__(kScoreThreads)
 score_grad_kernel(ScoreArgs a, const int32_t *__restrict__ ids, const float *__restrict__ d_gates, void *out, int64_t ldd) {
   constexpr int NT = kGradTokens, TW = NT / (kScoreThreads / kWave);
   __shared__ GradLds s;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int t0 = blockIdx.x * NT, k = a.k, E = a.E, items = std::min(NT, a.T - t0) * k;
-  const bool dense = !a.sigmoid && !a.renorm;
-  for (int i = tid; i < items; i += kScoreThreads) {
-    const int64_t p = (int64_t)t0 * k + i;
-    const int id = ids[p];
-    const bool ok = (uint32_t)id < (uint32_t)E;
-    s.id[i] = ok ? id : -1;
-    s.dg[i] = d_gates[p];
-    s.l[i] = ok ? logit(logit_row(a, t0 + i / k), a.dtype, id) : -__builtin_inff();
+  const int t0 = blockIdx.x * NT, k = a.k, E = a.E;
+  const bool dense = !a.sigmoid && !a.renorm, slot = tid < std::min(NT, a.T - t0) * k;
+  const int st = tid / k, s0 = st * k;   // this thread's slot: its token, and that token's first
+  int id = -1;
+  float l = -__builtin_inff(), dg = 0.f;
+  if (slot) {
+    const int64_t p = (int64_t)t0 * k + tid;
+    id = ids[p];
+    dg = d_gates[p];
+    if ((uint32_t)id < (uint32_t)E) l = logit(logit_row(a, t0 + st), a.dtype, id);
+    else id = -1;
+    s.id[tid] = id;
+    s.dg[tid] = dg;
+    s.l[tid] = l;
   }
 #pragma unroll
   for (int i = 0; i < NT * kMaxE / 4 / kScoreThreads; ++i) *(f32x4 *)&s.d[0][(i * kScoreThreads + tid) * 4] = f32x4{0.f, 0.f, 0.f, 0.f};
-  float u[TW][4];   // dense: exponentials of experts 4 lane ..
+  float u[TW][4];   // dense: exponentials of experts 4 lane .., then -1 for chosen ones
   if (dense) {
 #pragma unroll
     for (int i = 0; i < TW; ++i) {
@@ -636,69 +654,101 @@ score_grad_kernel(ScoreArgs a, const int32_t *__restrict__ ids, const float *__r
       if (t0 + t >= a.T) continue;
       load_run<4>(a, t0 + t, u[i]);
       const float m = of_key(all_max(key_of(__builtin_fmaxf(__builtin_fmaxf(u[i][0], u[i][1]), __builtin_fmaxf(u[i][2], u[i][3])))));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float v = u[i][q];
+        u[i][q] = v == -__builtin_inff() ? 0.f : v == m ? 1.f : expf(v - m);
+      }
+      if (lane == 0) s.m[t] = m;
+    }
+  }
+  __syncthreads();
+  // w: a slot's weight, of a softmax up to a factor; dense: of an expert's
+  // first slot, 0 for its others
+  bool first = id >= 0;
+  double w = 0.0, x = dg, c = 0.0;
+  if (slot && (a.renorm || dense)) {
+    float top = s.l[s0];
+    int at = s0;
+    for (int j = s0 + 1; j < s0 + k; ++j)
+      if (s.l[j] > top) {
+        top = s.l[j];
+        at = j;
+      }
+    if (dense) {
+      const int lead = top == s.m[st] ? s.id[at] : -2;
+      double mine = 0.0;
+      for (int j = s0; j < s0 + k; ++j) {
+        const int o = s.id[j];
+        const double b = s.dg[j];
+        mine += o == id ? b : 0.0;
+        c += o == lead ? b : 0.0;
+        first &= o != id || j >= tid;
+      }
+      x = mine - c;
+      if (first) w = exp_below(l, s.m[st]);
+      if (id >= 0) s.d[st][id] = 1.f;
+    } else {
+      x = (double)dg - (double)s.dg[at];
+      if (id >= 0) w = a.sigmoid ? sigmoid64(l) : exp_below(l, top);
+    }
+    s.w[tid] = w;
+    s.wx[tid] = w > 0.0 ? w * x : 0.0;
+  } else if (first) {
+    w = sigmoid64(l);
+  }
+  if (dense) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < TW; ++i) {
+      const int t = wave * TW + i;
+      if (t0 + t >= a.T) continue;
+      const f32x4 chosen = *(const f32x4 *)&s.d[t][lane * 4];
       float sum = 0.f;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const float l = u[i][q];
-        u[i][q] = l == -__builtin_inff() ? 0.f : l == m ? 1.f : expf(l - m);
-        sum += u[i][q];
+        if (chosen[q] != 0.f) u[i][q] = -1.f;
+        else sum += u[i][q];
       }
       sum = all_sum(sum);
-      if (lane == 0) {
-        s.m[t] = m;
-        s.total[t] = sum;
-        s.inv[t] = sum > 0.f ? 1.f / sum : 0.f;
-      }
+      if (lane == 0) s.rest[t] = sum;
     }
   }
-  __syncthreads();
-  for (int i = tid; i < items; i += kScoreThreads) {
-    const int t = i / k;
-    double w = 0.0;
-    if (s.id[i] >= 0) {
-      if (a.sigmoid) w = sigmoid64(s.l[i]);
-      else if (dense) w = s.total[t] > 0.0 ? exp_below(s.l[i], s.m[t]) / s.total[t] : 0.0;
-      else {
-        float top = s.l[t * k];
-        for (int j = 1; j < k; ++j) top = __builtin_fmaxf(top, s.l[t * k + j]);
-        w = exp_below(s.l[i], top);
-      }
-    }
-    s.w[i] = w;
-  }
-  __syncthreads();
-  for (int i = tid; i < items; i += kScoreThreads) {
-    const int t = i / k;
-    double total = 0.0, mean = 0.0, v = 0.0;   // mean: sum_i dg_i s_i
+  if (a.renorm || dense) __syncthreads();
+  if (slot) {
+    double d = w > 0.0 ? x * w : 0.0;
     if (a.renorm || dense) {
-      for (int j = 0; j < k; ++j) {
-        const double w = s.w[t * k + j];
-        total += w;
-        if (w > 0.0) mean += (double)s.dg[t * k + j] * w;
+      const double rest = dense ? (double)s.rest[st] : 0.0;
+      double chosen = 0.0, mean = 0.0;
+      for (int j = s0; j < s0 + k; ++j) {
+        chosen += s.w[j];
+        mean += s.wx[j];
       }
+      const double total = chosen + rest;
+      if (dense && tid == s0) {
+        s.down[st] = total > 0.0 ? (float)((double)a.scale * ((mean + c * chosen) / total)) : 0.f;
+        s.inv[st] = total > 0.0 ? (float)(1.0 / total) : 0.f;
+      }
+      d = w > 0.0 ? (x - (mean - rest * c) / total) * (w / total) : 0.0;
     }
-    if (dense) {
-      v = s.id[i] >= 0 ? s.dg[i] : 0.0;
-      if (i == t * k) s.down[t] = (float)((double)a.scale * mean);
-    } else if (s.w[i] > 0.0) {
-      v = a.renorm ? ((double)s.dg[i] - mean / total) * (s.w[i] / total) : (double)s.dg[i] * s.w[i];
-      if (a.sigmoid) v *= sigmoid64(-s.l[i]);
-    }
-    s.add[i] = (float)((double)a.scale * v);
+    if (a.sigmoid && w > 0.0) d *= sigmoid64(-l);
+    const float v = (float)((double)a.scale * d);
+    if (!dense) s.add[tid] = v;
+    else if (first) s.d[st][id] = v;
   }
   __syncthreads();
-  for (int i = tid; i < items; i += kScoreThreads) {   // an expert's first slot adds up all that are its
-    const int t = i / k, id = s.id[i];
-    float sum = 0.f;
-    int before = 0;
-    for (int j = 0; j < k; ++j) {
-      if (s.id[t * k + j] != id) continue;
-      sum += s.add[t * k + j];
-      before += t * k + j < i;
+  if (!dense) {
+    if (id >= 0) {   // an expert's first slot adds up all that are its
+      float sum = 0.f;
+      for (int j = s0; j < s0 + k; ++j) {
+        if (s.id[j] != id) continue;
+        sum += s.add[j];
+        first &= j >= tid;
+      }
+      if (first) s.d[st][id] = sum;
     }
-    if (id >= 0 && !before) s.d[t][id] = sum;
+    __syncthreads();
   }
-  __syncthreads();
 #pragma unroll
   for (int i = 0; i < TW; ++i) {
     const int t = wave * TW + i, n = E - lane * 4;
@@ -706,7 +756,8 @@ score_grad_kernel(ScoreArgs a, const int32_t *__restrict__ ids, const float *__r
     f32x4 d = *(const f32x4 *)&s.d[t][lane * 4];
     if (dense) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) d[q] = u[i][q] > 0.f ? u[i][q] * s.inv[t] * (d[q] - s.down[t]) : 0.f;
+      for (int q = 0; q < 4; ++q)
+        if (u[i][q] >= 0.f) d[q] = u[i][q] > 0.f ? u[i][q] * s.inv[t] * (0.f - s.down[t]) : 0.f;
     }
     const int64_t at = (int64_t)(t0 + t) * ldd + lane * 4;
     if (a.dtype == MOEQ_F32) {
@@ -727,107 +778,125 @@ score_grad_kernel(ScoreArgs a, const int32_t *__restrict__ ids, const float *__r
   }
 }
 
-// More than kPickMost slots: a wave per token, slot j in lane j % 64.
+// More than kPickMost slots: a wave per token, expert e in lane e % 64 (4096
+// tokens of 256 experts, 100 slots: 9.2 us with renorm, 9.8 us over all E).
 template <int TY>
 __global__ void __launch_bounds__(kScoreThreads)
 score_grad_wide_kernel(ScoreArgs a, const int32_t *__restrict__ ids, const float *__restrict__ d_gates, void *out,
                   int64_t ldd) {
-  const int t = blockIdx.x * (kScoreThreads / kWave) + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (t >= a.T) return;
+  __shared__ int s_n[kScoreThreads / kWave][kMaxE];
+  __shared__ float s_v[kScoreThreads / kWave][kMaxE];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t = blockIdx.x * (kScoreThreads / kWave) + wave;
+  if (t >= a.T) return;   // (a wave works in its own part of LDS)
   const int E = a.E, k = a.k;
+  const bool dense = !a.sigmoid && !a.renorm;
   float l[kSlots];
   load_row(a, t, l);
   int id[kSlots];
-  float sel[kSlots];
-  double dg[kSlots], w[kSlots], rest[kSlots];
-  float top = -__builtin_inff();
+  float dg[kSlots];
 #pragma unroll
   for (int s = 0; s < kSlots; ++s) {
     const int j = lane + s * kWave;
-    id[s] = -1;
-    dg[s] = 0.0;
-    if (j < k) {
-      id[s] = ids[(int64_t)t * k + j];
-      dg[s] = d_gates[(int64_t)t * k + j];
-    }
-    if (id[s] < 0 || id[s] >= E) id[s] = -1;
-    sel[s] = -__builtin_inff();
-#pragma unroll
-    for (int q = 0; q < kSlots; ++q) {
-      const float v = __shfl(l[q], id[s] & 63, kWave);
-      if (id[s] >= 0 && (id[s] >> 6) == q) sel[s] = v;
-    }
-    top = __builtin_fmaxf(top, sel[s]);
+    id[s] = j < k ? ids[(int64_t)t * k + j] : -1;
+    dg[s] = j < k ? d_gates[(int64_t)t * k + j] : 0.f;
+    if (id[s] >= E) id[s] = -1;
   }
-  float m = l[0];
+  // an expert's slots, and the sum of what they bring: through LDS, and where
+  // one has several, in slot order
+  int n[kSlots];
+  double v[kSlots];
+  bool several = false;
 #pragma unroll
-  for (int s = 1; s < kSlots; ++s) m = __builtin_fmaxf(m, l[s]);
+  for (int s = 0; s < kSlots; ++s) s_n[wave][lane + s * kWave] = 0;
+  lds_order();
+#pragma unroll
+  for (int s = 0; s < kSlots; ++s)
+    if (id[s] >= 0) {
+      atomicAdd(&s_n[wave][id[s]], 1);
+      s_v[wave][id[s]] = dg[s];
+    }
+  lds_order();
+#pragma unroll
+  for (int s = 0; s < kSlots; ++s) {
+    n[s] = s_n[wave][lane + s * kWave];
+    v[s] = n[s] ? s_v[wave][lane + s * kWave] : 0.f;
+    several |= n[s] > 1;
+  }
+  if (__ballot(several)) {
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s) v[s] = 0.0;
+#pragma unroll
+    for (int b = 0; b < kSlots; ++b)
+      for (int j = b * kWave; j < std::min(k, (b + 1) * kWave); ++j) {
+        const int e = __builtin_amdgcn_readlane(id[b], j & 63);
+        const float g = lane_value(dg[b], j & 63);
+#pragma unroll
+        for (int s = 0; s < kSlots; ++s)
+          if (e == lane + s * kWave) v[s] += g;
+      }
+  }
+  float m = l[0], top = -__builtin_inff();
+#pragma unroll
+  for (int s = 0; s < kSlots; ++s) {
+    m = __builtin_fmaxf(m, l[s]);
+    if (n[s]) top = __builtin_fmaxf(top, l[s]);
+  }
   m = wave_max(m);
   top = wave_max(top);
-  // w: the score, of a softmax up to a factor that cancels or follows; rest: 1 - s of a sigmoid
-  double total = 0.0, sum = 0.0;
-  float u[kSlots];
-  const bool dense = !a.sigmoid && !a.renorm;
+  // c: what a slot of the expert of the largest weight brings (dense: all its
+  // slots, 0 if it is not chosen)
+  double c = 0.0;
+  if (a.renorm || (dense && top == m)) {
+    bool found = false;
 #pragma unroll
-  for (int s = 0; s < kSlots; ++s) {
-    w[s] = rest[s] = 0.0;
-    u[s] = 0.f;
-    if (id[s] >= 0) {
-      if (a.sigmoid) {
-        w[s] = sigmoid64(sel[s]);
-        rest[s] = sigmoid64(-sel[s]);
-      } else {
-        w[s] = exp_below(sel[s], a.renorm ? top : m);
+    for (int s = 0; s < kSlots; ++s) {
+      const uint64_t is = __ballot(n[s] && l[s] == top);
+      if (!found && is) {
+        const int from = __builtin_ctzll(is);
+        c = lane_value(v[s], from) / (dense ? 1 : __builtin_amdgcn_readlane(n[s], from));
+        found = true;
       }
-      total += w[s];
     }
-    if (dense) {
+  }
+  // w: a chosen expert's score, of a softmax up to a factor; u: the others' exponentials
+  double w[kSlots], chosen = 0.0, rest = 0.0, mean = 0.0;
+  float u[kSlots];
+#pragma unroll
+  for (int s = 0; s < kSlots; ++s) {
+    w[s] = 0.0;
+    u[s] = 0.f;
+    if (n[s]) {
+      w[s] = a.sigmoid ? sigmoid64(l[s]) : exp_below(l[s], a.renorm ? top : m);
+      chosen += dense ? w[s] : n[s] * w[s];
+      v[s] -= (dense ? 1 : n[s]) * c;
+      if (w[s] > 0.0) mean += v[s] * w[s];
+    } else if (dense) {
       u[s] = l[s] == -__builtin_inff() ? 0.f : l[s] == m ? 1.f : expf(l[s] - m);
-      sum += u[s];
+      rest += u[s];
     }
   }
-  double mean = 0.0;   // sum_i dg_i s_i
-  if (a.renorm) total = wave_sum(total);
-  if (dense) sum = wave_sum(sum);
-#pragma unroll
-  for (int s = 0; s < kSlots; ++s) {
-    if (a.renorm) w[s] = total > 0.0 ? w[s] / total : 0.0;
-    else if (dense) w[s] = sum > 0.0 ? w[s] / sum : 0.0;
-    if (w[s] > 0.0) mean += dg[s] * w[s];
-  }
+  rest = wave_sum(rest);
+  chosen = wave_sum(chosen);
   mean = wave_sum(mean);
-  // what slot j adds to its expert: its share of the logit's gradient, or dg
-  // itself where the softmax over all experts takes it further
-  float add[kSlots];
-#pragma unroll
-  for (int s = 0; s < kSlots; ++s) {
-    double v = dense ? dg[s] : w[s] > 0.0 ? (dg[s] - (a.renorm ? mean : 0.0)) * w[s] : 0.0;
-    if (a.sigmoid) v *= rest[s];
-    add[s] = (float)((double)a.scale * v);
-  }
-  float d[kSlots];
-#pragma unroll
-  for (int s = 0; s < kSlots; ++s) d[s] = 0.f;
-  for (int j = 0; j < k; ++j) {
-    float v = 0.f;
-    int e = -1;
-#pragma unroll
-    for (int s = 0; s < kSlots; ++s)
-      if ((j >> 6) == s) { v = __shfl(add[s], j & 63, kWave); e = __shfl(id[s], j & 63, kWave); }
-#pragma unroll
-    for (int s = 0; s < kSlots; ++s)
-      if (e == lane + s * kWave) d[s] += v;
-  }
+  const double total = chosen + rest;
   uint8_t *row = (uint8_t *)out + t * ldd * Val<TY>::size;
-  const float inv = sum > 0.0 ? (float)(1.0 / sum) : 0.f, down = (float)((double)a.scale * mean);
+  const float inv = total > 0.0 ? (float)(1.0 / total) : 0.f, down = total > 0.0 ? (float)((double)a.scale * ((mean + c * chosen) / total)) : 0.f;
 #pragma unroll
   for (int s = 0; s < kSlots; ++s) {
     const int e = lane + s * kWave;
     if (e >= E) continue;
-    const float v = !dense ? d[s] : u[s] > 0.f ? u[s] * inv * (d[s] - down) : 0.f;
-    if constexpr (TY == MOEQ_F32) ((uint32_t *)row)[e] = Val<TY>::put(v);
-    else ((uint16_t *)row)[e] = (uint16_t)Val<TY>::put(v);
+    float g = 0.f;
+    if (w[s] > 0.0) {
+      double x = v[s] * w[s];
+      if (a.renorm || dense) x = (v[s] - (dense ? 1 : n[s]) * (mean - rest * c) / total) * (w[s] / total);
+      if (a.sigmoid) x *= sigmoid64(-l[s]);
+      g = (float)((double)a.scale * x);
+    } else if (u[s] > 0.f) {
+      g = u[s] * inv * (0.f - down);
+    }
+    if constexpr (TY == MOEQ_F32) ((uint32_t *)row)[e] = Val<TY>::put(g);
+    else ((uint16_t *)row)[e] = (uint16_t)Val<TY>::put(g);
   }
 }
 

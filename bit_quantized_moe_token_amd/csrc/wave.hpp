@@ -1,4 +1,5 @@
-// Exchanges and sums over the lanes of a wave by DPP.
+// Exchanges and sums over the lanes of a wave by DPP, and the order of its LDS
+// accesses.
 #pragma once
 #include "common.hpp"
 
@@ -47,5 +48,9 @@ __device__ __forceinline__ V all_sum(V v) {
   v += dpp_into<0x143, 0xc>(v, (V)0);
   return lane_value(v, 63);
 }
+
+// Between LDS accesses of one wave that may not change places (the hardware
+// keeps their order; this keeps the compiler to it).
+__device__ __forceinline__ void lds_order() { asm volatile("" ::: "memory"); }
 
 }  // namespace moeq

@@ -422,8 +422,11 @@ moeq_status moeq_route_scored(const moeq_scoring *d, const void *logits, int64_t
  *   v_j = scale * dg_j, with renorm scale * (dg_j - sum_i dg_i s_i / S) / S, S = sum_i s_i
  *   softmax:  d_l_e = s_e * (sum_{j: e_j = e} v_j - sum_i v_i s_i)
  *   sigmoid:  d_l_e = s_e * (1 - s_e) * sum_{j: e_j = e} v_j
- * (fp32, rounded once to dtype; the chosen experts' scores in 64 bits).  A
- * logit of -infinity or NaN gets 0; an id outside [0, E) is no expert.
+ * rounded once to dtype.  A chosen expert's entry is formed in 64 bits from
+ * differences of the v_j (so that it keeps its digits where one expert has
+ * nearly all the weight), but for the exponentials of the experts that were not
+ * chosen and their sum: these, and those experts' entries, are fp32.  A logit of
+ * -infinity or NaN gets 0; an id outside [0, E) is no expert.
  *   logits, d_logits DEVICE [T, E] of dtype, rows ld and ldd elements apart;
  *   ids DEVICE [T, k] int32; d_gates DEVICE [T, k] fp32.  d_logits may be
  *   logits (in place); no other operands may overlap.

@@ -99,3 +99,30 @@ def route_grad(logits, ids, d_gates, score="softmax", renorm=True, scale=1.0):
         np.add.at(out[t], e, scale * v)
         np.add.at(mag[t], e, abs(scale) * m)
     return out, mag
+
+
+def route_grad_apart(logits, ids, d_gates, score="softmax", renorm=True, scale=1.0):
+    """route_grad for distinct ids in [0, E) and finite logits, written so that
+    nothing cancels where one expert has nearly all the weight: the differences
+    of what experts bring are weighted, not the difference of the weighted taken.
+    (d_logits [T, E], and the sum of the magnitudes of each entry's weighted
+    differences)."""
+    logits = np.asarray(logits, dtype=np.float64)
+    out, mag = np.zeros(logits.shape), np.zeros(logits.shape)
+    for t, l in enumerate(logits):
+        e, dg = np.asarray(ids[t]), scale * np.asarray(d_gates[t], dtype=np.float64)
+        if score == "softmax" and not renorm:
+            s, v = scores(l, score), np.zeros(len(l))
+            v[e] = dg
+            apart = v[:, None] - v[None, :]
+            out[t], mag[t] = s * (apart @ s), s * (abs(apart) @ s)
+            continue
+        if renorm:
+            w = gates(l, e, score, True, 1.0)
+            apart = dg[:, None] - dg[None, :]
+            v, m = w * (apart @ w), w * (abs(apart) @ w)
+        else:
+            v, m = dg * scores(l, score)[e], abs(dg) * scores(l, score)[e]
+        rest = scores(-l, "sigmoid")[e] if score == "sigmoid" else 1.0
+        out[t][e], mag[t][e] = v * rest, m * rest
+    return out, mag

@@ -290,6 +290,56 @@ def test_gradient_against_differences():
             step = torch.zeros(E, device="cuda")
             step[e] = h
             num = (f(l + step) - f(l - step)) / (2 * h)
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_gradient_of_confident_rows(dtype, score, renorm):
+    """One expert leads by far, chosen or not, or all gates' gradients are
+    equal: every entry is small beside its terms, and is right beside itself.
+    Weighted differences in 64 bits; the exponentials of experts outside the
+    choice are fp32: 2 steps (2^-22) and the rounding of an argument of up to
+    `span` (span * 2^-24), in sums of at most 4 + 6 additions, a quotient and
+    two products (20 * 2^-24 in all)."""
+    from bit_quantized_moe_token_amd import moeq
+    tiny = {F32: 2.0 ** -126, BF16: 2.0 ** -126}[dtype]
+    for E, k in ((64, 1), (64, 6), (9, 9), (256, 8), (100, 64), (100, 70), (256, 256)):
+        leads = torch.tensor([0.0, 8.0, 12.0, 16.0, 20.0, 30.0, 60.0] * 2)
+        T = len(leads)
+        l = torch.randn((T, E), generator=torch.Generator().manual_seed(E + k))
+        l[:, 3] = leads + l.amax(1)
+        l = l.to(dtype)
+        ids = _ids(T, E, k)
+        for t in range(T):
+            if t < T - 2 and 3 not in ids[t]:
+                ids[t, k // 2] = 3                     # (the last two as they come)
+        for dg in (_dg(T, k), torch.ones(T, k)):
+            got = _np(moeq.route_scored_grad(l.cuda(), ids.int().cuda(), dg.cuda(), score=score, renorm=renorm, scale=2.5))
+            ref, mag = scores.route_grad_apart(_np(l), ids.numpy(), _np(dg), score, renorm, 2.5)
+            span = (_np(l).max(1) - _np(l).min(1))[:, None]
+            tol = torch.finfo(dtype).eps / 2 * 1.01 * np.abs(ref) + (20 + span) * 2.0 ** -24 * mag + tiny
+            bad = np.abs(got - ref) > tol
+            assert not bad.any(), (E, k, int(bad.sum()), float((np.abs(got - ref) / tol).max()))
+            if score == "softmax":                     # a row's entries add up to nothing
+                assert (np.abs(got.sum(1)) <= tol.sum(1)).all()
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gradient_of_repeated_experts_in_many_slots(score, renorm):
+    """More than 64 slots, some of one expert, some of none; the best expert
+    among the repeated ones."""
+    T, E, k = 9, 130, 100
+    l, ids = _logits(T, E), _ids(T, E, k)
+    ids[1, 50:] = ids[1, :50]
+    ids[2, ::3] = int(ids[2, 0])
+    ids[3, 10], ids[3, 70], ids[3, 99] = -1, 130, 2 ** 30
+    ids[4, :] = 7
+    for t in (1, 2, 4):
+        l[t, ids[t, 0]] = l[t].max() + 2
+    _check_grad(l, ids, _dg(T, k), score, renorm, 1.5)
+    _check_grad(l, ids, torch.ones(T, k), score, renorm, 1.5)
+
+
             assert float((num - d[:, e].double()).abs().max()) < 2.0 ** -10
 
 

@@ -202,6 +202,29 @@ def test_routing_gradient_against_differences(score, renorm):
             assert abs((f(up, t) - f(dn, t)) / (2 * h) - got[t, e]) < 1e-8
 
 
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_routing_gradient_without_cancellation(score, renorm):
+    """On ordinary rows the same as route_grad; of a row that one expert leads
+    by far, what the closed forms give."""
+    rng = np.random.default_rng(5)
+    T, E, k = 4, 9, 4
+    l, dg = rng.standard_normal((T, E)), rng.standard_normal((T, k))
+    ids = np.array([rng.permutation(E)[:k] for _ in range(T)])
+    a, mag = scores.route_grad_apart(l, ids, dg, score, renorm, -1.5)
+    assert np.allclose(a, scores.route_grad(l, ids, dg, score, renorm, -1.5)[0], rtol=1e-12, atol=1e-14)
+    assert (np.abs(a) <= mag * (1 + 1e-12)).all()
+    for lead in (5.0, 20.0, 60.0):
+        q = np.exp(-lead)
+        if score == "softmax" and not renorm:      # s (1 - s), and -s / 8 of it for each of the others
+            a, _ = scores.route_grad_apart([[lead] + [0.0] * 8], [[0]], [[1.0]], score, renorm)
+            rest = 8 * q / (1 + 8 * q)
+            assert np.allclose(a[0], [rest / (1 + 8 * q)] + [-rest / 8 / (1 + 8 * q)] * 8, rtol=1e-13, atol=0)
+        elif score == "softmax":                   # two experts: s_0 s_1 (dg_0 - dg_1)
+            a, _ = scores.route_grad_apart([[lead, 0.0, 3.0]], [[0, 1]], [[2.0, -1.0]], score, renorm)
+            assert np.allclose(a[0], [3 * q / (1 + q) ** 2, -3 * q / (1 + q) ** 2, 0], rtol=1e-13, atol=0)
+
+
 def test_combine_and_its_gradient():
     rng = np.random.default_rng(2)
     T, k, N = 3, 2, 5
