@@ -65,6 +65,16 @@ def test_route_long_batches(T, E, k):
     _check(rng.standard_normal((T, E)).astype(np.float32), k)
 
 
+@pytest.mark.parametrize("T,E,k", [(8193, 7, 2), (8193, 64, 6), (10241, 256, 8), (20001, 256, 2), (32768, 128, 8),
+                                   (65536, 64, 3)])
+def test_route_batches_of_many_segments(T, E, k):
+    """More than 128 segments: each of the scan's parts has more of them than
+    it keeps in registers, with ragged last segments and parts."""
+    rng = np.random.default_rng(T + E)
+    _check((rng.integers(-2, 3, size=(T, E)) * 0.25).astype(np.float32), k)
+    _check(rng.standard_normal((T, E)).astype(np.float32), k)
+
+
 def test_route_deterministic():
     cfg = configs.get("prefill")
     logits = gen.gen_logits(cfg, 0)
