@@ -251,6 +251,15 @@ def test_adapters_as_dense_matrices():
     assert np.allclose(out[2], y[2] + 0.5 * (b[0][:, :2] @ a[0][:2]) @ x[2])
 
 
+def test_adapters_adapter_by_adapter():
+    rng = np.random.default_rng(6)
+    x, a, b, y = (rng.standard_normal(s) for s in ((40, 6), (3, 4, 6), (3, 7, 4), (40, 7)))
+    ids, scale, ranks = rng.integers(-1, 4, 40), np.array([0.5, -1.0, 2.0]), [2, 0, 9]
+    for kw in ({}, dict(scale=scale), dict(scale=scale, ranks=ranks)):
+        for p, q in zip(requests.adapters(x, a, b, ids, y, **kw), requests.adapters_of_many_rows(x, a, b, ids, y, **kw)):
+            assert np.allclose(p, q, rtol=1e-13, atol=1e-13)
+
+
 @pytest.mark.skipif(not os.path.exists(build.HIPCC) and not shutil.which(build.HIPCC), reason="no compiler")
 @pytest.mark.parametrize("name,kernels", [("score", 9), ("combine", 9), ("adapters", 20)])
 def test_kernels_use_no_scratch(name, kernels):
