@@ -182,6 +182,27 @@ def test_rows_beyond_32_bit_offsets():
     assert torch.equal(d[P - 1].cpu(), (0.5 * want[0].float()).half()) and torch.equal(d[P - 2].cpu(), (2 * want[1].float()).half())
 
 
+def test_gradients_of_rows_beyond_32_bit_offsets():
+    """Whole numbers, whose sums are exact: rows read and gradients written
+    beyond 2^32 bytes and elements of the base, the rows left as they were."""
+    from bit_quantized_moe_token_amd import moeq
+    N, P = 1 << 20, 4200                              # 8.8 GB each
+    g = torch.Generator().manual_seed(1)
+    rows = torch.zeros((P, N), dtype=F16, device="cuda")
+    out = torch.zeros_like(rows)
+    pos = torch.tensor([P - 1, 3, 4097, P - 2], dtype=torch.int32)
+    vals, dy = torch.randint(-8, 9, (4, N), generator=g).half(), torch.randint(-4, 5, (2, N), generator=g).half()
+    rows[pos.long().cuda()] = vals.cuda()
+    gates = torch.tensor([[0.5, 0.25], [1.0, 2.0]])
+    d, dg = moeq.combine_grad(dy.cuda(), pos.cuda(), gates=gates.cuda(), rows=rows, out=out)
+    for p in range(4):
+        assert torch.equal(d[int(pos[p])].cpu(), (gates.view(-1)[p] * dy[p // 2].float()).half())
+        assert float(dg.view(-1)[p]) == float(dy[p // 2].double() @ vals[p].double())
+        assert torch.equal(rows[int(pos[p])].cpu(), vals[p])
+    d[pos.long().cuda()] = 0
+    assert not d.any()                                # nothing anywhere else
+
+
 def test_refusals():
     from bit_quantized_moe_token_amd import moeq
     rows, pos, g = torch.ones(8, 16).half().cuda(), torch.arange(8, dtype=torch.int32).cuda(), torch.ones(4, 2).cuda()
