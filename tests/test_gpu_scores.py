@@ -189,6 +189,38 @@ def test_no_tokens_and_reused_output():
         moeq.route_scored(_logits(49, 24).cuda(), 4, out=out)
 
 
+def test_saved_ids_and_written_offsets():
+    """A backward pass that saved a routing's ids and gates is not in the way
+    of a caller who uses the other outputs as scratch."""
+    from bit_quantized_moe_token_amd import moeq
+
+    class Gates(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, l, r):
+            ctx.save_for_backward(l, r.ids, r.gates)
+            return r.gates.clone()
+
+        @staticmethod
+        def backward(ctx, d):
+            l, ids, _ = ctx.saved_tensors
+            return moeq.route_scored_grad(l, ids, d.contiguous()), None
+
+    l = _logits(30, 16).cuda().requires_grad_()
+    for routing in (moeq.route_scored(l.detach(), 3), moeq.route(l.detach(), 3)):
+        loss = (Gates.apply(l, routing) ** 2).sum()
+        routing.offsets.zero_()
+        routing.sorted_pairs.add_(1)
+        routing.pair_pos.zero_()
+        loss.backward()
+        want = moeq.route_scored_grad(l.detach(), routing.ids, 2 * routing.gates)
+        assert torch.equal(l.grad, want)
+        l.grad = None
+        loss = (Gates.apply(l, routing) ** 2).sum()
+        routing.ids.zero_()
+        with pytest.raises(RuntimeError):          # (what was saved itself)
+            loss.backward()
+
+
 def test_softmax_over_the_chosen_is_the_plain_routing():
     """With renormalised softmax gates the choice is route's, bit for bit in
     the integers, within fp32 in the gates (there 2^-21: fast exponentials)."""

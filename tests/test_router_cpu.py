@@ -145,6 +145,23 @@ def test_sizes_beyond_32_bits_are_refused():
             moeq.adapters_workspace_size(*bad)
 
 
+@pytest.mark.parametrize("T", [5, 0, 5000])
+def test_tensors_of_a_routing_stand_alone(T):
+    """Each output has its own memory, so that keeping one keeps no other, and
+    its own version counter; the workspace is a tensor also where none is needed."""
+    import torch
+    from bit_quantized_moe_token_amd import moeq
+    r = moeq.RoutingOut(T, 8, 2, "cpu")
+    all_of = {n: getattr(r, n) for n in ("ids", "gates", "offsets", "sorted_pairs", "pair_pos")}
+    assert [tuple(t.shape) for t in all_of.values()] == [(T, 2), (T, 2), (9,), (2 * T,), (2 * T,)]
+    for n, t in all_of.items():
+        assert t.untyped_storage().nbytes() == 4 * t.numel() and not t._is_view(), n
+        before = {m: o._version for m, o in all_of.items()}
+        moeq._written(t)
+        assert [m for m, o in all_of.items() if o._version != before[m]] == [n]
+    assert r.ws.dtype == torch.uint8 and r.ws.numel() == max(1, r.ws_bytes) and r.ws is r.ws
+
+
 # ---- the fp64 forms
 
 def test_scores_closed_forms():
