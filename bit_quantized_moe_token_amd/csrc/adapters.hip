@@ -494,7 +494,7 @@ adapters_up_kernel(AdapterArgs a) {
         for (int i = 0; i < 8; ++i) v[i] = __builtin_fmaf(d[i >> 2][i & 3], up, y[h][i]);
         y[h].pack(v);
       }
-      y[h].store(op, h * 8 * a.ldo + n0, n, true);
+      y[h].template store<true>(op, h * 8 * a.ldo + n0, n);
     }
     lds_order();
 #pragma unroll

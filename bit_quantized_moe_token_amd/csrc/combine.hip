@@ -1,8 +1,17 @@
 // The experts' rows back to their tokens, weighted by the gates, and the
 // gradients of rows and gates.  Both are bound by their bytes: 4096 tokens of
-// six rows of 2048 in bf16 23 us (134 MB, 5.8 TB/s), their gradients 40 us
-// (218 MB, 5.4 TB/s).  Rows are read, and outputs written, once and past the
-// caches (with ordinary loads and stores 25.6 and 46 us).
+// six rows of 2048 in bf16 23.0 us (134 MB, 5.8 TB/s), their gradients 38.9 us
+// (218 MB, 5.6 TB/s).
+//
+// Past the caches or not, each against the other way (us): rows of more than 80
+// MiB are read past them (4096 tokens of six rows of 2048: 23.0 / 25.6, the
+// gradients 38.9 / 46.4), fewer by ordinary loads (1024 of eight, 32 MiB: 8.5 /
+// 9.3 and 15.3 / 16.7; 333 of four rows of 757: 4.3 / 5.4 and 6.3 / 8.2; at 80 MiB
+// 18.5 / 19.0 and 33.0 / 35.0).  Tokens' outputs are always written past them
+// (23.0 / 24.7, small ones within 0.2).  Gradients of rows only where the rows
+// are read by ordinary loads (2048 tokens of six: 19.7 / 22.7): of more they are
+// slower so (40.6 / 38.9), and so is the product that reads them next (both
+// together 210 / 200).
 #include "check.hpp"
 #include "vec8.hpp"
 #include "wave.hpp"
@@ -23,11 +32,12 @@ struct CombineArgs {
   int T, k, N, P;
   int lanes;             // forward: log2 of the threads along a row
 };
+constexpr int64_t kBigRows = (int64_t)80 << 20;   // bytes of the pairs' rows, see above
 
 // TR: type of the rows, TO: of base and out.  2^lanes threads along a row,
 // eight columns each; four rows under way at a time (decoding steps and long
 // batches: 3.0 and 25.4 us, one at a time 3.0 and 27.2, eight 3.2 and 24.7).
-template <int TR, int TO>
+template <int TR, int TO, bool BIG>
 __global__ void __launch_bounds__(kCombineThreads)
 combine_kernel(CombineArgs a) {
   constexpr int SLOTS = 4;
@@ -38,7 +48,7 @@ combine_kernel(CombineArgs a) {
   float acc[8];
   if (a.tok) {
     Oct<TO> b;
-    b.load(a.tok, t * a.ldt + c, n, true);
+    b.template load<BIG>(a.tok, t * a.ldt + c, n);
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = b[i];
   } else {
@@ -57,7 +67,7 @@ combine_kernel(CombineArgs a) {
     }
 #pragma unroll
     for (int j = 0; j < SLOTS; ++j)
-      if ((uint32_t)at[j] < (uint32_t)a.P) r[j].load(a.rows, at[j] * a.ldr + c, n, true);
+      if ((uint32_t)at[j] < (uint32_t)a.P) r[j].template load<BIG>(a.rows, at[j] * a.ldr + c, n);
 #pragma unroll
     for (int j = 0; j < SLOTS; ++j)
       if ((uint32_t)at[j] < (uint32_t)a.P) {
@@ -67,12 +77,12 @@ combine_kernel(CombineArgs a) {
   }
   Oct<TO> o;
   o.pack(acc);
-  o.store(a.out, t * a.ldo + c, n, true);
+  o.template store<true>(a.out, t * a.ldo + c, n);
 }
 
 // One workgroup per token: dy is read once for SLOTS pairs at a time, whose rows
 // are all loaded before the first is used.
-template <int TR, int TO>
+template <int TR, int TO, bool BIG>
 __global__ void __launch_bounds__(kCombineThreads)
 combine_grad_kernel(CombineArgs a) {
   constexpr int SLOTS = TR == MOEQ_F32 ? 4 : 8, NW = kCombineThreads / kWave;
@@ -94,11 +104,11 @@ combine_grad_kernel(CombineArgs a) {
       const int n = a.N - c;
       Oct<TO> d;
       Oct<TR> r[SLOTS];
-      d.load(a.tok, t * a.ldt + c, n, true);
+      d.template load<BIG>(a.tok, t * a.ldt + c, n);
       if (a.d_gates) {
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j)
-          if (at[j] >= 0) r[j].load(a.rows, at[j] * a.ldr + c, n, true);
+          if (at[j] >= 0) r[j].template load<BIG>(a.rows, at[j] * a.ldr + c, n);
       }
 #pragma unroll
       for (int j = 0; j < SLOTS; ++j) {
@@ -111,7 +121,7 @@ combine_grad_kernel(CombineArgs a) {
         }
         Oct<TR> o;
         o.pack(v);
-        o.store(a.out, at[j] * a.ldo + c, n, true);
+        o.template store<!BIG>(a.out, at[j] * a.ldo + c, n);
       }
     }
     if (!a.d_gates) continue;
@@ -132,17 +142,23 @@ combine_grad_kernel(CombineArgs a) {
   }
 }
 
-template <int TR, int TO>
-static void launch_combine(CombineArgs a, bool grad, hipStream_t s) {
+template <int TR, int TO, bool BIG>
+static void launch_combine_sized(CombineArgs a, bool grad, hipStream_t s) {
   if (grad) {
-    hipLaunchKernelGGL((combine_grad_kernel<TR, TO>), dim3(a.T), dim3(kCombineThreads), 0, s, a);
+    hipLaunchKernelGGL((combine_grad_kernel<TR, TO, BIG>), dim3(a.T), dim3(kCombineThreads), 0, s, a);
     return;
   }
   a.lanes = 0;
   while (a.lanes < 8 && (8 << a.lanes) < a.N) ++a.lanes;
   const int per = kCombineThreads >> a.lanes, cols = 8 << a.lanes;
-  hipLaunchKernelGGL((combine_kernel<TR, TO>), dim3((a.T + per - 1) / per, (a.N + cols - 1) / cols), dim3(kCombineThreads), 0,
-                     s, a);
+  hipLaunchKernelGGL((combine_kernel<TR, TO, BIG>), dim3((a.T + per - 1) / per, (a.N + cols - 1) / cols),
+                     dim3(kCombineThreads), 0, s, a);
+}
+
+template <int TR, int TO>
+static void launch_combine(const CombineArgs &a, bool grad, hipStream_t s) {
+  if ((int64_t)a.T * a.k * a.N * Val<TR>::size > kBigRows) launch_combine_sized<TR, TO, true>(a, grad, s);
+  else launch_combine_sized<TR, TO, false>(a, grad, s);
 }
 
 static void launch_combine_types(const CombineArgs &a, int tr, int to, bool grad, hipStream_t s) {

@@ -36,14 +36,18 @@ struct Oct {
   using Loose = typename Val<TY>::Loose;
   uint32_t w[W];
 
-  // (nt: non-temporal, for rows that are read, or written, once)
-  __device__ __forceinline__ void load(const void *base, int64_t i, int n, bool nt = false) {
+  // (NT: non-temporal, past the caches; no run-time argument, since a choice
+  // between two accesses to one address is merged into an ordinary one)
+  template <bool NT = false>
+  __device__ __forceinline__ void load(const void *base, int64_t i, int n) {
     const uint8_t *p = (const uint8_t *)base + i * Val<TY>::size;
     if (n >= 8) {
 #pragma unroll
       for (int q = 0; q < W / 4; ++q) {
         const auto at = &((const __attribute__((address_space(1))) Loose *)p)[q];
-        const u32x4 v = nt ? __builtin_nontemporal_load(at) : *at;
+        u32x4 v;
+        if constexpr (NT) v = __builtin_nontemporal_load(at);
+        else v = *at;
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[4 * q + j] = v[j];
       }
@@ -79,14 +83,15 @@ struct Oct {
       else w[j] = Val<TY>::put(v[2 * j]) | (Val<TY>::put(v[2 * j + 1]) << 16);
     }
   }
-  __device__ __forceinline__ void store(void *base, int64_t i, int n, bool nt = false) const {
+  template <bool NT = false>
+  __device__ __forceinline__ void store(void *base, int64_t i, int n) const {
     uint8_t *p = (uint8_t *)base + i * Val<TY>::size;
     if (n >= 8) {
 #pragma unroll
       for (int q = 0; q < W / 4; ++q) {
         const auto at = &((__attribute__((address_space(1))) Loose *)p)[q];
         const Loose v = u32x4{w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]};
-        if (nt) __builtin_nontemporal_store(v, at);
+        if constexpr (NT) __builtin_nontemporal_store(v, at);
         else *at = v;
       }
     } else {

@@ -182,6 +182,28 @@ def test_rows_beyond_32_bit_offsets():
     assert torch.equal(d[P - 1].cpu(), (0.5 * want[0].float()).half()) and torch.equal(d[P - 2].cpu(), (2 * want[1].float()).half())
 
 
+@pytest.mark.parametrize("types", PAIRS, ids=IDS)
+@pytest.mark.parametrize("T", [1075, 1100])
+def test_rows_on_both_sides_of_the_caches(types, T):
+    """Rows of a little less and a little more than 80 MiB, which are read in
+    different ways, with a ragged end and pairs that point nowhere."""
+    from bit_quantized_moe_token_amd import moeq
+    tr, to = types
+    k, N = 8, 2429 if tr == F32 else 4858
+    P = T * k - 5
+    size = 4 if tr == F32 else 2
+    assert (T * k * N * size > 80 << 20) == (T == 1100)
+    rows, base, pos = _rand((P, N), tr, 1), _rand((T, N), to, 2), _positions(T, k, P)
+    gates = torch.rand((T, k), generator=torch.Generator().manual_seed(3))
+    got = moeq.combine(rows.cuda(), pos.cuda(), gates=gates.cuda(), base=base.cuda())
+    ref, mag = products.combine(_np(rows), pos.numpy(), gates, _np(base), T, k)
+    _close(got, ref, mag, k + 1, "out")
+    d_rows, d_gates = moeq.combine_grad(base.cuda(), pos.cuda(), gates=gates.cuda(), rows=rows.cuda(), out=rows.cuda())
+    ref_r, ref_g, mag = products.combine_grad(_np(base), pos.numpy(), gates, _np(rows), P, _np(rows))
+    _close(d_rows, ref_r, np.abs(ref_r), 1, "d_rows")
+    _close(d_gates, ref_g, mag, N + 1, "d_gates")
+
+
 def test_gradients_of_rows_beyond_32_bit_offsets():
     """Whole numbers, whose sums are exact: rows read and gradients written
     beyond 2^32 bytes and elements of the base, the rows left as they were."""
