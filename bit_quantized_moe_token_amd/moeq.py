@@ -681,10 +681,10 @@ def _pairs_of(pair_pos, gates, k, dev):
         if k is not None and k != gates.shape[1]:
             raise ValueError(f"k={k} beside gates of shape {tuple(gates.shape)}")
         T, k = gates.shape
-    elif k is None:
-        raise ValueError("k is needed without gates")
+    elif k is None or k < 1:
+        raise ValueError(f"without gates k must be given and positive, got {k}")
     else:
-        T = pair_pos.shape[0] // k if k > 0 else -1
+        T = pair_pos.shape[0] // k
     if T * k != pair_pos.shape[0]:
         raise ValueError(f"pair_pos has {pair_pos.shape[0]} positions, not {k} for each of {T} tokens")
     return T, k

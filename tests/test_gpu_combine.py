@@ -253,6 +253,16 @@ def test_refusals():
             moeq.combine_grad(*a, **kw)
 
 
+def test_no_slots_and_no_tokens_are_refused_as_arguments():
+    from bit_quantized_moe_token_amd import moeq
+    rows, none = torch.ones(8, 16).half().cuda(), torch.zeros(0, dtype=torch.int32).cuda()
+    for k in (0, -1):
+        with pytest.raises(ValueError):
+            moeq.combine(rows, none, k=k)
+        with pytest.raises(ValueError):
+            moeq.combine_grad(rows[:0], none, k=k)
+
+
 def test_two_streams_and_captured_calls():
     from bit_quantized_moe_token_amd import moeq
     T, k, N = 500, 6, 1408
