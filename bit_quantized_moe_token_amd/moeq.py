@@ -766,8 +766,8 @@ def adapters(x, a, b, ids, y, scale=None, ranks=None, out=None, ws=None):
     x fp16 or bf16 [T, K]; a [n, R, K] and b [n, N, R] of the same type; ids
     int32 [T]; y [T, N] of that type or float32 (linear_i8 or grouped_gemm of
     the same x, or the expert layer's); scale fp32 [n] or None (ones); ranks
-    int32 [n] or None (R): how much of R counts.  Returns [T, N] of y's type;
-    out may be y (in place).  ws: uint8 workspace tensor, or None for one of
+    int32 [n] or None (R): how much of R counts, finite in b.  Returns [T, N] of
+    y's type; out may be y (in place).  ws: uint8 workspace tensor, or None for one of
     the call's own; neither it nor out may overlap the other inputs.  No
     autograd, and no gradient of its own."""
     dev = x.get_device() if isinstance(x, torch.Tensor) else -1

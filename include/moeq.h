@@ -679,7 +679,9 @@ typedef struct {
  * but are served in fewer passes over its matrices where they do.  A_i x is
  * summed in fp32; of each row of it 16 bits (22 of fp16 adapters) below its
  * largest value go on beside a 16-bit y, 24 beside MOEQ_F32; the rest is
- * fp32, rounded once.
+ * fp32, rounded once.  Infinities and NaN in x or A_i reach their rows as in
+ * fp32.  B_i is to be finite: an infinity in it may give NaN (its products with
+ * the lower bits of A_i x, which may be zero), in the outputs it belongs to.
  *   x DEVICE [T, K] of the adapters' dtype; ids DEVICE [T] int32; y, out
  *   DEVICE [T, N] of y_dtype (the adapters' dtype or MOEQ_F32); rows ldx, ldy,
  *   ldo elements apart, aligned to their elements; 0 <= T < 2^22.  out may be

@@ -136,3 +136,19 @@ def test_bits_of_z(types, T):
     top = z.abs().amax(1, keepdim=True).numpy()
     assert (off <= KEPT[types[1]] * top + 1.01 * torch.finfo(types[1]).eps / 2 * np.abs(want)
             + (2.0 ** -25 if types[1] == F16 else 0)).all(), float((off / top).max())
+
+
+@pytest.mark.parametrize("types", TYPES, ids=IDS)
+@pytest.mark.parametrize("T", [40, 2100])
+def test_infinities_in_b_stay_in_their_outputs(types, T):
+    """Of the adapter that has them, in the column they belong to, and not
+    beyond its rank."""
+    c = _case(T, 3, 20, 72, 70, types, "mixed")
+    c["ranks"] = torch.tensor([20, 12, 20]).int()
+    want = _call(c)
+    c["b"][1, 33, 4], c["b"][1, 60, 15] = float("inf"), float("-inf")       # (the second beyond the rank)
+    got = _call(c)
+    hit = torch.zeros(T, 70, dtype=torch.bool)
+    hit[c["ids"] == 1, 33] = True
+    assert not torch.isfinite(got.cpu()[hit]).any() and hit.any()
+    assert torch.equal(got.cpu()[~hit], want.cpu()[~hit])
