@@ -4,11 +4,14 @@
 // Two kernels, z = A_i x with K in parts and out = y + scale_i B_i z, both by
 // MFMA over tiles of 16 rows: the operations are few (4096 rows of 4096, rank
 // 64: 4.3 GFLOP), the bytes of x, y and out bound long batches, latency short
-// ones.  Measured: 4096 rows of 4096 in bf16 in runs of eight adapters 25.4 us
-// for rank 16 and 36.4 us for rank 64 (101 and 109 MB: 20 and 21 us at the rate
-// of a large copy), one row of 4096 -> 14336 with rank 32 7.7 us, 64 rows of 32
-// adapters of rank 16 13.6 us.  What is left in long batches is A_i and B_i
-// from L2 through LDS for every 16 (32) rows.
+// ones.  Measured by replays of a captured call: 4096 rows of 4096 in bf16 in
+// runs of eight adapters 25.8 us for rank 16 and 37.9 us for rank 64 (101 and 109
+// MB: 20 and 21 us at the rate of a large copy), one row of 4096 -> 14336 with
+// rank 32 7.5 us, 64 rows of 32 adapters of rank 16 13.1 us (a kernel trace, which
+// keeps the two launches apart, has 39.0, 9.1 and 16.0 us for the last three).
+// What is left in long batches is A_i and B_i from L2 through LDS for every 16
+// (32) rows; in the last, waves that have one chunk of K each and sixteen parts
+// of z that every workgroup sums.
 #include "check.hpp"
 #include "vec8.hpp"
 #include "wave.hpp"

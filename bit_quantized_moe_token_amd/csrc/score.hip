@@ -5,13 +5,19 @@
 // cannot tell apart.  A wave therefore picks its token's experts by choices in
 // fp32 and watches the distance of each from the next; where it is within what
 // fp32 may be off (0.2 to 1.2 tokens in a hundred), the same code picks again in
-// 64 bits.  (Choices without a bias are the logits themselves, and exact.)
+// 64 bits.  (Choices without a bias are the logits themselves, and exact.)  That
+// needs groups that fill a power of two of lanes, at 1, 2 or 4 experts a lane (up
+// to 64, 128, 256 experts): any number of experts in one group, 256 in eight, but
+// not 160 in eight, whose tokens are all picked in 64 bits, one group after the
+// other.  So are tokens of which a group has infinite choices only to sum up.
 //
 // Up to 16 tokens one launch does all (16 tokens of 128 experts: 7 us); more are
 // picked, scanned and placed.  8192 tokens of 256 experts in eight groups: the
-// pick takes 19.5 us for 8.4 MB of logits, bound by its instructions, about 600
-// a token (k rounds of a maximum over the wave, the groups' ranks); picked in 64
-// bits throughout 58 us, by comparisons of floats with their index 38 us.
+// pick takes 20 us of 31.6 for 8.4 MB of logits, bound by its instructions, about
+// 600 a token (k rounds of a maximum over the wave, the groups' ranks); picked in
+// 64 bits throughout 58 us, by comparisons of floats with their index 38 us.  64,
+// 512 and 4096 such tokens: 10.8, 14.5 and 28.9 us (each segment of the placement
+// counts all pairs up to 4096); 8192 tokens of 160 experts in eight groups 69 us.
 #include "check.hpp"
 #include "route.hpp"
 #include "vec8.hpp"
@@ -449,9 +455,10 @@ __device__ __forceinline__ bool pick(const ScoreArgs &a, const float (&l)[NS], i
 }
 
 // Gates of the `items` slots (k of each token from t0 on) whose experts stand
-// in sid: a thread each, in 64 bits, so that they are rounded once.  A
-// renormalised softmax needs no logits but the chosen.  (Every thread of the
-// workgroup calls it; the tokens' largest logits and sums in m and total.)
+// in sid: a thread each, in 64 bits, so that they are rounded once; but a softmax
+// over all E divides by the fp32 sum of the pick, which is off by up to 16 steps
+// of 2^-24.  A renormalised softmax needs no logits but the chosen.  (Every thread
+// of the workgroup calls it; the tokens' largest logits and sums in m and total.)
 template <int NTH>
 __device__ __forceinline__ void put_gates(const ScoreArgs &a, int t0, int items, const int *sid, const float *m,
                                           const float *total, float *sel, double *g, int32_t *__restrict__ ids,

@@ -407,6 +407,8 @@ typedef struct {
  * moeq_route_scored — routing by scores, into the same arrays as moeq_route
  * (topk_ids by descending choice, topk_gates as above) with the same counting
  * sort and the same workspace (moeq_route_workspace_size).
+ * Gates are formed in 64 bits and rounded once, but a softmax that is not
+ * renormalised divides by an fp32 sum of its E exponentials (16 * 2^-24).
  *   logits DEVICE [T, E] of dtype MOEQ_F16, MOEQ_BF16 or MOEQ_F32, rows ld
  *   elements apart, aligned to its elements.  0 <= T < 2^22, T * k <= 2^29,
  *   1 <= k <= E <= 256.
