@@ -255,13 +255,14 @@ class RoutingOut:
         self.T, self.E, self.k = T, E, k
         self.ws_bytes = _route_workspace_size(T, E, k)
         P = T * k
-        # (after the first by new_empty: 1.2 to 1.5 us on the host, by torch.empty 1.7)
-        self.offsets = torch.empty((E + 1,), dtype=torch.int32, device=device)
+        # (sizes as numbers, after the first by new_empty: 1.2 us each on the host,
+        # torch.empty of tuples 1.7)
+        self.offsets = torch.empty(E + 1, dtype=torch.int32, device=device)
         new = self.offsets.new_empty
-        self.ids = new((T, k))
+        self.ids = new(T, k)
         self.sorted_pairs = new(P)
         self.pair_pos = new(P)
-        self.gates = new((T, k), dtype=torch.float32)
+        self.gates = new(T, k, dtype=torch.float32)
         if self.ws_bytes:
             self.ws   # (made here, on the stream of the first call)
         self.c = _lib.Routing(self.ids.data_ptr(), self.gates.data_ptr(), self.offsets.data_ptr(),
@@ -767,8 +768,8 @@ def adapters(x, a, b, ids, y, scale=None, ranks=None, out=None, ws=None):
     int32 [T]; y [T, N] of that type or float32 (linear_i8 or grouped_gemm of
     the same x, or the expert layer's); scale fp32 [n] or None (ones); ranks
     int32 [n] or None (R): how much of R counts, finite in b.  Returns [T, N] of
-    y's type; out may be y (in place).  ws: uint8 workspace tensor, or None for one of
-    the call's own; neither it nor out may overlap the other inputs.  No
+    y's type; out may be y (in place).  ws: uint8 workspace tensor, or None for
+    one of the call's own; neither it nor out may overlap the other inputs.  No
     autograd, and no gradient of its own."""
     dev = x.get_device() if isinstance(x, torch.Tensor) else -1
     _like(x, _16BIT, 2, dev, "x")
